@@ -53,6 +53,29 @@ _SIGS = {
     "mq_gemm_residual_separate": [_p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _int, _int,
                                   _int, _p, _int, _p, _p],
 }
+_SIGS.update({
+    "mq_mx_quantize": [_p, _int, _i64, _i64, _i64, _i64, _i64, _p, _p, _p],
+    "mq_mx_dequantize": [_p, _p, _i64, _i64, _i64, _p, _int, _p],
+    "mq_mx_gemm": [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _int, _p],
+    "mq_mx_linear": [_p, _int, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _int, _p, C.c_size_t, _p],
+    "mq_route": [_p, _int, _i64, _i64, _i64, _p, _int, _i64, _i64, _int, _i64, _int, C.c_float, _p, _p, _p],
+    "mq_expert_plan": [_p, _i64, _i64, _i64, _p, _p, _p, _p],
+    "mq_mx_experts_up": [_p, _int, _i64, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _int, _p,
+                         C.c_size_t, _p],
+    "mq_mx_experts_down": [_p, _int, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _int, _p, C.c_size_t, _p],
+})
+_SIZES = {
+    "mq_mx_codes_bytes": [_i64, _i64],
+    "mq_mx_scales_bytes": [_i64, _i64],
+    "mq_mx_linear_workspace_bytes": [_i64, _i64, _i64],
+    "mq_mx_experts_up_workspace_bytes": [_i64, _i64, _i64, _i64, _i64],
+    "mq_mx_experts_down_workspace_bytes": [_i64, _i64, _i64, _i64, _i64],
+}
+for _name, _args in _SIZES.items():
+    getattr(_lib, _name).argtypes = _args
+    getattr(_lib, _name).restype = C.c_size_t
+_lib.mq_plan_rows.argtypes = [_i64, _i64, _i64]
+_lib.mq_plan_rows.restype = _i64
 for _name, _args in _SIGS.items():
     getattr(_lib, _name).argtypes = _args
     getattr(_lib, _name).restype = C.c_int
@@ -63,7 +86,8 @@ _lib.mq_version.restype = C.c_int
 _lib.mq_select_workspace_bytes.argtypes = [_i64, _i64, _int, _int]
 _lib.mq_select_workspace_bytes.restype = C.c_size_t
 
-EXPORTS = tuple(_SIGS) + ("mq_status_string", "mq_version", "mq_select_workspace_bytes")
+EXPORTS = tuple(_SIGS) + tuple(_SIZES) + ("mq_status_string", "mq_version", "mq_select_workspace_bytes",
+                                          "mq_plan_rows")
 
 
 class MQError(RuntimeError):
@@ -543,3 +567,8 @@ def forward_layer(x, w, k_blocks: int, bn: int = 64, out_dtype=torch.bfloat16, m
                            out_dtype=out_dtype, stream=stream)
     return dict(h=h, row_ptr=row_ptr, col_idx=col_idx, delta=delta, wq=wq, sw=sw, rq=rq, xq=xq,
                 sx=sx, y=y, s=s, r=r, w_hat=w if migrate else None)
+
+
+from .mx import MX, mx_dequantize, mx_linear, mx_quantize  # noqa: E402
+from .experts import (ExpertPlan, expert_plan, mx_experts, mx_experts_down, mx_experts_up,  # noqa: E402
+                      plan_rows, route)

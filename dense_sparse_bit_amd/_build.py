@@ -33,6 +33,10 @@ SOURCES = {
     "prep.hip": ["-ffp-contract=off"],
     "gemm.hip": [],
     "api.hip": ["-ffp-contract=off"],
+    "mx_quant.hip": [],
+    "mx_gemm.hip": [],
+    "route.hip": ["-ffp-contract=off"],
+    "api_mx.hip": [],
 }
 
 

@@ -125,7 +125,7 @@ const char* mq_status_string(int status) {
     switch (status) {
         case MQ_OK: return "ok";
         case MQ_ERR_INVALID_ARG: return "invalid argument (null pointer, size, alignment or count)";
-        case MQ_ERR_UNSUPPORTED: return "unsupported shape (needs K % 128 == 0, group 128, bk 64, bn 64 or 128, N % bn == 0)";
+        case MQ_ERR_UNSUPPORTED: return "unsupported shape (the int4 calls need K % 128 == 0, group 128, bk 64, bn 64 or 128, N % bn == 0; sizes as in mq.h)";
         case MQ_ERR_HIP: return "HIP runtime error";
         case MQ_ERR_SCRATCH: return "shape needs more scratch than the library's static array (MQ_NOALLOC_SCRATCH_BYTES)";
         default: return "unknown status";

@@ -1,0 +1,278 @@
+// C ABI of the microscaled 4-bit operators and the routing: argument checks, then
+// kernel launches. Declarations and the meaning of every argument are in include/mq.h.
+#include <stdint.h>
+
+#include "../../include/mq.h"
+#include "mx_internal.h"
+
+namespace {
+
+int status_of(hipError_t e) { return e == hipSuccess ? MQ_OK : MQ_ERR_HIP; }
+bool bad_type(int d) { return d != MQ_F32 && d != MQ_BF16 && d != MQ_F16; }
+int64_t type_size(int d) { return d == MQ_F32 ? 4 : 2; }
+bool off(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+constexpr int64_t kMaxRows = int64_t(1) << 24;
+constexpr int64_t kMaxCols = int64_t(1) << 20;
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kMaxSlots = int64_t(1) << 27;
+constexpr int kMaxTop = 32;
+
+// sizes of a microscaled matrix (or batch of them)
+int check_matrix(int64_t B, int64_t R, int64_t K) {
+    if (B < 0 || R < 0 || K <= 0) return MQ_ERR_INVALID_ARG;
+    if (B > kMaxBatch || R > kMaxRows || K > kMaxCols || B * R > kMaxElements / K) return MQ_ERR_UNSUPPORTED;
+    return MQ_OK;
+}
+
+int check_codes(const void* codes, const void* scales) {
+    return !codes || !scales || off(codes, 16) || off(scales, 4) ? MQ_ERR_INVALID_ARG : MQ_OK;
+}
+
+int check_product(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N <= 0 || K <= 0) return MQ_ERR_INVALID_ARG;
+    if (M > kMaxRows || N > kMaxRows || K > kMaxCols || N > kMaxElements / K || (M && N > kMaxElements / M))
+        return MQ_ERR_UNSUPPORTED;
+    return MQ_OK;
+}
+
+int check_slots(int64_t T, int64_t k, int64_t E) {
+    if (T < 0 || k <= 0 || E <= 0) return MQ_ERR_INVALID_ARG;
+    if (E > MQ_MAX_EXPERTS || T > kMaxSlots / k) return MQ_ERR_UNSUPPORTED;
+    return MQ_OK;
+}
+
+size_t round16(int64_t n) { return static_cast<size_t>((n + 15) / 16 * 16); }
+
+// codes, then scales, of an R x K matrix in a workspace
+size_t mx_bytes(int64_t R, int64_t K) { return round16(mq::mx_codes_size(R, K)) + round16(mq::mx_scales_size(R, K)); }
+
+mq::MxGemmArgs product(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* ws, int64_t M, int64_t N,
+                       int64_t K, void* y, int y_dtype) {
+    mq::MxGemmArgs a = {};
+    a.xq = xq;
+    a.xs = xs;
+    a.wq = wq;
+    a.ws = ws;
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.y = y;
+    a.y_dtype = y_dtype;
+    return a;
+}
+
+mq::MxQuantArgs rows_of(const void* x, int dtype, int64_t R, int64_t stride, int64_t K, uint8_t* codes, uint8_t* scales) {
+    mq::MxQuantArgs a = {};
+    a.x = x;
+    a.dtype = dtype;
+    a.B = 1;
+    a.R = R;
+    a.stride_r = stride;
+    a.K = static_cast<int>(K);
+    a.codes = codes;
+    a.scales = scales;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mq_mx_codes_bytes(int64_t R, int64_t K) {
+    return check_matrix(1, R, K) ? 0 : static_cast<size_t>(mq::mx_codes_size(R, K));
+}
+
+size_t mq_mx_scales_bytes(int64_t R, int64_t K) {
+    return check_matrix(1, R, K) ? 0 : static_cast<size_t>(mq::mx_scales_size(R, K));
+}
+
+int mq_mx_quantize(const void* x, int x_dtype, int64_t B, int64_t stride_b, int64_t R, int64_t stride_r, int64_t K,
+                   uint8_t* codes, uint8_t* scales, void* stream) {
+    int rc = check_matrix(B, R, K);
+    if (rc) return rc;
+    if (bad_type(x_dtype) || stride_b < 0 || stride_r < 0) return MQ_ERR_INVALID_ARG;
+    if (B == 0 || R == 0) return MQ_OK;
+    if (!x || off(x, type_size(x_dtype))) return MQ_ERR_INVALID_ARG;
+    if ((rc = check_codes(codes, scales))) return rc;
+    mq::MxQuantArgs a = rows_of(x, x_dtype, R, stride_r, K, codes, scales);
+    a.B = B;
+    a.stride_b = stride_b;
+    return status_of(mq::launch_mx_quant(a, static_cast<hipStream_t>(stream)));
+}
+
+int mq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t B, int64_t R, int64_t K, void* y, int y_dtype,
+                     void* stream) {
+    int rc = check_matrix(B, R, K);
+    if (rc) return rc;
+    if (bad_type(y_dtype)) return MQ_ERR_INVALID_ARG;
+    if (B == 0 || R == 0) return MQ_OK;
+    if ((rc = check_codes(codes, scales))) return rc;
+    if (!y || off(y, 16)) return MQ_ERR_INVALID_ARG;
+    return status_of(mq::launch_mx_dequant(codes, scales, B, R, K, y, y_dtype, static_cast<hipStream_t>(stream)));
+}
+
+int mq_mx_gemm(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* ws, int64_t M, int64_t N,
+               int64_t K, const float* bias, void* y, int y_dtype, void* stream) {
+    int rc = check_product(M, N, K);
+    if (rc) return rc;
+    if (bad_type(y_dtype) || off(bias, 4)) return MQ_ERR_INVALID_ARG;
+    if (M == 0) return MQ_OK;
+    if ((rc = check_codes(xq, xs)) || (rc = check_codes(wq, ws))) return rc;
+    if (!y || off(y, 16)) return MQ_ERR_INVALID_ARG;
+    mq::MxGemmArgs a = product(xq, xs, wq, ws, M, N, K, y, y_dtype);
+    a.bias = bias;
+    return status_of(mq::launch_mx_gemm(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t mq_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    return check_product(M, N, K) ? 0 : mx_bytes(M, K);
+}
+
+int mq_mx_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* wq, const uint8_t* ws, int64_t M,
+                 int64_t N, int64_t K, const float* bias, void* y, int y_dtype, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+    int rc = check_product(M, N, K);
+    if (rc) return rc;
+    if (bad_type(x_dtype) || bad_type(y_dtype) || stride_m < 0 || off(bias, 4)) return MQ_ERR_INVALID_ARG;
+    if (M == 0) return MQ_OK;
+    if (!x || off(x, type_size(x_dtype)) || !y || off(y, 16)) return MQ_ERR_INVALID_ARG;
+    if ((rc = check_codes(wq, ws))) return rc;
+    if (workspace_bytes < mq_mx_linear_workspace_bytes(M, N, K) || !workspace || off(workspace, 16))
+        return MQ_ERR_INVALID_ARG;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    uint8_t* xq = static_cast<uint8_t*>(workspace);
+    uint8_t* xs = xq + round16(mq::mx_codes_size(M, K));
+    hipError_t e = mq::launch_mx_quant(rows_of(x, x_dtype, M, stride_m, K, xq, xs), st);
+    if (e != hipSuccess) return MQ_ERR_HIP;
+    mq::MxGemmArgs a = product(xq, xs, wq, ws, M, N, K, y, y_dtype);
+    a.bias = bias;
+    return status_of(mq::launch_mx_gemm(a, st));
+}
+
+int mq_route(const void* logits, int dtype, int64_t T, int64_t stride_t, int64_t E, const float* bias, int score,
+             int64_t groups, int64_t top_groups, int group_score, int64_t k, int renormalize, float scale, int32_t* ids,
+             float* weights, void* stream) {
+    int rc = check_slots(T, k, E);
+    if (rc) return rc;
+    if (bad_type(dtype) || stride_t < 0 || off(bias, 4)) return MQ_ERR_INVALID_ARG;
+    if (score != MQ_SCORE_SOFTMAX && score != MQ_SCORE_SIGMOID) return MQ_ERR_INVALID_ARG;
+    if (group_score != MQ_GROUP_MAX && group_score != MQ_GROUP_TOP2) return MQ_ERR_INVALID_ARG;
+    if (groups <= 0 || E % groups || top_groups <= 0 || top_groups > groups) return MQ_ERR_INVALID_ARG;
+    if (k > top_groups * (E / groups)) return MQ_ERR_INVALID_ARG;
+    if (k > kMaxTop || groups > 64) return MQ_ERR_UNSUPPORTED;
+    if (T == 0) return MQ_OK;
+    if (!logits || off(logits, type_size(dtype)) || !ids || off(ids, 4) || !weights || off(weights, 4))
+        return MQ_ERR_INVALID_ARG;
+    mq::RouteArgs a;
+    a.logits = logits;
+    a.dtype = dtype;
+    a.T = T;
+    a.stride_t = stride_t;
+    a.E = static_cast<int>(E);
+    a.bias = bias;
+    a.score = score;
+    a.groups = static_cast<int>(groups);
+    a.top_groups = static_cast<int>(top_groups);
+    a.group_score = group_score;
+    a.k = static_cast<int>(k);
+    a.renormalize = renormalize != 0;
+    a.scale = scale;
+    a.ids = ids;
+    a.weights = weights;
+    return status_of(mq::launch_route(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t mq_plan_rows(int64_t T, int64_t k, int64_t E) { return check_slots(T, k, E) ? -1 : mq::plan_rows(T, k, E); }
+
+int mq_expert_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* offsets, int32_t* row_token,
+                   int32_t* row_of, void* stream) {
+    int rc = check_slots(T, k, E);
+    if (rc) return rc;
+    if (!offsets || off(offsets, 4)) return MQ_ERR_INVALID_ARG;
+    if (T > 0 && (!ids || off(ids, 4) || !row_of || off(row_of, 4) || !row_token || off(row_token, 4)))
+        return MQ_ERR_INVALID_ARG;
+    mq::PlanArgs a;
+    a.ids = ids;
+    a.T = T;
+    a.k = static_cast<int>(k);
+    a.E = static_cast<int>(E);
+    a.offsets = offsets;
+    a.row_token = row_token;
+    a.row_of = row_of;
+    a.rows = mq::plan_rows(T, k, E);
+    return status_of(mq::launch_plan(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t mq_mx_experts_up_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I) {
+    if (check_slots(T, k, E) || check_product(T * k, I, D)) return 0;
+    return mx_bytes(mq::plan_rows(T, k, E), D);
+}
+
+int mq_mx_experts_up(const void* x, int x_dtype, int64_t stride_t, int64_t T, int64_t k, int64_t E, int64_t D, int64_t I,
+                     const int32_t* offsets, const int32_t* row_token, const int32_t* row_of, const uint8_t* gate_q,
+                     const uint8_t* gate_s, const uint8_t* up_q, const uint8_t* up_s, void* h, int h_dtype,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_slots(T, k, E);
+    if (rc || (rc = check_product(mq::plan_rows(T, k, E), I, D)) || (rc = check_matrix(E, I, D))) return rc;
+    if (bad_type(x_dtype) || bad_type(h_dtype) || stride_t < 0) return MQ_ERR_INVALID_ARG;
+    if (T == 0) return MQ_OK;
+    if (!x || off(x, type_size(x_dtype)) || !h || off(h, 16)) return MQ_ERR_INVALID_ARG;
+    if (!offsets || off(offsets, 4) || !row_token || off(row_token, 4) || !row_of || off(row_of, 4))
+        return MQ_ERR_INVALID_ARG;
+    if ((rc = check_codes(gate_q, gate_s)) || (rc = check_codes(up_q, up_s))) return rc;
+    if (workspace_bytes < mq_mx_experts_up_workspace_bytes(T, k, E, D, I) || !workspace || off(workspace, 16))
+        return MQ_ERR_INVALID_ARG;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const int64_t P = mq::plan_rows(T, k, E);
+    uint8_t* xq = static_cast<uint8_t*>(workspace);
+    uint8_t* xs = xq + round16(mq::mx_codes_size(P, D));
+    mq::MxQuantArgs q = rows_of(x, x_dtype, T, stride_t, D, xq, xs);
+    q.row_of = row_of;
+    q.copies = static_cast<int>(k);
+    q.out_rows = P;
+    if (mq::launch_mx_quant(q, st) != hipSuccess) return MQ_ERR_HIP;
+    mq::MxGemmArgs a = product(xq, xs, gate_q, gate_s, P, I, D, h, h_dtype);
+    a.w2q = up_q;
+    a.w2s = up_s;
+    a.offsets = offsets;
+    a.row_token = row_token;
+    a.E = static_cast<int>(E);
+    a.T = static_cast<int>(T);
+    return status_of(mq::launch_mx_gemm(a, st));
+}
+
+size_t mq_mx_experts_down_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I) {
+    if (check_slots(T, k, E) || check_product(T * k, D, I)) return 0;
+    const int64_t P = mq::plan_rows(T, k, E);
+    return mx_bytes(P, I) + static_cast<size_t>(P) * static_cast<size_t>(D) * 4;
+}
+
+int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t E, int64_t D, int64_t I,
+                       const int32_t* offsets, const int32_t* row_of, const float* weights, const uint8_t* wq,
+                       const uint8_t* ws, void* y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_slots(T, k, E);
+    if (rc || (rc = check_product(mq::plan_rows(T, k, E), D, I)) || (rc = check_matrix(E, D, I))) return rc;
+    if (bad_type(h_dtype) || bad_type(y_dtype)) return MQ_ERR_INVALID_ARG;
+    if (T == 0) return MQ_OK;
+    if (!h || off(h, type_size(h_dtype)) || !y || off(y, 16)) return MQ_ERR_INVALID_ARG;
+    if (!offsets || off(offsets, 4) || !row_of || off(row_of, 4) || !weights || off(weights, 4)) return MQ_ERR_INVALID_ARG;
+    if ((rc = check_codes(wq, ws))) return rc;
+    if (workspace_bytes < mq_mx_experts_down_workspace_bytes(T, k, E, D, I) || !workspace || off(workspace, 16))
+        return MQ_ERR_INVALID_ARG;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const int64_t P = mq::plan_rows(T, k, E);
+    uint8_t* hq = static_cast<uint8_t*>(workspace);
+    uint8_t* hs = hq + round16(mq::mx_codes_size(P, I));
+    float* rows = reinterpret_cast<float*>(hs + round16(mq::mx_scales_size(P, I)));
+    if (mq::launch_mx_quant(rows_of(h, h_dtype, P, I, I, hq, hs), st) != hipSuccess) return MQ_ERR_HIP;
+    mq::MxGemmArgs a = product(hq, hs, wq, ws, P, D, I, rows, MQ_F32);
+    a.offsets = offsets;
+    a.E = static_cast<int>(E);
+    a.T = static_cast<int>(T);
+    if (mq::launch_mx_gemm(a, st) != hipSuccess) return MQ_ERR_HIP;
+    return status_of(mq::launch_combine(rows, P, row_of, weights, T, static_cast<int>(k), D, y, y_dtype, st));
+}
+
+}  // extern "C"

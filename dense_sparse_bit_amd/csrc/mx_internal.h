@@ -1,0 +1,87 @@
+// Internal interface of the microscaled 4-bit operators and the routing
+// (api_mx.hip checks arguments; mx_quant.hip, mx_gemm.hip and route.hip launch).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mq {
+
+// Layout of a microscaled matrix [R][K] (mq.h): 16-row x 128-input tiles in the lane
+// order of the 16x16x128 matrix instruction, one scale byte per lane and tile.
+constexpr int kMxGroup = 128;      // inputs per code tile
+constexpr int kMxTileBytes = 1024;
+inline int64_t mx_row_tiles(int64_t R) { return (R + 15) / 16; }
+inline int64_t mx_groups(int64_t K) { return (K + kMxGroup - 1) / kMxGroup; }
+inline int64_t mx_quads(int64_t K) { return (mx_groups(K) + 3) / 4; }
+inline int64_t mx_codes_size(int64_t R, int64_t K) { return mx_row_tiles(R) * mx_groups(K) * kMxTileBytes; }
+inline int64_t mx_scales_size(int64_t R, int64_t K) { return mx_row_tiles(R) * mx_quads(K) * 256; }
+
+// rows of an expert plan: every expert's rows start at a multiple of 16
+inline int64_t plan_rows(int64_t T, int64_t k, int64_t E) {
+    const int64_t n = T * k;
+    return (n + 15 * (n < E ? n : E)) / 16 * 16;
+}
+
+// x[b][r][c] of a strided matrix, as it is read by the quantizer. Row r of the output
+// is row r of x, or with `row_of` (int32 [R][copies]) row r goes to the output rows
+// row_of[r][*] that are in [0, out_rows).
+struct MxQuantArgs {
+    const void* x;
+    int dtype;
+    int64_t B, stride_b, R, stride_r;
+    int K;
+    const int32_t* row_of;
+    int copies;
+    int64_t out_rows;
+    uint8_t* codes;
+    uint8_t* scales;
+};
+
+// Y = X W^T over microscaled operands. Dense: M x N outputs. With offsets (expert
+// products): rows are a plan's rows, tile by tile of 16 the expert e with
+// offsets[e] <= row < offsets[e + 1] picks the weights, and rows of no token are zero.
+// With w2q: silu(X W^T) * (X W2^T) (gate and up).
+struct MxGemmArgs {
+    const uint8_t *xq, *xs;
+    const uint8_t *wq, *ws, *w2q, *w2s;
+    int M, N, K;
+    const float* bias;
+    void* y;
+    int y_dtype;
+    const int32_t* offsets;
+    const int32_t* row_token;
+    int E, T;
+};
+
+struct RouteArgs {
+    const void* logits;
+    int dtype;
+    int64_t T, stride_t;
+    int E;
+    const float* bias;
+    int score, groups, top_groups, group_score, k, renormalize;
+    float scale;
+    int32_t* ids;
+    float* weights;
+};
+
+struct PlanArgs {
+    const int32_t* ids;
+    int64_t T;
+    int k, E;
+    int32_t *offsets, *row_token, *row_of;
+    int64_t rows;
+};
+
+hipError_t launch_mx_quant(const MxQuantArgs& a, hipStream_t st);
+hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t B, int64_t R, int64_t K, void* y,
+                             int y_dtype, hipStream_t st);
+hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t st);
+hipError_t launch_route(const RouteArgs& a, hipStream_t st);
+hipError_t launch_plan(const PlanArgs& a, hipStream_t st);
+// y[t] = sum over j of weights[t][j] * rows[row_of[t][j]] (fp32 rows)
+hipError_t launch_combine(const float* rows, int64_t n_rows, const int32_t* row_of, const float* weights, int64_t T,
+                          int k, int64_t D, void* y, int y_dtype, hipStream_t st);
+
+}  // namespace mq

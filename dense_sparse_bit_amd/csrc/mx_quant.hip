@@ -1,0 +1,189 @@
+// Microscaled 4-bit quantization and its reverse.
+//
+// A block is 32 consecutive inputs of a row. X = 2^(floor(log2(max |v|)) - 2) puts the
+// largest magnitude into [4, 8) X; each value becomes the nearest of
+// 0, 0.5, 1, 1.5, 2, 3, 4, 6 times X.
+#include "mx_device.h"
+#include "mx_internal.h"
+
+namespace mq {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T>
+__device__ inline void load8(const T* p, int have, bool vec, float (&v)[8]) {
+    if (vec && have >= 8) {
+        typedef T V8 __attribute__((ext_vector_type(8), aligned(16)));
+        const V8 x = *reinterpret_cast<const V8*>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < have ? static_cast<float>(p[i]) : 0.0f;
+    }
+}
+
+__device__ inline uint32_t peak8(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+}
+
+// max over the four lanes of a block
+__device__ inline uint32_t quad_max(uint32_t m) {
+    m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xB1, 0xf, 0xf, true)));
+    return max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x4E, 0xf, 0xf, true)));
+}
+
+// One workgroup: 16 rows x 512 inputs (four code tiles, one scale entry per lane).
+// Wave w reads rows 4w .. 4w + 3, 1 KB of bf16 at a time; lane l holds inputs
+// 8l .. 8l + 7, four lanes a block. Codes and scales go through LDS, because a tile
+// keeps the rows of a block together and a row's blocks apart: they leave as 4 KB and
+// 256 B runs.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t stride_b, int64_t R, int64_t stride_r, int K,
+                                                       int vec, uint8_t* codes, uint8_t* scales) {
+    __shared__ uint32_t lds_codes[1024];
+    __shared__ uint8_t lds_scales[256];
+    const int G = (K + 127) / 128, G4 = (G + 3) / 4;
+    const int64_t RT = (R + 15) / 16;
+    const int q = blockIdx.x;                       // quad of tiles
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int k0 = q * 512 + 8 * lane;
+    const int64_t b = blockIdx.z;
+    for (int64_t rt = blockIdx.y; rt < RT; rt += gridDim.y) {
+        float v[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = rt * 16 + 4 * wave + i;
+            const int have = r < R ? K - k0 : 0;
+            load8(x + b * stride_b + r * stride_r + k0, have, vec, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 4 * wave + i;
+            const int byte = mx_scale_byte(quad_max(peak8(v[i])));
+            lds_codes[((lane >> 2) * 16 + row) * 4 + (lane & 3)] = mx_codes8(v[i], byte);
+            // blocks beyond K hold zeros, so their byte is 0
+            if ((lane & 3) == 0) lds_scales[(((lane >> 2) & 3) * 16 + row) * 4 + (lane >> 4)] = byte;
+        }
+        __syncthreads();
+        const int t = threadIdx.x;
+        if (q * 4 + (t >> 6) < G)
+            *reinterpret_cast<uint4*>(codes + ((b * RT + rt) * G + q * 4) * 1024 + t * 16) =
+                *reinterpret_cast<const uint4*>(&lds_codes[4 * t]);
+        if (t < 64)
+            *reinterpret_cast<uint32_t*>(scales + ((b * RT + rt) * G4 + q) * 256 + t * 4) =
+                *reinterpret_cast<const uint32_t*>(&lds_scales[4 * t]);
+        __syncthreads();
+    }
+}
+
+// The same blocks, each row written to its places in a plan (mx_experts_up): one wave
+// per row and 512 inputs, 16-byte pieces scattered to `copies` rows.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_mx_quant_scatter(const T* x, int64_t R, int64_t stride_r, int K, int vec,
+                                                               const int32_t* row_of, int copies, int out_rows,
+                                                               uint8_t* codes, uint8_t* scales) {
+    const int G = (K + 127) / 128, G4 = (G + 3) / 4;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+    if (r >= R) return;
+    const int q = blockIdx.y;
+    const int k0 = q * 512 + 8 * lane;
+    float v[8];
+    load8(x + r * stride_r + k0, K - k0, vec, v);
+    const int byte = mx_scale_byte(quad_max(peak8(v)));
+    const uint32_t word = mx_codes8(v, byte);
+    const int g = q * 4 + (lane >> 4), kc = (lane >> 2) & 3;
+    for (int j = 0; j < copies; ++j) {
+        const int p = row_of[r * copies + j];
+        if (p < 0 || p >= out_rows) continue;
+        const int64_t rt = p >> 4;
+        const int row = p & 15;
+        if (g < G) *reinterpret_cast<uint32_t*>(codes + ((rt * G + g) * 64 + kc * 16 + row) * 16 + (lane & 3) * 4) = word;
+        if ((lane & 3) == 0) scales[((rt * G4 + q) * 64 + kc * 16 + row) * 4 + (lane >> 4)] = byte;
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t R, int K,
+                                                         T* y) {
+    const int G = (K + 127) / 128, G4 = (G + 3) / 4;
+    const int64_t RT = (R + 15) / 16, b = blockIdx.z;
+    const int k0 = (blockIdx.x * kThreads + threadIdx.x) * 8;
+    if (k0 >= K) return;
+    const int g = k0 >> 7, kc = (k0 >> 5) & 3;
+    for (int64_t r = blockIdx.y; r < R; r += gridDim.y) {
+        const int64_t rt = b * RT + (r >> 4);
+        const int lane = kc * 16 + static_cast<int>(r & 15);
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + ((rt * G + g) * 64 + lane) * 16 + ((k0 >> 3) & 3) * 4);
+        const int byte = scales[((rt * G4 + (g >> 2)) * 64 + lane) * 4 + (g & 3)];
+        T* out = y + (b * R + r) * K + k0;
+        T v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = byte == 255 ? __uint_as_float(0x7fc00000u) : ldexpf(mx_code_value(w >> (4 * i)), byte - 127);
+            v[i] = mx_round<T>(f);
+        }
+        if (K % 8 == 0) {
+            typedef T V8 __attribute__((ext_vector_type(8), aligned(16)));
+            V8 o;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = v[i];
+            *reinterpret_cast<V8*>(out) = o;
+        } else {
+            for (int i = 0; i < 8 && k0 + i < K; ++i) out[i] = v[i];
+        }
+    }
+}
+
+template <typename T>
+hipError_t quant(const MxQuantArgs& a, hipStream_t st) {
+    const int64_t RT = mx_row_tiles(a.R);
+    const int quads = static_cast<int>(mx_quads(a.K));
+    const T* x = static_cast<const T*>(a.x);
+    // 16-byte loads where every row starts on 16 bytes
+    const int64_t n16 = 16 / sizeof(T);
+    const int vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && a.stride_r % n16 == 0 && a.stride_b % n16 == 0;
+    if (a.row_of) {
+        const dim3 grid(static_cast<unsigned>((a.R + 3) / 4), quads);
+        k_mx_quant_scatter<T><<<grid, kThreads, 0, st>>>(x, a.R, a.stride_r, a.K, vec, a.row_of, a.copies,
+                                                         static_cast<int>(a.out_rows), a.codes, a.scales);
+    } else {
+        const dim3 grid(quads, static_cast<unsigned>(RT < 32768 ? RT : 32768), static_cast<unsigned>(a.B));
+        k_mx_quant<T><<<grid, kThreads, 0, st>>>(x, a.stride_b, a.R, a.stride_r, a.K, vec, a.codes, a.scales);
+    }
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t dequant(const uint8_t* codes, const uint8_t* scales, int64_t B, int64_t R, int64_t K, void* y, hipStream_t st) {
+    const dim3 grid(static_cast<unsigned>((K + kThreads * 8 - 1) / (kThreads * 8)),
+                    static_cast<unsigned>(R < 32768 ? R : 32768), static_cast<unsigned>(B));
+    k_mx_dequant<T><<<grid, kThreads, 0, st>>>(codes, scales, R, static_cast<int>(K), static_cast<T*>(y));
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx_quant(const MxQuantArgs& a, hipStream_t st) {
+    switch (a.dtype) {
+        case MQ_F32: return quant<float>(a, st);
+        case MQ_BF16: return quant<__bf16>(a, st);
+        default: return quant<_Float16>(a, st);
+    }
+}
+
+hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t B, int64_t R, int64_t K, void* y,
+                             int y_dtype, hipStream_t st) {
+    switch (y_dtype) {
+        case MQ_F32: return dequant<float>(codes, scales, B, R, K, y, st);
+        case MQ_BF16: return dequant<__bf16>(codes, scales, B, R, K, y, st);
+        default: return dequant<_Float16>(codes, scales, B, R, K, y, st);
+    }
+}
+
+}  // namespace mq

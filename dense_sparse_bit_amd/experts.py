@@ -1,0 +1,144 @@
+"""Routing to experts, the plan of a batch's rows by expert, and the experts' products
+over microscaled 4-bit weights (include/mq.h)."""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import _lib
+from .mx import _TYPES, MX, _call, _check, _input, _Launch, _mx, _output
+
+_SCORES = {"softmax": 0, "sigmoid": 1}        # MQ_SCORE_*
+_GROUP_SCORES = {"max": 0, "top2": 1}         # MQ_GROUP_*
+
+
+class ExpertPlan(NamedTuple):
+    """A batch's rows by expert: one row per (token, slot) with an expert, each expert's
+    rows from a multiple of 16 on. offsets int32 [experts + 1], row_token int32 [rows]
+    (-1: no token), row_of int32 [T, k] (-1: no row)."""
+    offsets: torch.Tensor
+    row_token: torch.Tensor
+    row_of: torch.Tensor
+
+
+def plan_rows(T: int, k: int, experts: int) -> int:
+    """Rows of a plan of T tokens with k slots each: the most that any ids can take."""
+    rows = _lib.mq_plan_rows(T, k, experts)
+    if rows < 0:
+        raise ValueError(f"no plan for {T} tokens of {k} slots and {experts} experts")
+    return rows
+
+
+def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int | None = None,
+          group_score: str = "max", renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """The k experts of each token and their weights (ids int32 [T, k], weights fp32 [T, k])
+    from logits [T, E]. Scores are softmax or sigmoid; a bias [E] (fp32) is added for the
+    choice alone; with top_groups < groups only experts of the best groups are taken
+    ("max": a group's largest key, "top2": the sum of its two largest). Logits of -inf mask
+    experts: slots that none is left for have id -1 and weight 0. A NaN gives ids -1 and
+    weights NaN."""
+    code = _input(logits, "logits", 2)
+    T, E = logits.shape
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    if group_score not in _GROUP_SCORES:
+        raise ValueError(f"group_score must be one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
+    top_groups = groups if top_groups is None else top_groups
+    if groups <= 0 or E % groups or not 0 < top_groups <= groups:
+        raise ValueError(f"{E} experts do not make {groups} groups of which {top_groups} are kept")
+    if not 0 < k <= top_groups * (E // groups):
+        raise ValueError(f"k = {k} experts of {top_groups * (E // groups)}")
+    device = logits.device
+    with _Launch(device, stream, logits, bias) as at:
+        if bias is not None:
+            _check(bias, "bias", torch.float32, (E,), device)
+        ids = torch.empty((T, k), dtype=torch.int32, device=device) if ids is None else \
+            _check(ids, "ids", torch.int32, (T, k), device)
+        weights = torch.empty((T, k), dtype=torch.float32, device=device) if weights is None else \
+            _check(weights, "weights", torch.float32, (T, k), device)
+        _call("mq_route", logits.data_ptr(), code, T, logits.stride(0), E, None if bias is None else bias.data_ptr(),
+              _SCORES[score], groups, top_groups, _GROUP_SCORES[group_score], k, int(renormalize), scale, ids.data_ptr(),
+              weights.data_ptr(), at.stream)
+    return ids, weights
+
+
+def expert_plan(ids, experts: int, stream=None) -> ExpertPlan:
+    """The plan of ids int32 [T, k]. Ids outside [0, experts), such as -1 or another
+    rank's experts, get no row."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be an int32 tensor [T, k]")
+    T, k = ids.shape
+    device = ids.device
+    with _Launch(device, stream, ids) as at:
+        _check(ids, "ids", torch.int32, (T, k), device)
+        rows = plan_rows(T, k, experts)
+        plan = ExpertPlan(torch.empty(experts + 1, dtype=torch.int32, device=device),
+                          torch.empty(rows, dtype=torch.int32, device=device), torch.empty_like(ids))
+        _call("mq_expert_plan", ids.data_ptr(), T, k, experts, plan.offsets.data_ptr(), plan.row_token.data_ptr(),
+              plan.row_of.data_ptr(), at.stream)
+    return plan
+
+
+def _plan(plan, device):
+    """(T, k, experts, rows) of a plan, its tensors checked."""
+    if not isinstance(plan, ExpertPlan):
+        raise TypeError("plan must be an ExpertPlan (expert_plan)")
+    T, k = plan.row_of.shape
+    E = plan.offsets.numel() - 1
+    rows = plan_rows(T, k, E)
+    _check(plan.offsets, "plan.offsets", torch.int32, (E + 1,), device)
+    _check(plan.row_token, "plan.row_token", torch.int32, (rows,), device)
+    _check(plan.row_of, "plan.row_of", torch.int32, (T, k), device)
+    return T, k, E, rows
+
+
+def mx_experts_up(x, w_gate: MX, w_up: MX, plan: ExpertPlan, out_dtype=torch.bfloat16, h=None, stream=None):
+    """h [rows, I]: for each row of the plan silu(Q(x[t]) w_gate[e]^T) * (Q(x[t]) w_up[e]^T),
+    zero for rows of no token. x [T, D]; w_gate, w_up: MX batches [experts, I, D]."""
+    code = _input(x, "x", 2)
+    device = x.device
+    with _Launch(device, stream, x, w_gate, w_up, plan) as at:
+        T, k, E, rows = _plan(plan, device)
+        _mx(w_gate, "w_gate", device, E)
+        _mx(w_up, "w_up", device, E)
+        D, I = w_gate.cols, w_gate.rows
+        if (w_up.rows, w_up.cols) != (I, D):
+            raise ValueError(f"w_gate is {I} x {D}, w_up is {w_up.rows} x {w_up.cols}")
+        if x.shape != (T, D):
+            raise ValueError(f"x must be [{T}, {D}] for this plan and these weights, got {tuple(x.shape)}")
+        h = _output(h, "h", (rows, I), out_dtype if h is None else h.dtype, device)
+        need = _lib.mq_mx_experts_up_workspace_bytes(T, k, E, D, I)
+        work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        _call("mq_mx_experts_up", x.data_ptr(), code, x.stride(0), T, k, E, D, I, plan.offsets.data_ptr(),
+              plan.row_token.data_ptr(), plan.row_of.data_ptr(), w_gate.codes.data_ptr(), w_gate.scales.data_ptr(),
+              w_up.codes.data_ptr(), w_up.scales.data_ptr(), h.data_ptr(), _TYPES[h.dtype],
+              None if work is None else work.data_ptr(), need, at.stream)
+    return h
+
+
+def mx_experts_down(h, w_down: MX, plan: ExpertPlan, weights, out_dtype=torch.bfloat16, y=None, stream=None):
+    """y[t] = sum over slots j of weights[t, j] * (Q(h[row_of[t, j]]) w_down[e]^T), in the order
+    of the slots. h [rows, I], weights fp32 [T, k], w_down: MX batch [experts, D, I]."""
+    code = _input(h, "h", 2)
+    device = h.device
+    with _Launch(device, stream, h, w_down, plan, weights) as at:
+        T, k, E, rows = _plan(plan, device)
+        _mx(w_down, "w_down", device, E)
+        D, I = w_down.rows, w_down.cols
+        _check(h, "h", h.dtype, (rows, I), device)
+        _check(weights, "weights", torch.float32, (T, k), device)
+        y = _output(y, "y", (T, D), out_dtype if y is None else y.dtype, device)
+        need = _lib.mq_mx_experts_down_workspace_bytes(T, k, E, D, I)
+        work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        _call("mq_mx_experts_down", h.data_ptr(), code, T, k, E, D, I, plan.offsets.data_ptr(), plan.row_of.data_ptr(),
+              weights.data_ptr(), w_down.codes.data_ptr(), w_down.scales.data_ptr(), y.data_ptr(), _TYPES[y.dtype],
+              None if work is None else work.data_ptr(), need, at.stream)
+    return y
+
+
+def mx_experts(x, w_gate: MX, w_up: MX, w_down: MX, plan: ExpertPlan, weights, out_dtype=torch.bfloat16, stream=None):
+    """A mixture's feed-forward layer of x [T, D]: mx_experts_up (its result in bf16), then
+    mx_experts_down."""
+    h = mx_experts_up(x, w_gate, w_up, plan, stream=stream)
+    return mx_experts_down(h, w_down, plan, weights, out_dtype=out_dtype, stream=stream)

@@ -314,6 +314,128 @@ int mq_gemm_residual_separate(const uint8_t* xq, const float* sx, const uint8_t*
                               int group, int bn, int bk, void* y, int y_dtype, float* ws,
                               void* stream);
 
+/*
+ * ---------------------------------------------------------------------------------
+ * Microscaled 4-bit operands, routing to experts and the experts' products.
+ *
+ * The format (OCP microscaling, MXFP4): 32 consecutive inputs of a row are a block
+ * with one scale X = 2^(byte - 127); a value is code * X, the code one of 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 with a sign (4 bits: sign, then the index). gfx950 multiplies such
+ * operands directly, so a product needs no conversion and no scaling of its own.
+ *   Device layout of a matrix [R][K] (RT = ceil(R/16), G = ceil(K/128), G4 = ceil(G/4)):
+ *     codes   RT * G tiles of 1 KB, 16 rows x 128 inputs: the code of (r, k) is nibble
+ *             k % 32 (low nibble first) of the 16 bytes at
+ *               (((r/16)*G + k/128)*64 + ((k/32) % 4)*16 + r % 16) * 16
+ *     scales  one byte per block: the byte of (r, k) is at
+ *               (((r/16)*G4 + k/512)*64 + ((k/32) % 4)*16 + r % 16) * 4 + (k/128) % 4
+ *   Rows up to RT * 16 and blocks up to G * 128 (bytes: G4 * 512) inputs exist and hold
+ *   codes of zero. A batch [B][R][K] is B such matrices in a row (experts' weights:
+ *   B = experts). codes 16-byte aligned, scales 4-byte aligned.
+ *   Any R, K >= 1 (K <= 2^20, R <= 2^24).
+ *
+ * These calls take fp32, bf16 and fp16 (MQ_F16) wherever they take a type. Inputs'
+ * last axis is contiguous, other strides are arguments (in elements, >= 0). Outputs are
+ * contiguous and 16-byte aligned, except the routing's (4-byte). Sums are held in
+ * fp32 and rounded once to the output's type.
+ */
+#define MQ_F16 2
+
+size_t mq_mx_codes_bytes(int64_t R, int64_t K);   /* 0 outside the supported sizes */
+size_t mq_mx_scales_bytes(int64_t R, int64_t K);
+
+/*
+ * Quantization: X = 2^(floor(log2(max |x| over the block)) - 2), at least 2^-127;
+ * codes are x / X rounded to the nearest, ties to the even index, magnitudes above 6 to
+ * 6. A block with a NaN or an infinity gets byte 255 (the format's NaN) and reads back,
+ * and multiplies, as NaN.
+ * x: [B][R][K] with strides stride_b, stride_r.
+ */
+int mq_mx_quantize(const void* x, int x_dtype, int64_t B, int64_t stride_b, int64_t R, int64_t stride_r,
+                   int64_t K, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The values back: y [B][R][K], rounded once to y's type (bf16 and fp32 hold every
+ * quantized value exactly; fp16 those within its range). */
+int mq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t B, int64_t R, int64_t K, void* y,
+                     int y_dtype, void* stream);
+
+/* y[m][n] = sum_k xq[m][k] * wq[n][k] (+ bias[n], fp32, may be NULL). xq/xs: an
+ * M x K matrix, wq/ws: N x K. */
+int mq_mx_gemm(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* ws, int64_t M, int64_t N,
+               int64_t K, const float* bias, void* y, int y_dtype, void* stream);
+
+/* The same from unquantized activations x [M][K] (row stride stride_m): the bits of
+ * mq_mx_quantize followed by mq_mx_gemm. workspace: device scratch of at least
+ * mq_mx_linear_workspace_bytes, 16-byte aligned (may be NULL where that is 0). */
+size_t mq_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int mq_mx_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* wq, const uint8_t* ws, int64_t M,
+                 int64_t N, int64_t K, const float* bias, void* y, int y_dtype, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/*
+ * Routing: the k experts of each token and their weights, from logits [T][E].
+ *   score[e] = softmax over e, or sigmoid, of the logits; a logit of -inf masks its expert
+ *   key[e] = score[e] + bias[e] (bias fp32 [E]); without a bias the logit itself, in
+ *            whose order both scores are. A bias of -inf masks its expert too.
+ *   groups > top_groups: experts are `groups` runs of E / groups; a group is worth its
+ *            largest key (MQ_GROUP_MAX) or the sum of its two largest (MQ_GROUP_TOP2, of
+ *            score + bias); only the top_groups best groups are kept.
+ *   ids      the k experts of largest key, in that order
+ *   weights  their scores; renormalize: divided by their sum; then times scale
+ * Ties go to the lower index, of groups as of experts. Slots that no unmasked expert is
+ * left for hold id -1 and weight 0 (a token whose experts are all masked: all of its
+ * slots). A token with a NaN key (a NaN logit or bias, or +inf under softmax) has ids -1
+ * and weights NaN. Scores and keys are held in 64 bits.
+ * ids: int32 [T][k], weights: fp32 [T][k]. E <= MQ_MAX_EXPERTS, k <= 32, groups <= 64,
+ * k <= top_groups * E / groups.
+ */
+#define MQ_MAX_EXPERTS 1024
+#define MQ_SCORE_SOFTMAX 0
+#define MQ_SCORE_SIGMOID 1
+#define MQ_GROUP_MAX 0
+#define MQ_GROUP_TOP2 1
+int mq_route(const void* logits, int dtype, int64_t T, int64_t stride_t, int64_t E, const float* bias, int score,
+             int64_t groups, int64_t top_groups, int group_score, int64_t k, int renormalize, float scale,
+             int32_t* ids, float* weights, void* stream);
+
+/*
+ * A plan: one row for every (token, slot) whose id is in [0, E), ordered by expert, then
+ * by token and slot; each expert's rows start at a multiple of 16.
+ *   offsets    int32 [E + 1]: expert e's rows are from offsets[e]; offsets[e + 1] is that
+ *              plus its number of rows, rounded up to 16
+ *   row_token  int32 [mq_plan_rows(T, k, E)]: the row's token, -1 for rows of none
+ *   row_of     int32 [T][k]: the slot's row, -1 for ids outside [0, E)
+ * mq_plan_rows is the most rows that any ids can take (-1 outside the supported sizes).
+ * T * k <= 2^27.
+ */
+int64_t mq_plan_rows(int64_t T, int64_t k, int64_t E);
+int mq_expert_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* offsets, int32_t* row_token,
+                   int32_t* row_of, void* stream);
+
+/*
+ * The experts' gate and up products: for row p of expert e with token t = row_token[p]
+ *   h[p][i] = silu(g) * u,  g = Q(x[t]) . gate[e][i],  u = Q(x[t]) . up[e][i]
+ * with silu(g) = g / (1 + exp(-g)); rows of no token are zero. x: [T][D] (row stride
+ * stride_t), gate and up: E matrices I x D, h: [mq_plan_rows][I]. The plan is
+ * mq_expert_plan's; entries of it out of range are taken as "no row".
+ */
+size_t mq_mx_experts_up_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I);
+int mq_mx_experts_up(const void* x, int x_dtype, int64_t stride_t, int64_t T, int64_t k, int64_t E, int64_t D,
+                     int64_t I, const int32_t* offsets, const int32_t* row_token, const int32_t* row_of,
+                     const uint8_t* gate_q, const uint8_t* gate_s, const uint8_t* up_q, const uint8_t* up_s,
+                     void* h, int h_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The experts' down products and their weighted sum, added in the order of the slots:
+ *   y[t][d] = sum over j of weights[t][j] * (Q(h[row_of[t][j]]) . w[e][d])
+ * A slot without a row adds weights[t][j] * 0. h: [mq_plan_rows][I], w: E matrices
+ * D x I, y: [T][D].
+ */
+size_t mq_mx_experts_down_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I);
+int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t E, int64_t D, int64_t I,
+                       const int32_t* offsets, const int32_t* row_of, const float* weights, const uint8_t* wq,
+                       const uint8_t* ws, void* y, int y_dtype, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif
