@@ -76,6 +76,10 @@ mq::MxQuantArgs rows_of(const void* x, int dtype, int64_t R, int64_t stride, int
     return a;
 }
 
+// Whether the experts of a batch meet few rows each: at most two row tiles.
+bool few_tokens(int64_t T) { return T <= 32; }
+size_t tiles_bytes(int64_t P, int64_t E) { return round16(mq::mx_tiles_size(P, E) * 4); }
+
 }  // namespace
 
 extern "C" {
@@ -123,11 +127,12 @@ int mq_mx_gemm(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const ui
     if (!y || off(y, 16)) return MQ_ERR_INVALID_ARG;
     mq::MxGemmArgs a = product(xq, xs, wq, ws, M, N, K, y, y_dtype);
     a.bias = bias;
-    return status_of(mq::launch_mx_gemm(a, static_cast<hipStream_t>(stream)));
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    return status_of(mq::mx_few_rows(M, N, K) ? mq::launch_mx_few(a, st) : mq::launch_mx_wide(a, st));
 }
 
 size_t mq_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    return check_product(M, N, K) ? 0 : mx_bytes(M, K);
+    return check_product(M, N, K) || mq::mx_few_rows(M, N, K) ? 0 : mx_bytes(M, K);
 }
 
 int mq_mx_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* wq, const uint8_t* ws, int64_t M,
@@ -139,16 +144,22 @@ int mq_mx_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* wq
     if (M == 0) return MQ_OK;
     if (!x || off(x, type_size(x_dtype)) || !y || off(y, 16)) return MQ_ERR_INVALID_ARG;
     if ((rc = check_codes(wq, ws))) return rc;
-    if (workspace_bytes < mq_mx_linear_workspace_bytes(M, N, K) || !workspace || off(workspace, 16))
-        return MQ_ERR_INVALID_ARG;
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    mq::MxGemmArgs a = product(nullptr, nullptr, wq, ws, M, N, K, y, y_dtype);
+    a.bias = bias;
+    if (mq::mx_few_rows(M, N, K)) {
+        a.x = x;
+        a.x_dtype = x_dtype;
+        a.stride_x = stride_m;
+        return status_of(mq::launch_mx_few(a, st));
+    }
+    if (workspace_bytes < mx_bytes(M, K) || !workspace || off(workspace, 16)) return MQ_ERR_INVALID_ARG;
     uint8_t* xq = static_cast<uint8_t*>(workspace);
     uint8_t* xs = xq + round16(mq::mx_codes_size(M, K));
-    hipError_t e = mq::launch_mx_quant(rows_of(x, x_dtype, M, stride_m, K, xq, xs), st);
-    if (e != hipSuccess) return MQ_ERR_HIP;
-    mq::MxGemmArgs a = product(xq, xs, wq, ws, M, N, K, y, y_dtype);
-    a.bias = bias;
-    return status_of(mq::launch_mx_gemm(a, st));
+    if (mq::launch_mx_quant(rows_of(x, x_dtype, M, stride_m, K, xq, xs), st) != hipSuccess) return MQ_ERR_HIP;
+    a.xq = xq;
+    a.xs = xs;
+    return status_of(mq::launch_mx_wide(a, st));
 }
 
 int mq_route(const void* logits, int dtype, int64_t T, int64_t stride_t, int64_t E, const float* bias, int score,
@@ -206,8 +217,9 @@ int mq_expert_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t*
 }
 
 size_t mq_mx_experts_up_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I) {
-    if (check_slots(T, k, E) || check_product(T * k, I, D)) return 0;
-    return mx_bytes(mq::plan_rows(T, k, E), D);
+    if (check_slots(T, k, E) || check_product(T * k, I, D) || few_tokens(T)) return 0;
+    const int64_t P = mq::plan_rows(T, k, E);
+    return mx_bytes(P, D) + tiles_bytes(P, E);
 }
 
 int mq_mx_experts_up(const void* x, int x_dtype, int64_t stride_t, int64_t T, int64_t k, int64_t E, int64_t D, int64_t I,
@@ -222,31 +234,42 @@ int mq_mx_experts_up(const void* x, int x_dtype, int64_t stride_t, int64_t T, in
     if (!offsets || off(offsets, 4) || !row_token || off(row_token, 4) || !row_of || off(row_of, 4))
         return MQ_ERR_INVALID_ARG;
     if ((rc = check_codes(gate_q, gate_s)) || (rc = check_codes(up_q, up_s))) return rc;
-    if (workspace_bytes < mq_mx_experts_up_workspace_bytes(T, k, E, D, I) || !workspace || off(workspace, 16))
-        return MQ_ERR_INVALID_ARG;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const int64_t P = mq::plan_rows(T, k, E);
-    uint8_t* xq = static_cast<uint8_t*>(workspace);
-    uint8_t* xs = xq + round16(mq::mx_codes_size(P, D));
-    mq::MxQuantArgs q = rows_of(x, x_dtype, T, stride_t, D, xq, xs);
-    q.row_of = row_of;
-    q.copies = static_cast<int>(k);
-    q.out_rows = P;
-    if (mq::launch_mx_quant(q, st) != hipSuccess) return MQ_ERR_HIP;
-    mq::MxGemmArgs a = product(xq, xs, gate_q, gate_s, P, I, D, h, h_dtype);
+    mq::MxGemmArgs a = product(nullptr, nullptr, gate_q, gate_s, P, I, D, h, h_dtype);
     a.w2q = up_q;
     a.w2s = up_s;
     a.offsets = offsets;
     a.row_token = row_token;
     a.E = static_cast<int>(E);
     a.T = static_cast<int>(T);
-    return status_of(mq::launch_mx_gemm(a, st));
+    if (few_tokens(T)) {
+        a.x = x;
+        a.x_dtype = x_dtype;
+        a.stride_x = stride_t;
+        return status_of(mq::launch_mx_few(a, st));
+    }
+    if (workspace_bytes < mq_mx_experts_up_workspace_bytes(T, k, E, D, I) || !workspace || off(workspace, 16))
+        return MQ_ERR_INVALID_ARG;
+    uint8_t* xq = static_cast<uint8_t*>(workspace);
+    uint8_t* xs = xq + round16(mq::mx_codes_size(P, D));
+    a.xq = xq;
+    a.xs = xs;
+    a.tiles = reinterpret_cast<int32_t*>(xs + round16(mq::mx_scales_size(P, D)));
+    mq::MxQuantArgs q = rows_of(x, x_dtype, T, stride_t, D, xq, xs);
+    q.row_of = row_of;
+    q.copies = static_cast<int>(k);
+    q.out_rows = P;
+    if (mq::launch_mx_quant(q, st) != hipSuccess) return MQ_ERR_HIP;
+    if (mq::launch_mx_tiles(offsets, a.E, P, a.tiles, st) != hipSuccess) return MQ_ERR_HIP;
+    return status_of(mq::launch_mx_wide(a, st));
 }
 
 size_t mq_mx_experts_down_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I) {
     if (check_slots(T, k, E) || check_product(T * k, D, I)) return 0;
     const int64_t P = mq::plan_rows(T, k, E);
-    return mx_bytes(P, I) + static_cast<size_t>(P) * static_cast<size_t>(D) * 4;
+    const size_t rows = round16(P * D * 4);
+    return few_tokens(T) ? rows : rows + mx_bytes(P, I) + tiles_bytes(P, E);
 }
 
 int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t E, int64_t D, int64_t I,
@@ -263,15 +286,28 @@ int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t
         return MQ_ERR_INVALID_ARG;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const int64_t P = mq::plan_rows(T, k, E);
-    uint8_t* hq = static_cast<uint8_t*>(workspace);
-    uint8_t* hs = hq + round16(mq::mx_codes_size(P, I));
-    float* rows = reinterpret_cast<float*>(hs + round16(mq::mx_scales_size(P, I)));
-    if (mq::launch_mx_quant(rows_of(h, h_dtype, P, I, I, hq, hs), st) != hipSuccess) return MQ_ERR_HIP;
-    mq::MxGemmArgs a = product(hq, hs, wq, ws, P, D, I, rows, MQ_F32);
+    float* rows = static_cast<float*>(workspace);
+    mq::MxGemmArgs a = product(nullptr, nullptr, wq, ws, P, D, I, rows, MQ_F32);
     a.offsets = offsets;
     a.E = static_cast<int>(E);
     a.T = static_cast<int>(T);
-    if (mq::launch_mx_gemm(a, st) != hipSuccess) return MQ_ERR_HIP;
+    hipError_t e;
+    if (few_tokens(T)) {
+        a.x = h;
+        a.x_dtype = h_dtype;
+        a.stride_x = I;
+        e = mq::launch_mx_few(a, st);
+    } else {
+        uint8_t* hq = static_cast<uint8_t*>(workspace) + round16(P * D * 4);
+        uint8_t* hs = hq + round16(mq::mx_codes_size(P, I));
+        a.xq = hq;
+        a.xs = hs;
+        a.tiles = reinterpret_cast<int32_t*>(hs + round16(mq::mx_scales_size(P, I)));
+        if (mq::launch_mx_quant(rows_of(h, h_dtype, P, I, I, hq, hs), st) != hipSuccess) return MQ_ERR_HIP;
+        if (mq::launch_mx_tiles(offsets, a.E, P, a.tiles, st) != hipSuccess) return MQ_ERR_HIP;
+        e = mq::launch_mx_wide(a, st);
+    }
+    if (e != hipSuccess) return MQ_ERR_HIP;
     return status_of(mq::launch_combine(rows, P, row_of, weights, T, static_cast<int>(k), D, y, y_dtype, st));
 }
 

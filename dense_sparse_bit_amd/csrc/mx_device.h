@@ -14,11 +14,10 @@ typedef int mx_i4 __attribute__((ext_vector_type(4)));
 typedef int mx_i8 __attribute__((ext_vector_type(8)));
 typedef float mx_f4 __attribute__((ext_vector_type(4)));
 typedef float mx_f16 __attribute__((ext_vector_type(16)));
-
-template <int DT> struct MxType;
-template <> struct MxType<MQ_F32> { using type = float; };
-template <> struct MxType<MQ_BF16> { using type = __bf16; };
-template <> struct MxType<MQ_F16> { using type = _Float16; };
+typedef float mx_f2 __attribute__((ext_vector_type(2)));
+typedef __bf16 mx_b2 __attribute__((ext_vector_type(2)));
+typedef _Float16 mx_h2 __attribute__((ext_vector_type(2)));
+typedef unsigned short mx_u16x2 __attribute__((ext_vector_type(2)));
 
 // Scale byte of a block whose largest magnitude has the fp32 bits `peak`:
 // X = 2^(byte - 127) = 2^(floor(log2(peak)) - 2), at least 2^-127. The exponent field
@@ -30,23 +29,112 @@ __device__ inline int mx_scale_byte(uint32_t peak) {
     return e == 255 ? 255 : (e > 2 ? e - 2 : 0);
 }
 
-// Two values to two 4-bit codes in byte `SEL` of `old`: v * 2^shift rounded to the
-// nearest code, ties to even, magnitudes above 6 to 6. The scaling is exact (a power
-// of two; a result below the normal range rounds to code 0 either way).
-template <int SEL>
-__device__ inline uint32_t mx_codes2(uint32_t old, float a, float b, int shift) {
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, ldexpf(a, shift), ldexpf(b, shift), 1.0f, SEL);
+// The scale as the fp32 operand of the conversion instructions, which take its
+// exponent alone (2^-127 has no normal fp32 form: its subnormal stands for it).
+__device__ inline float mx_scale_value(int byte) {
+    return __uint_as_float(byte ? static_cast<uint32_t>(byte) << 23 : 0x00400000u);
 }
 
-// Eight values of one block to a word of codes (first value in the low nibble); zero
-// codes for a block with byte 255.
-__device__ inline uint32_t mx_codes8(const float (&v)[8], int byte) {
-    if (byte == 255) return 0;
-    const int shift = 127 - byte;
-    uint32_t w = mx_codes2<0>(0, v[0], v[1], shift);
-    w = mx_codes2<1>(w, v[2], v[3], shift);
-    w = mx_codes2<2>(w, v[4], v[5], shift);
-    return mx_codes2<3>(w, v[6], v[7], shift);
+// Eight consecutive values in registers, in the form the conversions take: four fp32
+// pairs, or four words of two 16-bit values.
+template <typename T> struct MxRaw8;
+
+template <> struct MxRaw8<float> {
+    float v[8];
+    __device__ void set(int i, float x) { v[i] = x; }
+    __device__ uint32_t peak() const {           // fp32 bits of the largest magnitude
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        return m;
+    }
+    // v / scale rounded to the nearest code, ties to even, magnitudes above 6 to 6;
+    // first value in the low nibble
+    __device__ uint32_t codes(float scale) const {
+        uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0, v[0], v[1], scale, 0);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], scale, 2);
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], scale, 3);
+    }
+};
+
+template <typename T> struct MxRaw16 {
+    uint32_t w[4];
+    __device__ void set(int i, T x) {
+        const uint32_t b = __builtin_bit_cast(unsigned short, x);
+        w[i >> 1] = (i & 1) ? (w[i >> 1] & 0xffffu) | b << 16 : (w[i >> 1] & 0xffff0000u) | b;
+    }
+    __device__ mx_u16x2 peak2() const {           // magnitudes compare as whole numbers
+        mx_u16x2 m = __builtin_bit_cast(mx_u16x2, w[0] & 0x7fff7fffu);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(mx_u16x2, w[i] & 0x7fff7fffu));
+        return m;
+    }
+    __device__ uint32_t peak_bits() const {
+        const mx_u16x2 m = peak2();
+        return max(m.x, m.y);
+    }
+};
+
+template <> struct MxRaw8<__bf16> : MxRaw16<__bf16> {
+    __device__ uint32_t peak() const { return peak_bits() << 16; }
+    __device__ uint32_t codes(float scale) const {
+        uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(0, __builtin_bit_cast(mx_b2, w[0]), scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(mx_b2, w[1]), scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(mx_b2, w[2]), scale, 2);
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(mx_b2, w[3]), scale, 3);
+    }
+};
+
+template <> struct MxRaw8<_Float16> : MxRaw16<_Float16> {
+    __device__ uint32_t peak() const {
+        return __float_as_uint(static_cast<float>(__builtin_bit_cast(_Float16, static_cast<unsigned short>(peak_bits()))));
+    }
+    __device__ uint32_t codes(float scale) const {
+        uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(0, __builtin_bit_cast(mx_h2, w[0]), scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(mx_h2, w[1]), scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(mx_h2, w[2]), scale, 2);
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(mx_h2, w[3]), scale, 3);
+    }
+};
+
+// `have` of eight values from p (any number; below 8 the rest are zero, at 0 and below
+// nothing is read). Rows need no alignment beyond their type's.
+template <typename T>
+__device__ inline MxRaw8<T> mx_load8(const T* p, int have) {
+    MxRaw8<T> r;
+    if (have >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(4)));
+            const Words a = *reinterpret_cast<const Words*>(p), b = *reinterpret_cast<const Words*>(p + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                r.v[i] = __uint_as_float(a[i]);
+                r.v[4 + i] = __uint_as_float(b[i]);
+            }
+        } else {
+            typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
+            const Words a = *reinterpret_cast<const Words*>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.w[i] = a[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.set(i, i < have ? p[i] : static_cast<T>(0.0f));
+    }
+    return r;
+}
+
+// 32 values of a block to the operand of the matrix instruction and its scale byte.
+// Blocks with a NaN or an infinity hold zero codes.
+template <typename T>
+__device__ inline mx_i4 mx_quant32(const MxRaw8<T> (&v)[4], int& byte) {
+    byte = mx_scale_byte(max(max(v[0].peak(), v[1].peak()), max(v[2].peak(), v[3].peak())));
+    const float scale = mx_scale_value(byte);
+    mx_i4 c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = byte == 255 ? 0 : static_cast<int>(v[i].codes(scale));
+    return c;
 }
 
 // value of a 4-bit code: 0, 0.5, 1, 1.5, 2, 3, 4, 6 with the sign in bit 3
@@ -58,5 +146,38 @@ __device__ inline float mx_code_value(uint32_t c) {
 
 template <typename T>
 __device__ inline T mx_round(float v) { return static_cast<T>(v); }
+
+// Two values rounded to a 16-bit type, the first in the low half.
+template <typename T>
+__device__ inline uint32_t mx_pack2(float a, float b) {
+    typedef T V2 __attribute__((ext_vector_type(2)));
+    const V2 v = {static_cast<T>(a), static_cast<T>(b)};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// Four neighbouring outputs y[at .. at + 3] of type `dtype`; `have` of them exist, and
+// `vec` says that `at` is a multiple of 4 wherever all four do.
+__device__ inline void mx_store4(void* y, int dtype, int64_t at, int have, bool vec, float a, float b, float c, float d) {
+    if (vec && have >= 4) {
+        if (dtype == MQ_F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(y) + at) = make_float4(a, b, c, d);
+        } else {
+            const uint2 p = dtype == MQ_BF16 ? make_uint2(mx_pack2<__bf16>(a, b), mx_pack2<__bf16>(c, d))
+                                             : make_uint2(mx_pack2<_Float16>(a, b), mx_pack2<_Float16>(c, d));
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) = p;
+        }
+        return;
+    }
+    const float v[4] = {a, b, c, d};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i >= have) return;
+        if (dtype == MQ_F32) static_cast<float*>(y)[at + i] = v[i];
+        else if (dtype == MQ_BF16) static_cast<__bf16*>(y)[at + i] = static_cast<__bf16>(v[i]);
+        else static_cast<_Float16*>(y)[at + i] = static_cast<_Float16>(v[i]);
+    }
+}
+
+__device__ inline float mx_silu(float g) { return g / (1.0f + __expf(-g)); }
 
 }  // namespace mq

@@ -39,19 +39,23 @@ struct MxQuantArgs {
 };
 
 // Y = X W^T over microscaled operands. Dense: M x N outputs. With offsets (expert
-// products): rows are a plan's rows, tile by tile of 16 the expert e with
-// offsets[e] <= row < offsets[e + 1] picks the weights, and rows of no token are zero.
-// With w2q: silu(X W^T) * (X W2^T) (gate and up).
+// products): rows are a plan's rows, the expert e with offsets[e] <= row < offsets[e + 1]
+// picks the weights, and rows of no token are zero. With w2q: silu(X W^T) * (X W2^T)
+// (gate and up).
 struct MxGemmArgs {
-    const uint8_t *xq, *xs;
+    const uint8_t *xq, *xs;          // quantized operand, or
+    const void* x;                   // rows to be quantized on the way (null: xq, xs)
+    int x_dtype;
+    int64_t stride_x;
     const uint8_t *wq, *ws, *w2q, *w2s;
     int M, N, K;
     const float* bias;
     void* y;
     int y_dtype;
     const int32_t* offsets;
-    const int32_t* row_token;
+    const int32_t* row_token;        // x's row of each of the plan's rows (x given), and which rows are live
     int E, T;
+    int32_t* tiles;                  // row blocks of the plan (launch_mx_tiles)
 };
 
 struct RouteArgs {
@@ -77,7 +81,15 @@ struct PlanArgs {
 hipError_t launch_mx_quant(const MxQuantArgs& a, hipStream_t st);
 hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t B, int64_t R, int64_t K, void* y,
                              int y_dtype, hipStream_t st);
-hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t st);
+// The product's kernel: split over K, with the rows quantized on the way where they are
+// not yet (M is the rows of a product, or of the busiest plan that could be), or tiles
+// of many rows.
+bool mx_few_rows(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx_few(const MxGemmArgs& a, hipStream_t st);
+hipError_t launch_mx_wide(const MxGemmArgs& a, hipStream_t st);
+// Row blocks of a plan of P rows, for launch_mx_wide; entries of `tiles`.
+int64_t mx_tiles_size(int64_t P, int64_t E);
+hipError_t launch_mx_tiles(const int32_t* offsets, int E, int64_t P, int32_t* tiles, hipStream_t st);
 hipError_t launch_route(const RouteArgs& a, hipStream_t st);
 hipError_t launch_plan(const PlanArgs& a, hipStream_t st);
 // y[t] = sum over j of weights[t][j] * rows[row_of[t][j]] (fp32 rows)

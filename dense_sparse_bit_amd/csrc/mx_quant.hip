@@ -11,26 +11,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T>
-__device__ inline void load8(const T* p, int have, bool vec, float (&v)[8]) {
-    if (vec && have >= 8) {
-        typedef T V8 __attribute__((ext_vector_type(8), aligned(16)));
-        const V8 x = *reinterpret_cast<const V8*>(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(x[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < have ? static_cast<float>(p[i]) : 0.0f;
-    }
-}
-
-__device__ inline uint32_t peak8(const float (&v)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    return m;
-}
-
 // max over the four lanes of a block
 __device__ inline uint32_t quad_max(uint32_t m) {
     m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xB1, 0xf, 0xf, true)));
@@ -44,7 +24,7 @@ __device__ inline uint32_t quad_max(uint32_t m) {
 // 256 B runs.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t stride_b, int64_t R, int64_t stride_r, int K,
-                                                       int vec, uint8_t* codes, uint8_t* scales) {
+                                                       uint8_t* codes, uint8_t* scales) {
     __shared__ uint32_t lds_codes[1024];
     __shared__ uint8_t lds_scales[256];
     const int G = (K + 127) / 128, G4 = (G + 3) / 4;
@@ -54,18 +34,17 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t strid
     const int k0 = q * 512 + 8 * lane;
     const int64_t b = blockIdx.z;
     for (int64_t rt = blockIdx.y; rt < RT; rt += gridDim.y) {
-        float v[4][8];
+        MxRaw8<T> v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t r = rt * 16 + 4 * wave + i;
-            const int have = r < R ? K - k0 : 0;
-            load8(x + b * stride_b + r * stride_r + k0, have, vec, v[i]);
+            v[i] = mx_load8(x + b * stride_b + r * stride_r + k0, r < R ? K - k0 : 0);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 4 * wave + i;
-            const int byte = mx_scale_byte(quad_max(peak8(v[i])));
-            lds_codes[((lane >> 2) * 16 + row) * 4 + (lane & 3)] = mx_codes8(v[i], byte);
+            const int byte = mx_scale_byte(quad_max(v[i].peak()));
+            lds_codes[((lane >> 2) * 16 + row) * 4 + (lane & 3)] = byte == 255 ? 0 : v[i].codes(mx_scale_value(byte));
             // blocks beyond K hold zeros, so their byte is 0
             if ((lane & 3) == 0) lds_scales[(((lane >> 2) & 3) * 16 + row) * 4 + (lane >> 4)] = byte;
         }
@@ -84,7 +63,7 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t strid
 // The same blocks, each row written to its places in a plan (mx_experts_up): one wave
 // per row and 512 inputs, 16-byte pieces scattered to `copies` rows.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_mx_quant_scatter(const T* x, int64_t R, int64_t stride_r, int K, int vec,
+__global__ __launch_bounds__(kThreads) void k_mx_quant_scatter(const T* x, int64_t R, int64_t stride_r, int K,
                                                                const int32_t* row_of, int copies, int out_rows,
                                                                uint8_t* codes, uint8_t* scales) {
     const int G = (K + 127) / 128, G4 = (G + 3) / 4;
@@ -93,10 +72,9 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant_scatter(const T* x, int64
     if (r >= R) return;
     const int q = blockIdx.y;
     const int k0 = q * 512 + 8 * lane;
-    float v[8];
-    load8(x + r * stride_r + k0, K - k0, vec, v);
-    const int byte = mx_scale_byte(quad_max(peak8(v)));
-    const uint32_t word = mx_codes8(v, byte);
+    const MxRaw8<T> v = mx_load8(x + r * stride_r + k0, K - k0);
+    const int byte = mx_scale_byte(quad_max(v.peak()));
+    const uint32_t word = byte == 255 ? 0 : v.codes(mx_scale_value(byte));
     const int g = q * 4 + (lane >> 4), kc = (lane >> 2) & 3;
     for (int j = 0; j < copies; ++j) {
         const int p = row_of[r * copies + j];
@@ -145,16 +123,13 @@ hipError_t quant(const MxQuantArgs& a, hipStream_t st) {
     const int64_t RT = mx_row_tiles(a.R);
     const int quads = static_cast<int>(mx_quads(a.K));
     const T* x = static_cast<const T*>(a.x);
-    // 16-byte loads where every row starts on 16 bytes
-    const int64_t n16 = 16 / sizeof(T);
-    const int vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && a.stride_r % n16 == 0 && a.stride_b % n16 == 0;
     if (a.row_of) {
         const dim3 grid(static_cast<unsigned>((a.R + 3) / 4), quads);
-        k_mx_quant_scatter<T><<<grid, kThreads, 0, st>>>(x, a.R, a.stride_r, a.K, vec, a.row_of, a.copies,
+        k_mx_quant_scatter<T><<<grid, kThreads, 0, st>>>(x, a.R, a.stride_r, a.K, a.row_of, a.copies,
                                                          static_cast<int>(a.out_rows), a.codes, a.scales);
     } else {
         const dim3 grid(quads, static_cast<unsigned>(RT < 32768 ? RT : 32768), static_cast<unsigned>(a.B));
-        k_mx_quant<T><<<grid, kThreads, 0, st>>>(x, a.stride_b, a.R, a.stride_r, a.K, vec, a.codes, a.scales);
+        k_mx_quant<T><<<grid, kThreads, 0, st>>>(x, a.stride_b, a.R, a.stride_r, a.K, a.codes, a.scales);
     }
     return hipGetLastError();
 }
