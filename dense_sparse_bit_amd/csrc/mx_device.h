@@ -41,7 +41,11 @@ template <typename T> struct MxRaw8;
 
 template <> struct MxRaw8<float> {
     float v[8];
-    __device__ void set(int i, float x) { v[i] = x; }
+    __device__ void push(float x) {              // x becomes the first, the others move up
+#pragma unroll
+        for (int i = 7; i > 0; --i) v[i] = v[i - 1];
+        v[0] = x;
+    }
     __device__ uint32_t peak() const {           // fp32 bits of the largest magnitude
         uint32_t m = 0;
 #pragma unroll
@@ -60,9 +64,10 @@ template <> struct MxRaw8<float> {
 
 template <typename T> struct MxRaw16 {
     uint32_t w[4];
-    __device__ void set(int i, T x) {
-        const uint32_t b = __builtin_bit_cast(unsigned short, x);
-        w[i >> 1] = (i & 1) ? (w[i >> 1] & 0xffffu) | b << 16 : (w[i >> 1] & 0xffff0000u) | b;
+    __device__ void push(T x) {
+#pragma unroll
+        for (int i = 3; i > 0; --i) w[i] = w[i] << 16 | w[i - 1] >> 16;
+        w[0] = w[0] << 16 | __builtin_bit_cast(unsigned short, x);
     }
     __device__ mx_u16x2 peak2() const {           // magnitudes compare as whole numbers
         mx_u16x2 m = __builtin_bit_cast(mx_u16x2, w[0] & 0x7fff7fffu);
@@ -119,22 +124,25 @@ __device__ inline MxRaw8<T> mx_load8(const T* p, int have) {
             for (int i = 0; i < 4; ++i) r.w[i] = a[i];
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r.set(i, i < have ? p[i] : static_cast<T>(0.0f));
+        r = MxRaw8<T>{};
+#pragma clang loop unroll(disable)
+        for (int i = have - 1; i >= 0; --i) r.push(p[i]);   // rare: kept small
     }
     return r;
 }
 
-// 32 values of a block to the operand of the matrix instruction and its scale byte.
-// Blocks with a NaN or an infinity hold zero codes.
+// max over the four lanes of a block
+__device__ inline uint32_t mx_quad_max(uint32_t m) {
+    m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xB1, 0xf, 0xf, true)));
+    return max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x4E, 0xf, 0xf, true)));
+}
+
+// Eight values of a block whose other values are in the lane's quad: their word of
+// codes (zero codes where the block has a NaN or an infinity) and the block's byte.
 template <typename T>
-__device__ inline mx_i4 mx_quant32(const MxRaw8<T> (&v)[4], int& byte) {
-    byte = mx_scale_byte(max(max(v[0].peak(), v[1].peak()), max(v[2].peak(), v[3].peak())));
-    const float scale = mx_scale_value(byte);
-    mx_i4 c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = byte == 255 ? 0 : static_cast<int>(v[i].codes(scale));
-    return c;
+__device__ inline uint32_t mx_quant8(const MxRaw8<T>& v, int& byte) {
+    byte = mx_scale_byte(mx_quad_max(v.peak()));
+    return byte == 255 ? 0 : v.codes(mx_scale_value(byte));
 }
 
 // value of a 4-bit code: 0, 0.5, 1, 1.5, 2, 3, 4, 6 with the sign in bit 3
@@ -178,6 +186,8 @@ __device__ inline void mx_store4(void* y, int dtype, int64_t at, int have, bool 
     }
 }
 
-__device__ inline float mx_silu(float g) { return g / (1.0f + __expf(-g)); }
+// g / (1 + exp(-g)). The hardware's reciprocal is within one unit in the last place, as
+// the exponential is; a division would cost twice the instructions of all the rest.
+__device__ inline float mx_silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 }  // namespace mq

@@ -38,82 +38,143 @@ __device__ inline int expert_of(const int32_t* offsets, int E, int row) {
 }
 
 // ------------------------------------------------------------------- few rows
-// The matrix of rows as it is found: codes and scales of a quantized operand (MxReady),
-// or rows of a type that are quantized here, block by block, in the lane that feeds the
-// block to the matrix instruction.
-struct MxReady {};
+// A batch is four groups (512 inputs) of a wave's run of K.
+constexpr int kBatch = 4;
+// The rows' codes of a batch in LDS, per 16 rows: [16 blocks][16 rows][16 B]; blocks are
+// 16 B further apart than they are long, so that a row's 16 blocks, written by one
+// instruction, fall into different banks. Then a word of scales per (block % 4, row).
+constexpr int kBlockPitch = 16 * 16 + 16;
+constexpr int kRowsLds = 16 * kBlockPitch + 256;
 
-template <typename XT, int U>
-struct XBlocks {                                   // blocks of U groups of one lane's row
-    MxRaw8<XT> v[U][4];
-    __device__ void load(const MxGemmArgs& a, int64_t row, int, int kc, int g, int end) {
-        const XT* p = static_cast<const XT*>(a.x) + row * a.stride_x;
+struct MxReady {};                                   // rows that are quantized already
+
+// Quantizes rows 0 .. rows - 1 (row i of x: row_at(i), wave-uniform) of the groups
+// [g, min(g + 4, end)) into the wave's LDS: a row's 512 inputs are one 16-byte load a
+// lane, four lanes a block. RB rows are loaded before the first is converted; `between`
+// runs after the first loads are issued (the weights' loads, which must come after them:
+// loads complete in order).
+template <typename XT, int RB, typename Row, typename Between>
+__device__ __forceinline__ void rows_to_lds(const XT* x, int64_t stride, int K, int rows, Row row_at, int g, int end,
+                                            uint8_t* lds, Between between) {
+    const int lane = threadIdx.x & 63;
+    const int k = g * 128 + 8 * lane;
+    auto put = [&](int r, const MxRaw8<XT>& v) __attribute__((always_inline)) {
+        int byte;
+        const uint32_t word = mx_quant8(v, byte);
+        uint8_t* to = lds + (r >> 4) * kRowsLds;
+        *reinterpret_cast<uint32_t*>(to + (lane >> 2) * kBlockPitch + (r & 15) * 16 + (lane & 3) * 4) = word;
+        if ((lane & 3) == 0) to[16 * kBlockPitch + ((lane >> 2 & 3) * 16 + (r & 15)) * 4 + (lane >> 4)] = byte;
+    };
+    if (g + kBatch <= end && (g + kBatch) * 128 <= K) {
+        MxRaw8<XT> v[RB];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = (g + u) * 128 + kc * 32;
-            const int have = g + u < end ? a.K - k : 0;
-            if (have >= 32) {
+        for (int i = 0; i < RB; ++i) v[i] = mx_load8(x + row_at(min(i, rows - 1)) * stride + k, 8);
+        between();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[u][i] = mx_load8(p + k + 8 * i, 8);
-            } else {
+        for (int i = 0; i < RB; ++i)
+            if (RB == 1 || i < rows) put(i, v[i]);
+        for (int r = RB; r < rows; r += RB) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[u][i] = mx_load8(p + k + 8 * i, have - 8 * i);
+            for (int i = 0; i < RB; ++i) v[i] = mx_load8(x + row_at(min(r + i, rows - 1)) * stride + k, 8);
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+                if (r + i < rows) put(r + i, v[i]);
+        }
+    } else {
+        // the end of the run or of the rows
+        between();
+        const int have = min(K, end * 128) - k;
+        for (int r = 0; r < rows; ++r) put(r, mx_load8(x + row_at(r) * stride + k, have));
+    }
+}
+
+// One wave's share of 16 MT rows x NT weight tiles: the products of the groups
+// [g0, end). w and ws: the tiles' codes and scales, at this lane. Bound by the weights'
+// read: a batch's loads are all issued before its first product.
+template <typename XT, int NT, int MT, int RB, typename Row>
+__device__ __forceinline__ void few_run(const MxGemmArgs& a, const uint8_t* const (&w)[NT], const uint8_t* const (&ws)[NT],
+                                        int rows, Row row_at, int g0, int end, uint8_t* lds, mx_f4 (&acc)[NT][MT]) {
+    const int lane = threadIdx.x & 63;
+    for (int g = g0; g < end; g += kBatch) {
+        mx_i4 wc[kBatch][NT];
+        int wb[kBatch][NT];
+        auto load_w = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int h = min(g + u, end - 1);         // past the run's end: its last, times codes of zero
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    wc[u][j] = *reinterpret_cast<const mx_i4*>(w[j] + static_cast<int64_t>(h) * 1024);
+                    wb[u][j] = ws[j][(h >> 2) * 256 + (h & 3)];
+                }
+            }
+        };
+        if constexpr (__is_same(XT, MxReady)) {
+            const int G = (a.K + 127) / 128, G4 = (G + 3) / 4;
+            mx_i4 c[kBatch][MT];
+            int b[kBatch][MT];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int h = min(g + u, end - 1);
+                    const int64_t m = row_at(min(16 * i + (lane & 15), rows - 1));
+                    const int at = (lane & 48) + static_cast<int>(m & 15);
+                    c[u][i] = *reinterpret_cast<const mx_i4*>(a.xq + (((m >> 4) * G + h) * 64 + at) * 16);
+                    b[u][i] = a.xs[(((m >> 4) * G4 + (h >> 2)) * 64 + at) * 4 + (h & 3)];
+                    if (g + u >= end) { c[u][i] = mx_i4{0, 0, 0, 0}; b[u][i] = 0; }
+                }
+            }
+            load_w();
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[j][i] = mfma16(wc[u][j], c[u][i], acc[j][i], wb[u][j], b[u][i]);
+        } else {
+            __builtin_amdgcn_wave_barrier();               // the last batch's reads come first
+            rows_to_lds<XT, RB>(static_cast<const XT*>(a.x), a.stride_x, a.K, rows, row_at, g, end, lds, load_w);
+            __builtin_amdgcn_wave_barrier();               // a wave's LDS accesses complete in order
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const uint8_t* from = lds + i * kRowsLds;
+                const uint32_t b = *reinterpret_cast<const uint32_t*>(from + 16 * kBlockPitch + lane * 4);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const mx_i4 c = *reinterpret_cast<const mx_i4*>(from + (u * 4 + (lane >> 4)) * kBlockPitch + (lane & 15) * 16);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[j][i] = mfma16(wc[u][j], c, acc[j][i], wb[u][j], b >> 8 * u);
+                }
             }
         }
     }
-    __device__ void take(int u, mx_i4& codes, int& byte) const { codes = mx_quant32<XT>(v[u], byte); }
-};
-
-template <int U>
-struct XBlocks<MxReady, U> {
-    mx_i4 c[U];
-    int b[U];
-    __device__ void load(const MxGemmArgs& a, int64_t row, int G4, int kc, int g, int end) {
-        const int G = (a.K + 127) / 128;
-        const int at = kc * 16 + static_cast<int>(row & 15);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = g + u < end ? g + u : end - 1;
-            const mx_i4 t = *reinterpret_cast<const mx_i4*>(a.xq + (((row >> 4) * G + h) * 64 + at) * 16);
-            c[u] = g + u < end ? t : mx_i4{0, 0, 0, 0};
-            b[u] = g + u < end ? a.xs[(((row >> 4) * G4 + (h >> 2)) * 64 + at) * 4 + (h & 3)] : 0;
-        }
-    }
-    __device__ void take(int u, mx_i4& codes, int& byte) const { codes = c[u]; byte = b[u]; }
-};
+}
 
 // One workgroup: 16 MT rows x NT column tiles of 16 (GATED: NT / 2 of each matrix), its
 // waves each a run of K; the partial sums are added through LDS in the order of the
-// waves. Bound by the weights' read: every load of a wave's run is issued before its
-// first product, the rows' first, so that they are quantized while the weights arrive.
-template <typename XT, int NT, int MT, bool GATED>
+// waves.
+template <typename XT, int NT, int MT, int RB, bool GATED>
 __global__ __launch_bounds__(512) void k_mx_few(MxGemmArgs a) {
-    constexpr int U = sizeof(XT) == 4 || MT > 1 ? 2 : 4;     // groups loaded together
     constexpr int NC = GATED ? NT / 2 : NT;
-    extern __shared__ mx_f4 red[];                            // [waves][NT * MT][64]
+    extern __shared__ __align__(16) uint8_t lds[];    // each wave's rows, then the waves' sums
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int G = (a.K + 127) / 128, G4 = (G + 3) / 4;
     const int n_tiles = (a.N + 15) / 16;
     const int row0 = blockIdx.y * 16 * MT, ct = blockIdx.x * NC;
-    int e = 0;
-    if (a.offsets) e = __builtin_amdgcn_readfirstlane(expert_of(a.offsets, a.E, row0));
-    bool live[MT];
-    int64_t xrow[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int m = row0 + 16 * i + (lane & 15);
-        live[i] = m < a.M && e >= 0;
-        xrow[i] = m < a.M ? m : a.M - 1;
-        if (a.row_token) {
-            const int t = a.row_token[xrow[i]];
-            const bool ok = static_cast<unsigned>(t) < static_cast<unsigned>(a.T);
-            live[i] = live[i] && ok;
-            if (a.x) xrow[i] = ok ? t : 0;
-        }
+    int rows = min(16 * MT, a.M - row0), e = 0, token = 0;
+    uint64_t alive = ~0ull;                            // which of the rows have a token
+    if (a.offsets) {
+        // (MT = 1) lane l % 16 is row l % 16 of the plan's tile
+        token = a.row_token ? a.row_token[row0 + (lane & 15)] : 0;
+        alive = __ballot(static_cast<unsigned>(token) < static_cast<unsigned>(a.T)) & 0xffff;
+        e = __builtin_amdgcn_readfirstlane(expert_of(a.offsets, a.E, row0));
+        if (e < 0) alive = 0;
+        rows = 64 - __builtin_clzll(alive | 1);
     }
     mx_f4 acc[NT][MT] = {};
-    if (e >= 0) {
+    if (alive) {
         const uint8_t *w[NT], *ws[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -122,51 +183,27 @@ __global__ __launch_bounds__(512) void k_mx_few(MxGemmArgs a) {
             w[j] = ((GATED && (j & 1)) ? a.w2q : a.wq) + tile * G * 1024 + lane * 16;
             ws[j] = ((GATED && (j & 1)) ? a.w2s : a.ws) + tile * G4 * 256 + lane * 4;
         }
+        const bool gather = a.row_token && a.x;
+        auto row_at = [&](int i) __attribute__((always_inline)) -> int64_t {
+            if (!gather) return row0 + i;
+            const int t = __builtin_amdgcn_readlane(token, i & 15);
+            return static_cast<unsigned>(t) < static_cast<unsigned>(a.T) ? t : 0;
+        };
+        const int g0 = static_cast<int>(static_cast<int64_t>(G) * wave / waves);
         const int end = static_cast<int>(static_cast<int64_t>(G) * (wave + 1) / waves);
-        for (int g = static_cast<int>(static_cast<int64_t>(G) * wave / waves); g < end; g += U) {
-            XBlocks<XT, U> x[MT];
-#pragma unroll
-            for (int i = 0; i < MT; ++i) x[i].load(a, xrow[i], G4, lane >> 4, g, end);
-            mx_i4 wc[U][NT];
-            int wb[U][NT];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = g + u < end ? g + u : end - 1;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    wc[u][j] = *reinterpret_cast<const mx_i4*>(w[j] + static_cast<int64_t>(h) * 1024);
-                    wb[u][j] = ws[j][(h >> 2) * 256 + (h & 3)];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    mx_i4 c;
-                    int b;
-                    x[i].take(u, c, b);
-                    // past the run's end both operands are there, and the rows' codes zero
-                    if (g + u >= end) { c = mx_i4{0, 0, 0, 0}; b = 0; }
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        acc[j][i] = mfma16(wc[u][j], c, acc[j][i], wb[u][j], b);
-                }
-            }
+        if constexpr (__is_same(XT, MxReady)) {
+            auto here = [&](int i) __attribute__((always_inline)) -> int64_t { return row0 + i; };
+            few_run<XT, NT, MT, RB>(a, w, ws, rows, here, g0, end, nullptr, acc);
+        } else {
+            few_run<XT, NT, MT, RB>(a, w, ws, rows, row_at, g0, end, lds + wave * MT * kRowsLds, acc);
         }
     }
+    mx_f4* red = reinterpret_cast<mx_f4*>(lds);        // [waves][NT * MT][64]
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < MT; ++i) red[(wave * NT * MT + j * MT + i) * 64 + lane] = acc[j][i];
-    // which rows are live, for the threads that write them
-    __shared__ unsigned short alive[MT];
-    if (wave == 0) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const unsigned long long mask = __ballot(live[i]);
-            if (lane == 0) alive[i] = static_cast<unsigned short>(mask & 0xffff);
-        }
-    }
     __syncthreads();
     for (int o = threadIdx.x; o < NC * MT * 64; o += blockDim.x) {
         const int l = o & 63, i = (o >> 6) % MT, c = (o >> 6) / MT;
@@ -185,25 +222,30 @@ __global__ __launch_bounds__(512) void k_mx_few(MxGemmArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] += n + r < a.N ? a.bias[n + r] : 0.0f;
         }
-        if (!(alive[i] >> (l & 15) & 1)) v = mx_f4{0, 0, 0, 0};
+        if (GATED && !(alive >> (l & 15) & 1)) v = mx_f4{0, 0, 0, 0};
         mx_store4(a.y, a.y_dtype, static_cast<int64_t>(m) * a.N + n, a.N - n, a.N % 4 == 0, v[0], v[1], v[2], v[3]);
     }
 }
 
-template <typename XT>
+template <typename XT, int NT, int MT, int RB, bool GATED>
 hipError_t few(const MxGemmArgs& a, hipStream_t st) {
-    const unsigned tiles = static_cast<unsigned>((a.N + 15) / 16);
+    constexpr int NC = GATED ? NT / 2 : NT;
+    const unsigned cols = static_cast<unsigned>(((a.N + 15) / 16 + NC - 1) / NC);
+    const unsigned rows = static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT));
     const int G = (a.K + 127) / 128;
-    const int waves = G >= 16 ? 8 : (G >= 4 ? 4 : 1);
-    const unsigned rows = static_cast<unsigned>((a.M + 15) / 16);
-    if (a.w2q) {
-        k_mx_few<XT, 2, 1, true><<<dim3(tiles, rows), 64 * waves, waves * 2 * 1024, st>>>(a);
-    } else if (a.offsets || a.M <= 16) {
-        k_mx_few<XT, 1, 1, false><<<dim3(tiles, rows), 64 * waves, waves * 1024, st>>>(a);
-    } else {
-        k_mx_few<XT, 2, 2, false><<<dim3((tiles + 1) / 2, (rows + 1) / 2), 64 * waves, waves * 4 * 1024, st>>>(a);
-    }
+    const int waves = G >= 32 ? 8 : (G >= 8 ? 4 : (G >= 4 ? 2 : 1));
+    const size_t lds = static_cast<size_t>(waves) * (kRowsLds > NT * 1024 ? kRowsLds : NT * 1024) * MT;
+    k_mx_few<XT, NT, MT, RB, GATED><<<dim3(cols, rows), 64 * waves, lds, st>>>(a);
     return hipGetLastError();
+}
+
+// rows: the most that a row tile can have
+template <typename XT>
+hipError_t few_rows(const MxGemmArgs& a, int64_t rows, hipStream_t st) {
+    if (a.w2q) return rows == 1 ? few<XT, 2, 1, 1, true>(a, st) : few<XT, 2, 1, 8, true>(a, st);
+    if (rows == 1) return few<XT, 1, 1, 1, false>(a, st);
+    if (a.offsets || rows <= 16) return few<XT, 1, 1, 8, false>(a, st);
+    return few<XT, 2, 2, 16, false>(a, st);
 }
 
 // ------------------------------------------------------------------- many rows
@@ -229,11 +271,12 @@ __device__ inline int load4(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
 // One wave's part of a tile of SUB * 32 rows: 64 columns (GATED: 32 of gate and 32 of
 // up). Its weights go from memory straight to registers, three steps of 128 inputs
 // ahead (the layout is the instruction's own); the rows, which the four waves share, go
-// through two LDS stages, one barrier a step. Reads beyond the operands' ends give zero
+// through four LDS stages, one barrier a step. Reads beyond the operands' ends give zero
 // (buffer loads with the operands' sizes).
-template <int SUB, bool GATED>
+template <typename T, int SUB, bool GATED>
 __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int rt0, int n16, int e, int col16) {
     constexpr int XL = (SUB + 1) / 2;                // 16-row tiles that a wave fetches a step
+    static_assert(4 * XL <= kBlockTiles);            // (odd SUB: two tiles of zeros too, and no branch)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int G = (a.K + 127) / 128, G4 = (G + 3) / 4;
@@ -255,25 +298,16 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
     mx_i4 W[4][2][2];                                // [step % 4][column pair][half]
     // The scalar part of an offset stays within the buffer (the range check subtracts
     // it): steps past the last read the last again, and are not used.
-    auto load_w = [&](int step, mx_i4 (&w)[2][2]) __attribute__((always_inline)) {
-        const int g = min(step, G - 1);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            w[0][h] = load16(wr, lane_pair + h * 512, g * 1024);
-            w[1][h] = load16(w2r, lane_pair + pair1 + h * 512, g * 1024);
-        }
+    auto load_w = [&](int step, int piece) __attribute__((always_inline)) {       // a fourth of a step's weights
+        const int g = min(step, G - 1), h = piece & 1;
+        return piece < 2 ? load16(wr, lane_pair + h * 512, g * 1024) : load16(w2r, lane_pair + pair1 + h * 512, g * 1024);
     };
     mx_i4 X[2][XL];                                  // rows on the way to LDS
-    auto load_x = [&](int step, mx_i4 (&x)[XL]) __attribute__((always_inline)) {
-        const int g = min(step, G - 1);
-#pragma unroll
-        for (int i = 0; i < XL; ++i) x[i] = load16(xr, (i * 4 + wave) * G * 1024 + lane * 16, g * 1024);
+    auto load_x = [&](int step, int i) __attribute__((always_inline)) {
+        return load16(xr, (i * 4 + wave) * G * 1024 + lane * 16, min(step, G - 1) * 1024);
     };
-    auto store_x = [&](int stage, const mx_i4 (&x)[XL]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < XL; ++i)
-            if ((i * 4 + 3 < 2 * SUB) || i * 4 + wave < 2 * SUB)
-                *reinterpret_cast<mx_i4*>(lds + (stage * kBlockTiles + i * 4 + wave) * 1024 + lane * 16) = x[i];
+    auto store_x = [&](int stage, int i, mx_i4 x) __attribute__((always_inline)) {
+        *reinterpret_cast<mx_i4*>(lds + (stage * kBlockTiles + i * 4 + wave) * 1024 + lane * 16) = x;
     };
     int sw[2][2], sx[SUB][2], swn[2][2], sxn[SUB][2];
     auto load_s = [&](int quad, int (&w)[2][2], int (&x)[SUB][2]) __attribute__((always_inline)) {
@@ -287,35 +321,76 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
         }
     };
     mx_f16 acc[SUB][2] = {};
+    if (!GATED && a.bias) {                          // the sums start from the bias
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int c = col16 * 16 + 32 * j + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+                const float b = c < a.N ? a.bias[c] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < SUB; ++i) acc[i][j][r] = b;
+            }
+    }
     const uint8_t* xl = lds + (lane >> 4 & 1) * 1024 + (lane >> 5) * 256 + (lane & 15) * 16;
-    // step g (S = g % 4): products of group g; the weights of g + 3 and rows of g + 3
-    // leave memory, rows of g + 1 enter LDS
+    auto read = [&](int stage, int i, mx_i4 (&f)[2]) __attribute__((always_inline)) {
+        f[0] = *reinterpret_cast<const mx_i4*>(xl + (stage * kBlockTiles + 2 * i) * 1024);
+        f[1] = *reinterpret_cast<const mx_i4*>(xl + (stage * kBlockTiles + 2 * i) * 1024 + 512);
+    };
+    // Step g (S = g % 4): the products of group g. Rows of g + 2 enter LDS (the barrier
+    // before step g + 1 shows them to it, which reads its successor's first pieces),
+    // rows of g + 4 and weights of g + 3 leave memory. Pieces are read two products
+    // ahead, across the step's end. The scheduling barriers keep each piece's products
+    // with its reads: left alone, the compiler moves all reads of four steps, and their
+    // waits, before the first product.
+    constexpr int kAhead = SUB < 2 ? SUB : 2;
+    mx_i4 F[kAhead][2];
     auto step = [&](auto phase, int g) __attribute__((always_inline)) {
         constexpr int S = decltype(phase)::value;
-        load_w(g + 3, W[(S + 3) & 3]);
-        const int stage = S & 1;
+        mx_i4 f[SUB + kAhead][2];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) { f[i][0] = F[i][0]; f[i][1] = F[i][1]; }
 #pragma unroll
         for (int i = 0; i < SUB; ++i) {
-            const mx_i4 b0 = *reinterpret_cast<const mx_i4*>(xl + (stage * kBlockTiles + 2 * i) * 1024);
-            const mx_i4 b1 = *reinterpret_cast<const mx_i4*>(xl + (stage * kBlockTiles + 2 * i) * 1024 + 512);
+            // the step's loads are spread over its pieces: issued together by four waves
+            // that just left a barrier, they hold up the products behind them
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<S>(W[S][j][0], b0, acc[i][j], sw[j][0], sx[i][0]);
+            for (int p = 0; p < 4; ++p)
+                if (p * SUB / 4 == i) W[(S + 3) & 3][p >> 1][p & 1] = load_w(g + 3, p);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<S>(W[S][j][1], b1, acc[i][j], sw[j][1], sx[i][1]);
+            for (int p = 0; p < XL; ++p)
+                if (SUB - 1 - p * SUB / (2 * XL) == i) {
+                    store_x((S + 2) & 3, p, X[S & 1][p]);
+                    X[S & 1][p] = load_x(g + 4, p);
+                }
+            if (i + kAhead < SUB) read(S, i + kAhead, f[i + kAhead]);
+            else read((S + 1) & 3, i + kAhead - SUB, f[i + kAhead]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<S>(W[S][j][h], f[i][h], acc[i][j], sw[j][h], sx[i][h]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        store_x(stage ^ 1, X[stage ^ 1]);
-        load_x(g + 3, X[stage ^ 1]);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) { F[i][0] = f[SUB + i][0]; F[i][1] = f[SUB + i][1]; }
         __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
     };
-    load_x(0, X[0]);
-    load_w(0, W[0]);
+#pragma unroll
+    for (int p = 0; p < 2 * XL; ++p) X[p / XL][p % XL] = load_x(p / XL, p % XL);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) W[0][p >> 1][p & 1] = load_w(0, p);
     load_s(0, sw, sx);
-    load_x(1, X[1]);
-    load_w(1, W[1]);
-    load_w(2, W[2]);
-    store_x(0, X[0]);
-    load_x(2, X[0]);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) W[1 + p / 4][p >> 1 & 1][p & 1] = load_w(1 + p / 4, p & 3);
+#pragma unroll
+    for (int p = 0; p < 2 * XL; ++p) {
+        store_x(p / XL, p % XL, X[p / XL][p % XL]);
+        X[p / XL][p % XL] = load_x(2 + p / XL, p % XL);
+    }
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) read(0, i, F[i]);
     int g = 0;
     for (; g + 4 <= G; g += 4) {
         load_s((g >> 2) + 1, swn, sxn);
@@ -337,53 +412,64 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
         if (g + 2 < G) step(Phase<2>{}, g + 2);
     }
 
-    // lane: row m = l % 32 of a piece; register r: column 8 (r / 4) + 4 (l / 32) + r % 4
-    const int lm = lane & 31;
+    // The results leave through LDS, piece by piece: a lane holds one row's columns
+    // 8 (r / 4) + 4 (l / 32) + r % 4, four neighbours; read back, eight lanes (fp32:
+    // sixteen) hold 128 (256) bytes of a row, and a store covers whole lines.
+    constexpr int kWaveCols = GATED ? 32 : 64;
+    constexpr int kPitch = kWaveCols * sizeof(T) + 16;           // rows 16 B apart in the banks
+    constexpr int kPer = 16 / sizeof(T);                         // columns of a lane's 16 bytes
+    constexpr int kLanes = kWaveCols / kPer;                     // lanes of a row
+    constexpr int kRound = 64 / kLanes;                          // rows of a store
+    static_assert(32 * kPitch <= kBlockTiles * 1024);
+    uint8_t* tile = lds + wave * kBlockTiles * 1024;             // every wave is past the last barrier
+    const int n = col16 * 16 + (lane & (kLanes - 1)) * kPer;
+    const int rows = min(n16 * 16, a.M - rt0 * 16);
+    T* y = static_cast<T*>(a.y) + static_cast<int64_t>(rt0) * 16 * a.N;
+    // 16-byte stores, those beyond the block's rows or N dropped by their offset
+    const bool vec = a.N % kPer == 0 && a.N <= (1 << 21);
+    const __amdgpu_buffer_rsrc_t yr = buffer(y, static_cast<int64_t>(rows) * a.N * sizeof(T));
+    uint32_t at = n < a.N ? ((lane / kLanes) * a.N + n) * sizeof(T) : 0x80000000u;
 #pragma unroll
     for (int i = 0; i < SUB; ++i) {
-        const int64_t m = rt0 * 16 + 32 * i + lm;
-        const bool row_there = 32 * i + lm < n16 * 16 && m < a.M;
-        bool live = row_there;
-        if (GATED && row_there) live = static_cast<unsigned>(a.row_token[m]) < static_cast<unsigned>(a.T);
+        bool live = true;
+        if (GATED) {
+            const int m = 32 * i + (lane & 31);
+            live = m < rows && static_cast<unsigned>(a.row_token[rt0 * 16 + m]) < static_cast<unsigned>(a.T);
+        }
+        __builtin_amdgcn_wave_barrier();                         // a wave's LDS accesses complete in order
 #pragma unroll
         for (int j = 0; j < (GATED ? 1 : 2); ++j) {
-            const int n0 = col16 * 16 + 32 * j;
-            float v[16];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                v[r] = GATED ? mx_silu(acc[i][0][r]) * acc[i][1][r] : acc[i][j][r];
-                if (GATED && !live) v[r] = 0.0f;
+            for (int c = 0; c < 4; ++c) {
+                float v[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int q = 4 * c + r;
+                    v[r] = GATED ? (live ? mx_silu(acc[i][0][q]) * acc[i][1][q] : 0.0f) : acc[i][j][q];
+                }
+                uint8_t* to = tile + (lane & 31) * kPitch + (32 * j + 8 * c + 4 * (lane >> 5)) * sizeof(T);
+                if constexpr (sizeof(T) == 4)
+                    *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+                else
+                    *reinterpret_cast<uint2*>(to) = make_uint2(mx_pack2<T>(v[0], v[1]), mx_pack2<T>(v[2], v[3]));
             }
-            if (a.bias) {
+        }
+        __builtin_amdgcn_wave_barrier();
+        if (vec) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int n = n0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-                    v[r] += n < a.N ? a.bias[n] : 0.0f;
-                }
+            for (int s = 0; s < 32 / kRound; ++s) {
+                const mx_u4 v = *reinterpret_cast<const mx_u4*>(tile + (s * kRound + lane / kLanes) * kPitch + (lane & (kLanes - 1)) * 16);
+                __builtin_amdgcn_raw_buffer_store_b128(v, yr, at, 0, 0);
+                at += kRound * a.N * sizeof(T);
             }
-            if (a.y_dtype != MQ_F32 && a.N % 8 == 0) {
-                // halves of the wave trade pieces: eight neighbouring columns a lane
-#pragma unroll
-                for (int c = 0; c < 4; c += 2) {
-                    uint32_t p[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        p[k] = a.y_dtype == MQ_BF16 ? mx_pack2<__bf16>(v[4 * c + 2 * k], v[4 * c + 2 * k + 1])
-                                                    : mx_pack2<_Float16>(v[4 * c + 2 * k], v[4 * c + 2 * k + 1]);
-                    const auto s0 = __builtin_amdgcn_permlane32_swap(p[0], p[2], false, false);
-                    const auto s1 = __builtin_amdgcn_permlane32_swap(p[1], p[3], false, false);
-                    const int n = n0 + 8 * c + 8 * (lane >> 5);
-                    if (row_there && n < a.N)
-                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + m * a.N + n) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int n = n0 + 8 * c + 4 * (lane >> 5);
-                    if (row_there && n < a.N)
-                        mx_store4(a.y, a.y_dtype, m * a.N + n, a.N - n, a.N % 4 == 0, v[4 * c], v[4 * c + 1], v[4 * c + 2],
-                                  v[4 * c + 3]);
-                }
+        } else {
+            const T* from = reinterpret_cast<const T*>(tile);
+            const int cols = min(kWaveCols, a.N - col16 * 16);
+#pragma clang loop unroll(disable)
+            for (int o = lane; o < 32 * kWaveCols; o += 64) {
+                const int r = o / kWaveCols, c = o % kWaveCols;
+                if (32 * i + r < rows && c < cols)
+                    y[static_cast<int64_t>(32 * i + r) * a.N + col16 * 16 + c] = from[r * (kPitch / sizeof(T)) + c];
             }
         }
     }
@@ -402,9 +488,9 @@ __device__ inline void zero_rows(const MxGemmArgs& a, int rt0, int n16, int n0, 
 // Four waves, each 64 columns (GATED: 32), of one row block. Workgroups go to the eight
 // dies in turn, so each die takes a run of neighbouring tiles: they share rows and
 // weights in its L2.
-template <bool GATED>
+template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void k_mx_wide(MxGemmArgs a, int blocks, int block_tiles) {
-    __shared__ __align__(16) uint8_t lds[2 * kBlockTiles * 1024];
+    __shared__ __align__(16) uint8_t lds[4 * kBlockTiles * 1024];
     constexpr int kCols = GATED ? 128 : 256;
     const int ncol = (a.N + kCols - 1) / kCols;
     const int count = a.tiles ? a.tiles[0] : blocks;
@@ -429,12 +515,12 @@ __global__ __launch_bounds__(256) void k_mx_wide(MxGemmArgs a, int blocks, int b
     }
     const int col16 = col * (kCols / 16) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (kCols / 64);
     switch ((n16 + 1) / 2) {
-        case 1: wide_tile<1, GATED>(a, lds, rt0, n16, e, col16); break;
-        case 2: wide_tile<2, GATED>(a, lds, rt0, n16, e, col16); break;
-        case 3: wide_tile<3, GATED>(a, lds, rt0, n16, e, col16); break;
-        case 4: wide_tile<4, GATED>(a, lds, rt0, n16, e, col16); break;
-        case 5: wide_tile<5, GATED>(a, lds, rt0, n16, e, col16); break;
-        default: wide_tile<6, GATED>(a, lds, rt0, n16, e, col16); break;
+        case 1: wide_tile<T, 1, GATED>(a, lds, rt0, n16, e, col16); break;
+        case 2: wide_tile<T, 2, GATED>(a, lds, rt0, n16, e, col16); break;
+        case 3: wide_tile<T, 3, GATED>(a, lds, rt0, n16, e, col16); break;
+        case 4: wide_tile<T, 4, GATED>(a, lds, rt0, n16, e, col16); break;
+        case 5: wide_tile<T, 5, GATED>(a, lds, rt0, n16, e, col16); break;
+        default: wide_tile<T, 6, GATED>(a, lds, rt0, n16, e, col16); break;
     }
 }
 
@@ -511,20 +597,8 @@ hipError_t combine(const float* rows, int64_t n_rows, const int32_t* row_of, con
 
 int64_t tiles_cap(int64_t P, int64_t E) { return P / 16 / kBlockTiles + E + 2; }
 
-}  // namespace
-
-bool mx_few_rows(int64_t M, int64_t N, int64_t K) { return M <= 32; }
-
-hipError_t launch_mx_few(const MxGemmArgs& a, hipStream_t st) {
-    if (!a.x) return few<MxReady>(a, st);
-    switch (a.x_dtype) {
-        case MQ_F32: return few<float>(a, st);
-        case MQ_BF16: return few<__bf16>(a, st);
-        default: return few<_Float16>(a, st);
-    }
-}
-
-hipError_t launch_mx_wide(const MxGemmArgs& a, hipStream_t st) {
+template <typename T>
+hipError_t wide(const MxGemmArgs& a, hipStream_t st) {
     const int rt = (a.M + 15) / 16;
     const bool gated = a.w2q != nullptr;
     const int64_t ncol = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
@@ -537,10 +611,32 @@ hipError_t launch_mx_wide(const MxGemmArgs& a, hipStream_t st) {
     const int64_t n = a.tiles ? tiles_cap(a.M, a.E) : blocks;
     const unsigned grid = static_cast<unsigned>((n * ncol + 7) / 8 * 8);
     if (gated)
-        k_mx_wide<true><<<grid, 256, 0, st>>>(a, blocks, block_tiles);
+        k_mx_wide<T, true><<<grid, 256, 0, st>>>(a, blocks, block_tiles);
     else
-        k_mx_wide<false><<<grid, 256, 0, st>>>(a, blocks, block_tiles);
+        k_mx_wide<T, false><<<grid, 256, 0, st>>>(a, blocks, block_tiles);
     return hipGetLastError();
+}
+
+}  // namespace
+
+bool mx_few_rows(int64_t M, int64_t N, int64_t K) { return M <= 32; }
+
+hipError_t launch_mx_few(const MxGemmArgs& a, hipStream_t st) {
+    const int64_t rows = a.offsets ? a.T : a.M;
+    if (!a.x) return few_rows<MxReady>(a, rows, st);
+    switch (a.x_dtype) {
+        case MQ_F32: return few_rows<float>(a, rows, st);
+        case MQ_BF16: return few_rows<__bf16>(a, rows, st);
+        default: return few_rows<_Float16>(a, rows, st);
+    }
+}
+
+hipError_t launch_mx_wide(const MxGemmArgs& a, hipStream_t st) {
+    switch (a.y_dtype) {
+        case MQ_F32: return wide<float>(a, st);
+        case MQ_BF16: return wide<__bf16>(a, st);
+        default: return wide<_Float16>(a, st);
+    }
 }
 
 int64_t mx_tiles_size(int64_t P, int64_t E) { return 4 + 4 * tiles_cap(P, E); }

@@ -11,12 +11,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// max over the four lanes of a block
-__device__ inline uint32_t quad_max(uint32_t m) {
-    m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xB1, 0xf, 0xf, true)));
-    return max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x4E, 0xf, 0xf, true)));
-}
-
 // One workgroup: 16 rows x 512 inputs (four code tiles, one scale entry per lane).
 // Wave w reads rows 4w .. 4w + 3, 1 KB of bf16 at a time; lane l holds inputs
 // 8l .. 8l + 7, four lanes a block. Codes and scales go through LDS, because a tile
@@ -43,8 +37,8 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t strid
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 4 * wave + i;
-            const int byte = mx_scale_byte(quad_max(v[i].peak()));
-            lds_codes[((lane >> 2) * 16 + row) * 4 + (lane & 3)] = byte == 255 ? 0 : v[i].codes(mx_scale_value(byte));
+            int byte;
+            lds_codes[((lane >> 2) * 16 + row) * 4 + (lane & 3)] = mx_quant8(v[i], byte);
             // blocks beyond K hold zeros, so their byte is 0
             if ((lane & 3) == 0) lds_scales[(((lane >> 2) & 3) * 16 + row) * 4 + (lane >> 4)] = byte;
         }
@@ -73,8 +67,8 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant_scatter(const T* x, int64
     const int q = blockIdx.y;
     const int k0 = q * 512 + 8 * lane;
     const MxRaw8<T> v = mx_load8(x + r * stride_r + k0, K - k0);
-    const int byte = mx_scale_byte(quad_max(v.peak()));
-    const uint32_t word = byte == 255 ? 0 : v.codes(mx_scale_value(byte));
+    int byte;
+    const uint32_t word = mx_quant8(v, byte);
     const int g = q * 4 + (lane >> 4), kc = (lane >> 2) & 3;
     for (int j = 0; j < copies; ++j) {
         const int p = row_of[r * copies + j];
