@@ -76,8 +76,14 @@ mq::MxQuantArgs rows_of(const void* x, int dtype, int64_t R, int64_t stride, int
     return a;
 }
 
+size_t row_bytes(int64_t R, int64_t K) {
+    return round16(mq::mx_row_codes_size(R, K)) + round16(mq::mx_row_scales_size(R, K));
+}
+
 // Whether the experts of a batch meet few rows each: at most two row tiles.
 bool few_tokens(int64_t T) { return T <= 32; }
+// Whether the down products go token by token.
+bool one_by_one(int64_t T, int64_t k) { return T <= 8 && k <= 32; }
 size_t tiles_bytes(int64_t P, int64_t E) { return round16(mq::mx_tiles_size(P, E) * 4); }
 
 }  // namespace
@@ -219,7 +225,7 @@ int mq_expert_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t*
 size_t mq_mx_experts_up_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I) {
     if (check_slots(T, k, E) || check_product(T * k, I, D) || few_tokens(T)) return 0;
     const int64_t P = mq::plan_rows(T, k, E);
-    return mx_bytes(P, D) + tiles_bytes(P, E);
+    return row_bytes(T, D) + tiles_bytes(P, E);
 }
 
 int mq_mx_experts_up(const void* x, int x_dtype, int64_t stride_t, int64_t T, int64_t k, int64_t E, int64_t D, int64_t I,
@@ -252,14 +258,12 @@ int mq_mx_experts_up(const void* x, int x_dtype, int64_t stride_t, int64_t T, in
     if (workspace_bytes < mq_mx_experts_up_workspace_bytes(T, k, E, D, I) || !workspace || off(workspace, 16))
         return MQ_ERR_INVALID_ARG;
     uint8_t* xq = static_cast<uint8_t*>(workspace);
-    uint8_t* xs = xq + round16(mq::mx_codes_size(P, D));
+    uint8_t* xs = xq + round16(mq::mx_row_codes_size(T, D));
     a.xq = xq;
     a.xs = xs;
-    a.tiles = reinterpret_cast<int32_t*>(xs + round16(mq::mx_scales_size(P, D)));
+    a.tiles = reinterpret_cast<int32_t*>(xs + round16(mq::mx_row_scales_size(T, D)));
     mq::MxQuantArgs q = rows_of(x, x_dtype, T, stride_t, D, xq, xs);
-    q.row_of = row_of;
-    q.copies = static_cast<int>(k);
-    q.out_rows = P;
+    q.by_row = true;
     if (mq::launch_mx_quant(q, st) != hipSuccess) return MQ_ERR_HIP;
     if (mq::launch_mx_tiles(offsets, a.E, P, a.tiles, st) != hipSuccess) return MQ_ERR_HIP;
     return status_of(mq::launch_mx_wide(a, st));
@@ -269,6 +273,7 @@ size_t mq_mx_experts_down_workspace_bytes(int64_t T, int64_t k, int64_t E, int64
     if (check_slots(T, k, E) || check_product(T * k, D, I)) return 0;
     const int64_t P = mq::plan_rows(T, k, E);
     const size_t rows = round16(P * D * 4);
+    if (one_by_one(T, k)) return 0;
     return few_tokens(T) ? rows : rows + mx_bytes(P, I) + tiles_bytes(P, E);
 }
 
@@ -282,10 +287,20 @@ int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t
     if (!h || off(h, type_size(h_dtype)) || !y || off(y, 16)) return MQ_ERR_INVALID_ARG;
     if (!offsets || off(offsets, 4) || !row_of || off(row_of, 4) || !weights || off(weights, 4)) return MQ_ERR_INVALID_ARG;
     if ((rc = check_codes(wq, ws))) return rc;
-    if (workspace_bytes < mq_mx_experts_down_workspace_bytes(T, k, E, D, I) || !workspace || off(workspace, 16))
-        return MQ_ERR_INVALID_ARG;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const int64_t P = mq::plan_rows(T, k, E);
+    if (one_by_one(T, k)) {
+        mq::MxGemmArgs a = product(nullptr, nullptr, wq, ws, P, D, I, y, y_dtype);
+        a.offsets = offsets;
+        a.E = static_cast<int>(E);
+        a.T = static_cast<int>(T);
+        a.x = h;
+        a.x_dtype = h_dtype;
+        a.stride_x = I;
+        return status_of(mq::launch_mx_down_few(a, row_of, weights, static_cast<int>(k), P, st));
+    }
+    if (workspace_bytes < mq_mx_experts_down_workspace_bytes(T, k, E, D, I) || !workspace || off(workspace, 16))
+        return MQ_ERR_INVALID_ARG;
     float* rows = static_cast<float*>(workspace);
     mq::MxGemmArgs a = product(nullptr, nullptr, wq, ws, P, D, I, rows, MQ_F32);
     a.offsets = offsets;

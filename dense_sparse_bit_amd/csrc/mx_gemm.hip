@@ -248,6 +248,68 @@ hipError_t few_rows(const MxGemmArgs& a, int64_t rows, hipStream_t st) {
     return few<XT, 2, 2, 16, false>(a, st);
 }
 
+// The experts' down products of few tokens, each token by itself: workgroup (16 NT
+// columns, token), a wave for each slot (of up to kDownWaves; fewer slots: several waves
+// split a slot's K). The slots' sums meet in LDS and are added in their order, so the
+// rows need no memory of their own and no second launch. Experts that tokens share are
+// read once a token: for few tokens there are few of those.
+constexpr int kDownWaves = 16;
+
+template <typename XT, int NT>
+__global__ __launch_bounds__(64 * kDownWaves) void k_mx_down_few(MxGemmArgs a, const int32_t* row_of, const float* weights, int k,
+                                                                 int parts, int64_t P) {
+    extern __shared__ __align__(16) uint8_t lds[];        // each wave's rows; the sums [k * parts][16 NT]
+    mx_f4* sums = reinterpret_cast<mx_f4*>(lds + kDownWaves * kRowsLds);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int G = (a.K + 127) / 128, G4 = (G + 3) / 4;
+    const int n_tiles = (a.N + 15) / 16, ct = blockIdx.x * NT;
+    const int64_t t = blockIdx.y;
+    for (int u = wave; u < k * parts; u += kDownWaves) {
+        const int part = u % parts;
+        const int p = __builtin_amdgcn_readfirstlane(row_of[t * k + u / parts]);
+        const int e = p >= 0 && p < P ? __builtin_amdgcn_readfirstlane(expert_of(a.offsets, a.E, p)) : -1;
+        mx_f4 acc[NT][1] = {};
+        if (e >= 0) {
+            const uint8_t *w[NT], *ws[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int64_t tile = static_cast<int64_t>(e) * n_tiles + min(ct + j, n_tiles - 1);
+                w[j] = a.wq + tile * G * 1024 + lane * 16;
+                ws[j] = a.ws + tile * G4 * 256 + lane * 4;
+            }
+            few_run<XT, NT, 1, 1>(a, w, ws, 1, [&](int) __attribute__((always_inline)) -> int64_t { return p; },
+                                  G * part / parts, G * (part + 1) / parts, lds + wave * kRowsLds, acc);
+        }
+        if ((lane & 15) == 0) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) sums[(u * NT + j) * 4 + (lane >> 4)] = acc[j][0];
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 4 * NT) {
+        const int n = ct * 16 + 4 * threadIdx.x;
+        mx_f4 y = {};
+        for (int j = 0; j < k; ++j) {
+            mx_f4 v = sums[j * parts * NT * 4 + threadIdx.x];
+            for (int i = 1; i < parts; ++i) v += sums[(j * parts + i) * NT * 4 + threadIdx.x];
+            y += weights[t * k + j] * v;
+        }
+        if (n < a.N) mx_store4(a.y, a.y_dtype, t * a.N + n, a.N - n, a.N % 4 == 0, y[0], y[1], y[2], y[3]);
+    }
+}
+
+template <typename XT>
+hipError_t down_few(const MxGemmArgs& a, const int32_t* row_of, const float* weights, int k, int64_t P, hipStream_t st) {
+    const int G = (a.K + 127) / 128;
+    int parts = kDownWaves / k > 1 ? kDownWaves / k : 1;
+    if (parts > G) parts = G;
+    const size_t lds = kDownWaves * kRowsLds + static_cast<size_t>(k) * parts * 64;
+    k_mx_down_few<XT, 1><<<dim3(static_cast<unsigned>((a.N + 15) / 16), static_cast<unsigned>(a.T)), 64 * kDownWaves, lds, st>>>(
+        a, row_of, weights, k, parts, P);
+    return hipGetLastError();
+}
+
 // ------------------------------------------------------------------- many rows
 template <int S> struct Phase { static constexpr int value = S; };
 constexpr int kMaxSub = 6;                    // 32-row pieces of a row block
@@ -276,6 +338,9 @@ __device__ inline int load4(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
 template <typename T, int SUB, bool GATED>
 __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int rt0, int n16, int e, int col16) {
     constexpr int XL = (SUB + 1) / 2;                // 16-row tiles that a wave fetches a step
+    // LDS: a tile's four runs of 16 blocks; gathered rows are written across the runs, and
+    // 64 bytes between these keep eight lanes on different banks
+    constexpr int kBlock = GATED ? 320 : 256, kTile = 4 * kBlock, kStage = kBlockTiles * kTile + (GATED ? 16 : 0);
     static_assert(4 * XL <= kBlockTiles);            // (odd SUB: two tiles of zeros too, and no branch)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -292,8 +357,23 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
     const __amdgpu_buffer_rsrc_t w2r = GATED ? buffer(a.w2q + first * G * 1024, static_cast<int64_t>(have) * G * 1024) : wr;
     const __amdgpu_buffer_rsrc_t w2sr = GATED ? buffer(a.w2s + first * G4 * 256, static_cast<int64_t>(have) * G4 * 256) : wsr;
     const int pair1 = GATED ? 0 : 2 * G * 1024, spair1 = GATED ? 0 : 2 * G4 * 256;
-    const __amdgpu_buffer_rsrc_t xr = buffer(a.xq + static_cast<int64_t>(rt0) * G * 1024, static_cast<int64_t>(n16) * G * 1024);
-    const __amdgpu_buffer_rsrc_t xsr = buffer(a.xs + static_cast<int64_t>(rt0) * G4 * 256, static_cast<int64_t>(n16) * G4 * 256);
+    // rows: tiles in the weights' layout, or (GATED) rows of their own, picked by token:
+    const int G2 = (G + 1) / 2;
+    const __amdgpu_buffer_rsrc_t xr = buffer(a.xq + static_cast<int64_t>(GATED ? 0 : rt0) * G * 1024, static_cast<int64_t>(n16) * G * 1024);
+    const __amdgpu_buffer_rsrc_t xsr = buffer(a.xs + static_cast<int64_t>(GATED ? 0 : rt0) * G4 * 256, static_cast<int64_t>(n16) * G4 * 256);
+    const uint8_t* xrow[2][GATED ? XL : 1];
+    const uint8_t* xsrow[GATED ? SUB : 1];
+    if constexpr (GATED) {
+        auto token = [&](int r) __attribute__((always_inline)) -> int64_t {       // of no row: token 0's, never written
+            const int t = r < n16 * 16 ? a.row_token[rt0 * 16 + r] : 0;
+            return static_cast<unsigned>(t) < static_cast<unsigned>(a.T) ? t : 0;
+        };
+#pragma unroll
+        for (int p = 0; p < 2 * XL; ++p)
+            xrow[p / XL][p % XL] = a.xq + token((p % XL * 4 + wave) * 16 + 8 * (p / XL) + (lane >> 3)) * G2 * 128 + (lane & 7) * 16;
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) xsrow[i] = a.xs + token(32 * i + (lane & 31)) * G4 * 16 + (lane >> 5) * 4;
+    }
 
     mx_i4 W[4][2][2];                                // [step % 4][column pair][half]
     // The scalar part of an offset stays within the buffer (the range check subtracts
@@ -302,12 +382,19 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
         const int g = min(step, G - 1), h = piece & 1;
         return piece < 2 ? load16(wr, lane_pair + h * 512, g * 1024) : load16(w2r, lane_pair + pair1 + h * 512, g * 1024);
     };
-    mx_i4 X[2][XL];                                  // rows on the way to LDS
-    auto load_x = [&](int step, int i) __attribute__((always_inline)) {
-        return load16(xr, (i * 4 + wave) * G * 1024 + lane * 16, min(step, G - 1) * 1024);
+    // Rows on the way to LDS, two steps' worth: X[s][p] is piece p of step g + s of a pair
+    // of steps; of gathered rows, rows 8 s to 8 s + 7 of a tile for both steps (eight lanes
+    // read 128 bytes of a row: a whole line, where one step's 64 were half of one).
+    mx_i4 X[2][XL];
+    auto load_x = [&](int step, int s, int i) __attribute__((always_inline)) {     // step: the pair's first
+        if constexpr (GATED) return *reinterpret_cast<const mx_i4*>(xrow[s][i] + min(step, (G - 1) & ~1) * 64);
+        else return load16(xr, (i * 4 + wave) * G * 1024 + lane * 16, min(step + s, G - 1) * 1024);
     };
-    auto store_x = [&](int stage, int i, mx_i4 x) __attribute__((always_inline)) {
-        *reinterpret_cast<mx_i4*>(lds + (stage * kBlockTiles + i * 4 + wave) * 1024 + lane * 16) = x;
+    auto store_x = [&](int stage, int s, int i, mx_i4 x) __attribute__((always_inline)) {   // stage: the pair's first
+        uint8_t* to = lds + (i * 4 + wave) * kTile;
+        if constexpr (GATED) to += (stage + (lane >> 2 & 1)) * kStage + (lane & 3) * kBlock + (8 * s + (lane >> 3)) * 16;
+        else to += (stage + s) * kStage + lane * 16;
+        *reinterpret_cast<mx_i4*>(to) = x;
     };
     int sw[2][2], sx[SUB][2], swn[2][2], sxn[SUB][2];
     auto load_s = [&](int quad, int (&w)[2][2], int (&x)[SUB][2]) __attribute__((always_inline)) {
@@ -317,7 +404,10 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
             w[0][h] = load4(wsr, scale_pair + h * 128, q * 256);
             w[1][h] = load4(w2sr, scale_pair + spair1 + h * 128, q * 256);
 #pragma unroll
-            for (int i = 0; i < SUB; ++i) x[i][h] = load4(xsr, scale_pair + h * 128, (2 * i * G4 + q) * 256);
+            for (int i = 0; i < SUB; ++i) {
+                if constexpr (GATED) x[i][h] = *reinterpret_cast<const int*>(xsrow[i] + q * 16 + h * 8);
+                else x[i][h] = load4(xsr, scale_pair + h * 128, (2 * i * G4 + q) * 256);
+            }
         }
     };
     mx_f16 acc[SUB][2] = {};
@@ -332,14 +422,14 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
                 for (int i = 0; i < SUB; ++i) acc[i][j][r] = b;
             }
     }
-    const uint8_t* xl = lds + (lane >> 4 & 1) * 1024 + (lane >> 5) * 256 + (lane & 15) * 16;
+    const uint8_t* xl = lds + (lane >> 4 & 1) * kTile + (lane >> 5) * kBlock + (lane & 15) * 16;
     auto read = [&](int stage, int i, mx_i4 (&f)[2]) __attribute__((always_inline)) {
-        f[0] = *reinterpret_cast<const mx_i4*>(xl + (stage * kBlockTiles + 2 * i) * 1024);
-        f[1] = *reinterpret_cast<const mx_i4*>(xl + (stage * kBlockTiles + 2 * i) * 1024 + 512);
+        f[0] = *reinterpret_cast<const mx_i4*>(xl + stage * kStage + 2 * i * kTile);
+        f[1] = *reinterpret_cast<const mx_i4*>(xl + stage * kStage + 2 * i * kTile + 2 * kBlock);
     };
-    // Step g (S = g % 4): the products of group g. Rows of g + 2 enter LDS (the barrier
-    // before step g + 1 shows them to it, which reads its successor's first pieces),
-    // rows of g + 4 and weights of g + 3 leave memory. Pieces are read two products
+    // Step g (S = g % 4): the products of group g. Even steps: rows of g + 2 and g + 3 enter
+    // LDS (the barrier before step g + 1 shows them to it, which reads its successor's
+    // first pieces), those of g + 4 and g + 5 leave memory; weights of g + 3 do in each. Pieces are read two products
     // ahead, across the step's end. The scheduling barriers keep each piece's products
     // with its reads: left alone, the compiler moves all reads of four steps, and their
     // waits, before the first product.
@@ -357,12 +447,14 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
 #pragma unroll
             for (int p = 0; p < 4; ++p)
                 if (p * SUB / 4 == i) W[(S + 3) & 3][p >> 1][p & 1] = load_w(g + 3, p);
+            if (!(S & 1)) {
 #pragma unroll
-            for (int p = 0; p < XL; ++p)
-                if (SUB - 1 - p * SUB / (2 * XL) == i) {
-                    store_x((S + 2) & 3, p, X[S & 1][p]);
-                    X[S & 1][p] = load_x(g + 4, p);
-                }
+                for (int p = 0; p < 2 * XL; ++p)
+                    if (SUB - 1 - p * SUB / (2 * XL) == i) {
+                        store_x((S + 2) & 3, p / XL, p % XL, X[p / XL][p % XL]);
+                        X[p / XL][p % XL] = load_x(g + 4, p / XL, p % XL);
+                    }
+            }
             if (i + kAhead < SUB) read(S, i + kAhead, f[i + kAhead]);
             else read((S + 1) & 3, i + kAhead - SUB, f[i + kAhead]);
 #pragma unroll
@@ -377,7 +469,7 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
         __builtin_amdgcn_sched_barrier(0);
     };
 #pragma unroll
-    for (int p = 0; p < 2 * XL; ++p) X[p / XL][p % XL] = load_x(p / XL, p % XL);
+    for (int p = 0; p < 2 * XL; ++p) X[p / XL][p % XL] = load_x(0, p / XL, p % XL);
 #pragma unroll
     for (int p = 0; p < 4; ++p) W[0][p >> 1][p & 1] = load_w(0, p);
     load_s(0, sw, sx);
@@ -385,8 +477,8 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
     for (int p = 0; p < 8; ++p) W[1 + p / 4][p >> 1 & 1][p & 1] = load_w(1 + p / 4, p & 3);
 #pragma unroll
     for (int p = 0; p < 2 * XL; ++p) {
-        store_x(p / XL, p % XL, X[p / XL][p % XL]);
-        X[p / XL][p % XL] = load_x(2 + p / XL, p % XL);
+        store_x(0, p / XL, p % XL, X[p / XL][p % XL]);
+        X[p / XL][p % XL] = load_x(2, p / XL, p % XL);
     }
     __syncthreads();
 #pragma unroll
@@ -490,7 +582,7 @@ __device__ inline void zero_rows(const MxGemmArgs& a, int rt0, int n16, int n0, 
 // weights in its L2.
 template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void k_mx_wide(MxGemmArgs a, int blocks, int block_tiles) {
-    __shared__ __align__(16) uint8_t lds[4 * kBlockTiles * 1024];
+    __shared__ __align__(16) uint8_t lds[4 * kBlockTiles * (GATED ? 1280 : 1024) + (GATED ? 64 : 0)];
     constexpr int kCols = GATED ? 128 : 256;
     const int ncol = (a.N + kCols - 1) / kCols;
     const int count = a.tiles ? a.tiles[0] : blocks;
@@ -628,6 +720,15 @@ hipError_t launch_mx_few(const MxGemmArgs& a, hipStream_t st) {
         case MQ_F32: return few_rows<float>(a, rows, st);
         case MQ_BF16: return few_rows<__bf16>(a, rows, st);
         default: return few_rows<_Float16>(a, rows, st);
+    }
+}
+
+hipError_t launch_mx_down_few(const MxGemmArgs& a, const int32_t* row_of, const float* weights, int k, int64_t P,
+                              hipStream_t st) {
+    switch (a.x_dtype) {
+        case MQ_F32: return down_few<float>(a, row_of, weights, k, P, st);
+        case MQ_BF16: return down_few<__bf16>(a, row_of, weights, k, P, st);
+        default: return down_few<_Float16>(a, row_of, weights, k, P, st);
     }
 }
 

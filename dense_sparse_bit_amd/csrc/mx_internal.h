@@ -23,17 +23,20 @@ inline int64_t plan_rows(int64_t T, int64_t k, int64_t E) {
     return (n + 15 * (n < E ? n : E)) / 16 * 16;
 }
 
-// x[b][r][c] of a strided matrix, as it is read by the quantizer. Row r of the output
-// is row r of x, or with `row_of` (int32 [R][copies]) row r goes to the output rows
-// row_of[r][*] that are in [0, out_rows).
+// Row by row, for rows that are picked one by one (experts' tokens): a row's codes are
+// whole runs of 128 bytes (256 inputs) in the order of the inputs; its scales 16 bytes per 512 inputs, the byte
+// of block b at (b / 16) * 16 + (b % 4) * 4 + b / 4 % 4.
+inline int64_t mx_row_codes_size(int64_t R, int64_t K) { return R * ((mx_groups(K) + 1) / 2) * 128; }
+inline int64_t mx_row_scales_size(int64_t R, int64_t K) { return R * mx_quads(K) * 16; }
+
+// x[b][r][c] of a strided matrix, as it is read by the quantizer. by_row (B = 1): the
+// row by row layout.
 struct MxQuantArgs {
     const void* x;
     int dtype;
     int64_t B, stride_b, R, stride_r;
     int K;
-    const int32_t* row_of;
-    int copies;
-    int64_t out_rows;
+    bool by_row;
     uint8_t* codes;
     uint8_t* scales;
 };
@@ -43,7 +46,7 @@ struct MxQuantArgs {
 // picks the weights, and rows of no token are zero. With w2q: silu(X W^T) * (X W2^T)
 // (gate and up).
 struct MxGemmArgs {
-    const uint8_t *xq, *xs;          // quantized operand, or
+    const uint8_t *xq, *xs;          // quantized operand (w2q: row by row, picked by row_token), or
     const void* x;                   // rows to be quantized on the way (null: xq, xs)
     int x_dtype;
     int64_t stride_x;
@@ -86,6 +89,10 @@ hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_
 // of many rows.
 bool mx_few_rows(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx_few(const MxGemmArgs& a, hipStream_t st);
+// y[t] = sum over j of weights[t][j] * (Q(x[row_of[t][j]]) . w[expert of the row]), in one
+// launch, for few tokens (P: rows of x; k <= 32)
+hipError_t launch_mx_down_few(const MxGemmArgs& a, const int32_t* row_of, const float* weights, int k, int64_t P,
+                              hipStream_t st);
 hipError_t launch_mx_wide(const MxGemmArgs& a, hipStream_t st);
 // Row blocks of a plan of P rows, for launch_mx_wide; entries of `tiles`.
 int64_t mx_tiles_size(int64_t P, int64_t E);

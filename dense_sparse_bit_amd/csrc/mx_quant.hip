@@ -54,29 +54,27 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t strid
     }
 }
 
-// The same blocks, each row written to its places in a plan (mx_experts_up): one wave
-// per row and 512 inputs, 16-byte pieces scattered to `copies` rows.
+// The same blocks row by row: a wave takes 512 inputs of kRows rows, each row's codes
+// leave as one run of 256 bytes.
+constexpr int kRows = 4;
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_mx_quant_scatter(const T* x, int64_t R, int64_t stride_r, int K,
-                                                               const int32_t* row_of, int copies, int out_rows,
-                                                               uint8_t* codes, uint8_t* scales) {
-    const int G = (K + 127) / 128, G4 = (G + 3) / 4;
+__global__ __launch_bounds__(kThreads) void k_mx_quant_rows(const T* x, int64_t R, int64_t stride_r, int K, uint8_t* codes,
+                                                            uint8_t* scales) {
+    const int G = (K + 127) / 128, G2 = (G + 1) / 2, G4 = (G + 3) / 4;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + wave;
-    if (r >= R) return;
-    const int q = blockIdx.y;
-    const int k0 = q * 512 + 8 * lane;
-    const MxRaw8<T> v = mx_load8(x + r * stride_r + k0, K - k0);
-    int byte;
-    const uint32_t word = mx_quant8(v, byte);
-    const int g = q * 4 + (lane >> 4), kc = (lane >> 2) & 3;
-    for (int j = 0; j < copies; ++j) {
-        const int p = row_of[r * copies + j];
-        if (p < 0 || p >= out_rows) continue;
-        const int64_t rt = p >> 4;
-        const int row = p & 15;
-        if (g < G) *reinterpret_cast<uint32_t*>(codes + ((rt * G + g) * 64 + kc * 16 + row) * 16 + (lane & 3) * 4) = word;
-        if ((lane & 3) == 0) scales[((rt * G4 + q) * 64 + kc * 16 + row) * 4 + (lane >> 4)] = byte;
+    const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * kRows;
+    const int q = blockIdx.y, k0 = q * 512 + 8 * lane;
+    MxRaw8<T> v[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) v[i] = mx_load8(x + (r0 + i) * stride_r + k0, r0 + i < R ? K - k0 : 0);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        int byte;
+        const uint32_t word = mx_quant8(v[i], byte);
+        const int64_t r = r0 + i;
+        if (r >= R) return;
+        if (q * 4 + (lane >> 5) * 2 < G) *reinterpret_cast<uint32_t*>(codes + r * G2 * 128 + q * 256 + lane * 4) = word;
+        if ((lane & 3) == 0) scales[(r * G4 + q) * 16 + (lane >> 2 & 3) * 4 + (lane >> 4)] = byte;
     }
 }
 
@@ -117,10 +115,9 @@ hipError_t quant(const MxQuantArgs& a, hipStream_t st) {
     const int64_t RT = mx_row_tiles(a.R);
     const int quads = static_cast<int>(mx_quads(a.K));
     const T* x = static_cast<const T*>(a.x);
-    if (a.row_of) {
-        const dim3 grid(static_cast<unsigned>((a.R + 3) / 4), quads);
-        k_mx_quant_scatter<T><<<grid, kThreads, 0, st>>>(x, a.R, a.stride_r, a.K, a.row_of, a.copies,
-                                                         static_cast<int>(a.out_rows), a.codes, a.scales);
+    if (a.by_row) {
+        const dim3 grid(static_cast<unsigned>((a.R + 4 * kRows - 1) / (4 * kRows)), quads);
+        k_mx_quant_rows<T><<<grid, kThreads, 0, st>>>(x, a.R, a.stride_r, a.K, a.codes, a.scales);
     } else {
         const dim3 grid(quads, static_cast<unsigned>(RT < 32768 ? RT : 32768), static_cast<unsigned>(a.B));
         k_mx_quant<T><<<grid, kThreads, 0, st>>>(x, a.stride_b, a.R, a.stride_r, a.K, a.codes, a.scales);
