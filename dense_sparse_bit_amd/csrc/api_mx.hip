@@ -60,6 +60,8 @@ mq::MxGemmArgs product(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, 
     a.K = static_cast<int>(K);
     a.y = y;
     a.y_dtype = y_dtype;
+    a.ldy = static_cast<int>(N);
+    a.w_tiles = static_cast<int>(mq::mx_row_tiles(N));
     return a;
 }
 
@@ -84,6 +86,14 @@ size_t row_bytes(int64_t R, int64_t K) {
 bool few_tokens(int64_t T) { return T <= 32; }
 // Whether the down products go token by token.
 bool one_by_one(int64_t T, int64_t k) { return T <= 8 && k <= 32; }
+// Columns of the down products that are made, and summed, at a time: even parts of at
+// most kDownBytes of fp32 rows.
+constexpr int64_t kDownBytes = int64_t(200) << 20;
+int64_t down_cols(int64_t P, int64_t D) {
+    const int64_t parts = (P * D * 4 + kDownBytes - 1) / kDownBytes;
+    const int64_t cols = ((D + parts - 1) / (parts ? parts : 1) + 255) / 256 * 256;
+    return cols < D ? cols : (D + 3) / 4 * 4;
+}
 size_t tiles_bytes(int64_t P, int64_t E) { return round16(mq::mx_tiles_size(P, E) * 4); }
 
 }  // namespace
@@ -270,10 +280,9 @@ int mq_mx_experts_up(const void* x, int x_dtype, int64_t stride_t, int64_t T, in
 }
 
 size_t mq_mx_experts_down_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I) {
-    if (check_slots(T, k, E) || check_product(T * k, D, I)) return 0;
+    if (check_slots(T, k, E) || check_product(T * k, D, I) || one_by_one(T, k)) return 0;
     const int64_t P = mq::plan_rows(T, k, E);
-    const size_t rows = round16(P * D * 4);
-    if (one_by_one(T, k)) return 0;
+    const size_t rows = round16(P * down_cols(P, D) * 4);
     return few_tokens(T) ? rows : rows + mx_bytes(P, I) + tiles_bytes(P, E);
 }
 
@@ -302,28 +311,35 @@ int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t
     if (workspace_bytes < mq_mx_experts_down_workspace_bytes(T, k, E, D, I) || !workspace || off(workspace, 16))
         return MQ_ERR_INVALID_ARG;
     float* rows = static_cast<float*>(workspace);
+    const int64_t step = down_cols(P, D);
     mq::MxGemmArgs a = product(nullptr, nullptr, wq, ws, P, D, I, rows, MQ_F32);
     a.offsets = offsets;
     a.E = static_cast<int>(E);
     a.T = static_cast<int>(T);
-    hipError_t e;
-    if (few_tokens(T)) {
+    a.ldy = static_cast<int>(step);
+    const bool few = few_tokens(T);
+    if (few) {
         a.x = h;
         a.x_dtype = h_dtype;
         a.stride_x = I;
-        e = mq::launch_mx_few(a, st);
     } else {
-        uint8_t* hq = static_cast<uint8_t*>(workspace) + round16(P * D * 4);
+        uint8_t* hq = static_cast<uint8_t*>(workspace) + round16(P * step * 4);
         uint8_t* hs = hq + round16(mq::mx_codes_size(P, I));
         a.xq = hq;
         a.xs = hs;
         a.tiles = reinterpret_cast<int32_t*>(hs + round16(mq::mx_scales_size(P, I)));
         if (mq::launch_mx_quant(rows_of(h, h_dtype, P, I, I, hq, hs), st) != hipSuccess) return MQ_ERR_HIP;
         if (mq::launch_mx_tiles(offsets, a.E, P, a.tiles, st) != hipSuccess) return MQ_ERR_HIP;
-        e = mq::launch_mx_wide(a, st);
     }
-    if (e != hipSuccess) return MQ_ERR_HIP;
-    return status_of(mq::launch_combine(rows, P, row_of, weights, T, static_cast<int>(k), D, y, y_dtype, st));
+    for (int64_t d = 0; d < D; d += step) {
+        a.N = static_cast<int>(D - d < step ? D - d : step);
+        a.w_tile0 = static_cast<int>(d / 16);
+        if ((few ? mq::launch_mx_few(a, st) : mq::launch_mx_wide(a, st)) != hipSuccess) return MQ_ERR_HIP;
+        if (mq::launch_combine(rows, P, row_of, weights, T, static_cast<int>(k), static_cast<int>(step), a.N, d, D, y, y_dtype,
+                               st) != hipSuccess)
+            return MQ_ERR_HIP;
+    }
+    return MQ_OK;
 }
 
 }  // extern "C"

@@ -179,7 +179,7 @@ __global__ __launch_bounds__(512) void k_mx_few(MxGemmArgs a) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const int c = GATED ? j >> 1 : j;
-            const int64_t tile = static_cast<int64_t>(e) * n_tiles + (ct + c < n_tiles ? ct + c : n_tiles - 1);
+            const int64_t tile = static_cast<int64_t>(e) * a.w_tiles + a.w_tile0 + (ct + c < n_tiles ? ct + c : n_tiles - 1);
             w[j] = ((GATED && (j & 1)) ? a.w2q : a.wq) + tile * G * 1024 + lane * 16;
             ws[j] = ((GATED && (j & 1)) ? a.w2s : a.ws) + tile * G4 * 256 + lane * 4;
         }
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(512) void k_mx_few(MxGemmArgs a) {
             for (int r = 0; r < 4; ++r) v[r] += n + r < a.N ? a.bias[n + r] : 0.0f;
         }
         if (GATED && !(alive >> (l & 15) & 1)) v = mx_f4{0, 0, 0, 0};
-        mx_store4(a.y, a.y_dtype, static_cast<int64_t>(m) * a.N + n, a.N - n, a.N % 4 == 0, v[0], v[1], v[2], v[3]);
+        mx_store4(a.y, a.y_dtype, static_cast<int64_t>(m) * a.ldy + n, a.N - n, a.ldy % 4 == 0, v[0], v[1], v[2], v[3]);
     }
 }
 
@@ -348,7 +348,7 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
     const int n_tiles = (a.N + 15) / 16;
     // a wave with no column of its own (past N) reads the last one's and writes nothing
     const int col_there = min(col16, n_tiles - 1);
-    const int64_t first = static_cast<int64_t>(e) * n_tiles + col_there;
+    const int64_t first = static_cast<int64_t>(e) * a.w_tiles + a.w_tile0 + col_there;
     const int have = min(n_tiles - col_there, GATED ? 2 : 4);
     const int lane_pair = (lane >> 4 & 1) * G * 1024 + (lane >> 5) * 256 + (lane & 15) * 16;
     const int scale_pair = (lane >> 4 & 1) * G4 * 256 + (lane >> 5) * 64 + (lane & 15) * 4;
@@ -516,11 +516,11 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
     uint8_t* tile = lds + wave * kBlockTiles * 1024;             // every wave is past the last barrier
     const int n = col16 * 16 + (lane & (kLanes - 1)) * kPer;
     const int rows = min(n16 * 16, a.M - rt0 * 16);
-    T* y = static_cast<T*>(a.y) + static_cast<int64_t>(rt0) * 16 * a.N;
+    T* y = static_cast<T*>(a.y) + static_cast<int64_t>(rt0) * 16 * a.ldy;
     // 16-byte stores, those beyond the block's rows or N dropped by their offset
-    const bool vec = a.N % kPer == 0 && a.N <= (1 << 21);
-    const __amdgpu_buffer_rsrc_t yr = buffer(y, static_cast<int64_t>(rows) * a.N * sizeof(T));
-    uint32_t at = n < a.N ? ((lane / kLanes) * a.N + n) * sizeof(T) : 0x80000000u;
+    const bool vec = a.ldy % kPer == 0 && a.ldy <= (1 << 21);
+    const __amdgpu_buffer_rsrc_t yr = buffer(y, static_cast<int64_t>(rows) * a.ldy * sizeof(T));
+    uint32_t at = n < a.N ? ((lane / kLanes) * a.ldy + n) * sizeof(T) : 0x80000000u;
 #pragma unroll
     for (int i = 0; i < SUB; ++i) {
         bool live = true;
@@ -552,7 +552,7 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
             for (int s = 0; s < 32 / kRound; ++s) {
                 const mx_u4 v = *reinterpret_cast<const mx_u4*>(tile + (s * kRound + lane / kLanes) * kPitch + (lane & (kLanes - 1)) * 16);
                 __builtin_amdgcn_raw_buffer_store_b128(v, yr, at, 0, 0);
-                at += kRound * a.N * sizeof(T);
+                at += kRound * a.ldy * sizeof(T);
             }
         } else {
             const T* from = reinterpret_cast<const T*>(tile);
@@ -561,7 +561,7 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
             for (int o = lane; o < 32 * kWaveCols; o += 64) {
                 const int r = o / kWaveCols, c = o % kWaveCols;
                 if (32 * i + r < rows && c < cols)
-                    y[static_cast<int64_t>(32 * i + r) * a.N + col16 * 16 + c] = from[r * (kPitch / sizeof(T)) + c];
+                    y[static_cast<int64_t>(32 * i + r) * a.ldy + col16 * 16 + c] = from[r * (kPitch / sizeof(T)) + c];
             }
         }
     }
@@ -573,7 +573,7 @@ __device__ inline void zero_rows(const MxGemmArgs& a, int rt0, int n16, int n0, 
     for (int i = threadIdx.x; i < n16 * 16 * ((c + 3) / 4); i += blockDim.x) {
         const int64_t m = rt0 * 16 + i / ((c + 3) / 4);
         const int n = n0 + 4 * (i % ((c + 3) / 4));
-        if (m < a.M) mx_store4(a.y, a.y_dtype, m * a.N + n, a.N - n, a.N % 4 == 0, 0.0f, 0.0f, 0.0f, 0.0f);
+        if (m < a.M) mx_store4(a.y, a.y_dtype, m * a.ldy + n, a.N - n, a.ldy % 4 == 0, 0.0f, 0.0f, 0.0f, 0.0f);
     }
 }
 
@@ -664,26 +664,38 @@ __global__ __launch_bounds__(1024) void k_mx_tiles(const int32_t* offsets, int E
     }
 }
 
+// y[t][d0 + d] = sum over j of weights[t][j] * rows[row_of[t][j]][d], d < cols. Four columns
+// a thread; a token's rows are read eight at a time.
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine(const float* rows, int64_t n_rows, const int32_t* row_of,
-                                                 const float* weights, int64_t T_, int k, int64_t D, T* y) {
-    const int64_t d = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;
+                                                 const float* weights, int k, int pitch, int cols, int64_t d0, int64_t D, T* y) {
+    const int d = (blockIdx.y * 256 + threadIdx.x) * 4;
     const int64_t t = blockIdx.x;
-    if (d >= D) return;
-    float acc = 0.0f;
-    for (int j = 0; j < k; ++j) {
-        const int p = row_of[t * k + j];
-        const float r = p >= 0 && p < n_rows ? rows[p * D + d] : 0.0f;
-        acc += weights[t * k + j] * r;
+    if (d >= cols) return;
+    mx_f4 acc = {};
+    for (int j0 = 0; j0 < k; j0 += 8) {
+        mx_f4 r[8];
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool there = j0 + j < k;
+            const int p = there ? row_of[t * k + j0 + j] : -1;
+            w[j] = there ? weights[t * k + j0 + j] : 0.0f;
+            r[j] = mx_f4{0, 0, 0, 0};
+            if (p >= 0 && p < n_rows) r[j] = *reinterpret_cast<const mx_f4*>(rows + static_cast<int64_t>(p) * pitch + d);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc += w[j] * r[j];
     }
-    y[t * D + d] = mx_round<T>(acc);
+    mx_store4(y, sizeof(T) == 4 ? MQ_F32 : (__is_same(T, __bf16) ? MQ_BF16 : MQ_F16), t * D + d0 + d, cols - d,
+              D % 4 == 0 && d0 % 4 == 0, acc[0], acc[1], acc[2], acc[3]);
 }
 
 template <typename T>
 hipError_t combine(const float* rows, int64_t n_rows, const int32_t* row_of, const float* weights, int64_t T_, int k,
-                   int64_t D, void* y, hipStream_t st) {
-    k_combine<T><<<dim3(static_cast<unsigned>(T_), static_cast<unsigned>((D + 255) / 256)), 256, 0, st>>>(
-        rows, n_rows, row_of, weights, T_, k, D, static_cast<T*>(y));
+                   int pitch, int cols, int64_t d0, int64_t D, void* y, hipStream_t st) {
+    k_combine<T><<<dim3(static_cast<unsigned>(T_), static_cast<unsigned>((cols + 1023) / 1024)), 256, 0, st>>>(
+        rows, n_rows, row_of, weights, k, pitch, cols, d0, D, static_cast<T*>(y));
     return hipGetLastError();
 }
 
@@ -748,11 +760,11 @@ hipError_t launch_mx_tiles(const int32_t* offsets, int E, int64_t P, int32_t* ti
 }
 
 hipError_t launch_combine(const float* rows, int64_t n_rows, const int32_t* row_of, const float* weights, int64_t T,
-                          int k, int64_t D, void* y, int y_dtype, hipStream_t st) {
+                          int k, int pitch, int cols, int64_t d0, int64_t D, void* y, int y_dtype, hipStream_t st) {
     switch (y_dtype) {
-        case MQ_F32: return combine<float>(rows, n_rows, row_of, weights, T, k, D, y, st);
-        case MQ_BF16: return combine<__bf16>(rows, n_rows, row_of, weights, T, k, D, y, st);
-        default: return combine<_Float16>(rows, n_rows, row_of, weights, T, k, D, y, st);
+        case MQ_F32: return combine<float>(rows, n_rows, row_of, weights, T, k, pitch, cols, d0, D, y, st);
+        case MQ_BF16: return combine<__bf16>(rows, n_rows, row_of, weights, T, k, pitch, cols, d0, D, y, st);
+        default: return combine<_Float16>(rows, n_rows, row_of, weights, T, k, pitch, cols, d0, D, y, st);
     }
 }
 

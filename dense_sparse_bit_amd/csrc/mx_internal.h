@@ -53,8 +53,9 @@ struct MxGemmArgs {
     const uint8_t *wq, *ws, *w2q, *w2s;
     int M, N, K;
     const float* bias;
-    void* y;
-    int y_dtype;
+    void* y;                         // rows ldy apart
+    int y_dtype, ldy;
+    int w_tile0, w_tiles;            // N is a run of the weights' rows: from 16-row tile w_tile0 of w_tiles
     const int32_t* offsets;
     const int32_t* row_token;        // x's row of each of the plan's rows (x given), and which rows are live
     int E, T;
@@ -99,8 +100,9 @@ int64_t mx_tiles_size(int64_t P, int64_t E);
 hipError_t launch_mx_tiles(const int32_t* offsets, int E, int64_t P, int32_t* tiles, hipStream_t st);
 hipError_t launch_route(const RouteArgs& a, hipStream_t st);
 hipError_t launch_plan(const PlanArgs& a, hipStream_t st);
-// y[t] = sum over j of weights[t][j] * rows[row_of[t][j]] (fp32 rows)
+// y[t][d0 + d] = sum over j of weights[t][j] * rows[row_of[t][j]][d], d < cols (fp32 rows,
+// a multiple of 4 apart)
 hipError_t launch_combine(const float* rows, int64_t n_rows, const int32_t* row_of, const float* weights, int64_t T,
-                          int k, int64_t D, void* y, int y_dtype, hipStream_t st);
+                          int k, int pitch, int cols, int64_t d0, int64_t D, void* y, int y_dtype, hipStream_t st);
 
 }  // namespace mq
