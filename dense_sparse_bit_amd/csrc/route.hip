@@ -75,6 +75,8 @@ __device__ inline int first_best(uint32_t key) {
 }
 __device__ inline int first_best(uint64_t key) {
     const uint32_t hi = static_cast<uint32_t>(key >> 32), top = wave_max(hi);
+    const uint64_t some = __ballot(hi == top);
+    if (top && !(some & (some - 1))) return __builtin_ctzll(some);      // most often one lane alone
     const uint32_t lo = hi == top ? static_cast<uint32_t>(key) : 0, low = wave_max(lo);
     return top || low ? __builtin_ctzll(__ballot(hi == top && lo == low)) : -1;
 }
@@ -95,12 +97,17 @@ __global__ __launch_bounds__(64 * kTokens) void k_route(RouteArgs a) {
     if (t >= a.T) return;
     const T* logits = static_cast<const T*>(a.logits) + t * a.stride_t;
     const bool softmax = a.score == MQ_SCORE_SOFTMAX;
-    float x[V];
+    float x[V], bias[V];
     bool fault = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = lane * V + i;
-        x[i] = e < a.E ? static_cast<float>(logits[e]) : -INFINITY;
+        const int e = min(lane * V + i, a.E - 1);      // lanes past the last expert: its values, masked
+        x[i] = static_cast<float>(logits[e]);
+        bias[i] = BIAS ? a.bias[e] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (lane * V + i >= a.E) x[i] = -INFINITY;
         fault |= !(x[i] == x[i]) || (softmax && x[i] == INFINITY);
     }
     double sum = 1.0, base = 0.0;
@@ -125,18 +132,23 @@ __global__ __launch_bounds__(64 * kTokens) void k_route(RouteArgs a) {
         return softmax ? exp(static_cast<double>(v) - base) / sum : 1.0 / (1.0 + exp(-static_cast<double>(v)));
     };
     Key key[V];
+    if constexpr (BIAS) {
+        if (softmax) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane * V + i;
-        if constexpr (BIAS) {
-            score[i] = softmax ? score[i] / sum : 1.0 / (1.0 + exp(-static_cast<double>(x[i])));
-            const double b = e < a.E ? static_cast<double>(a.bias[e]) : 0.0;
-            const double v = x[i] == -INFINITY ? -HUGE_VAL : score[i] + b;
+            for (int i = 0; i < V; ++i) score[i] /= sum;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) score[i] = 1.0 / (1.0 + exp(-static_cast<double>(x[i])));
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const double v = x[i] == -INFINITY ? -HUGE_VAL : score[i] + static_cast<double>(bias[i]);
             fault |= !(v == v);
             key[i] = v == -HUGE_VAL ? 0 : ordered(v);
-        } else {
-            key[i] = x[i] == -INFINITY ? 0 : ordered(x[i]);
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = x[i] == -INFINITY ? 0 : ordered(x[i]);
     }
     float* weights = a.weights + t * a.k;
     int32_t* ids = a.ids + t * a.k;
@@ -154,7 +166,7 @@ __global__ __launch_bounds__(64 * kTokens) void k_route(RouteArgs a) {
         for (int i = 0; i < V; ++i) {
             double v = -HUGE_VAL;
             if (key[i]) {
-                if constexpr (BIAS) v = score[i] + static_cast<double>(a.bias[lane * V + i]);
+                if constexpr (BIAS) v = score[i] + static_cast<double>(bias[i]);
                 else v = x[i];
             }
             mine[lane * V + i] = v;
@@ -163,6 +175,7 @@ __global__ __launch_bounds__(64 * kTokens) void k_route(RouteArgs a) {
         double worth = -HUGE_VAL;
         if (lane < a.groups) {
             double first = -HUGE_VAL, second = -HUGE_VAL;
+#pragma unroll 4
             for (int i = 0; i < per; ++i) {
                 const double v = mine[lane * per + i];
                 if (v > first) { second = first; first = v; } else if (v > second) second = v;
@@ -355,13 +368,13 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PlanArgs a) {
     s.count[tid] = 0;
     __syncthreads();
     const int n = static_cast<int>(a.T * a.k), from = blockIdx.x * kPlanThreads;
-    for (int i = tid; i < from; i += kPlanThreads) {
-        const int e = a.ids[i];
-        if (e >= 0 && e < a.E) atomicAdd(&s.before[e], 1);
-    }
-    for (int i = from + tid; i < n; i += kPlanThreads) {
-        const int e = a.ids[i];
-        if (e >= 0 && e < a.E) atomicAdd(&s.count[e], 1);
+    for (int i0 = tid; i0 < n; i0 += 8 * kPlanThreads) {
+        int e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = i0 + j * kPlanThreads < n ? a.ids[i0 + j * kPlanThreads] : -1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (e[j] >= 0 && e[j] < a.E) atomicAdd(i0 + j * kPlanThreads < from ? &s.before[e[j]] : &s.count[e[j]], 1);
     }
     __syncthreads();
     s.count[tid] += s.before[tid];
