@@ -6,8 +6,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import _lib
-from .mx import _TYPES, MX, _call, _check, _input, _Launch, _mx, _output
+from . import MQError, _lib
+from .mx import _TYPES, MX, _check, _current_device, _empty_strided_cuda, _input, _mx, _on, _output, _raw_stream
 
 _SCORES = {"softmax": 0, "sigmoid": 1}        # MQ_SCORE_*
 _GROUP_SCORES = {"max": 0, "top2": 1}         # MQ_GROUP_*
@@ -22,9 +22,14 @@ class ExpertPlan(NamedTuple):
     row_of: torch.Tensor
 
 
+_route, _plan_rows, _expert_plan = _lib.mq_route, _lib.mq_plan_rows, _lib.mq_expert_plan
+_up, _up_workspace = _lib.mq_mx_experts_up, _lib.mq_mx_experts_up_workspace_bytes
+_down, _down_workspace = _lib.mq_mx_experts_down, _lib.mq_mx_experts_down_workspace_bytes
+
+
 def plan_rows(T: int, k: int, experts: int) -> int:
     """Rows of a plan of T tokens with k slots each: the most that any ids can take."""
-    rows = _lib.mq_plan_rows(T, k, experts)
+    rows = _plan_rows(T, k, experts)
     if rows < 0:
         raise ValueError(f"no plan for {T} tokens of {k} slots and {experts} experts")
     return rows
@@ -40,56 +45,73 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
     weights NaN."""
     code = _input(logits, "logits", 2)
     T, E = logits.shape
-    if score not in _SCORES:
+    score_code, group_code = _SCORES.get(score), _GROUP_SCORES.get(group_score)
+    if score_code is None:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
-    if group_score not in _GROUP_SCORES:
+    if group_code is None:
         raise ValueError(f"group_score must be one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
-    top_groups = groups if top_groups is None else top_groups
+    if top_groups is None:
+        top_groups = groups
     if groups <= 0 or E % groups or not 0 < top_groups <= groups:
         raise ValueError(f"{E} experts do not make {groups} groups of which {top_groups} are kept")
     if not 0 < k <= top_groups * (E // groups):
         raise ValueError(f"k = {k} experts of {top_groups * (E // groups)}")
-    device = logits.device
-    with _Launch(device, stream, logits, bias) as at:
-        if bias is not None:
-            _check(bias, "bias", torch.float32, (E,), device)
-        ids = torch.empty((T, k), dtype=torch.int32, device=device) if ids is None else \
-            _check(ids, "ids", torch.int32, (T, k), device)
-        weights = torch.empty((T, k), dtype=torch.float32, device=device) if weights is None else \
-            _check(weights, "weights", torch.float32, (T, k), device)
-        _call("mq_route", logits.data_ptr(), code, T, logits.stride(0), E, None if bias is None else bias.data_ptr(),
-              _SCORES[score], groups, top_groups, _GROUP_SCORES[group_score], k, int(renormalize), scale, ids.data_ptr(),
-              weights.data_ptr(), at.stream)
+    index = logits.get_device()
+    if stream is not None or index < 0 or index != _current_device():
+        with _on(index, stream, logits, bias, ids, weights):
+            return route(logits, k, score, bias, groups, top_groups, group_score, renormalize, scale, ids, weights)
+    b = None if bias is None else _check(bias, "bias", torch.float32, (E,), index).data_ptr()
+    if ids is None:
+        ids = _empty_strided_cuda((T, k), (k, 1), torch.int32)
+    else:
+        _check(ids, "ids", torch.int32, (T, k), index)
+    if weights is None:
+        weights = _empty_strided_cuda((T, k), (k, 1), torch.float32)
+    else:
+        _check(weights, "weights", torch.float32, (T, k), index)
+    rc = _route(logits.data_ptr(), code, T, logits.stride(0), E, b, score_code, groups, top_groups, group_code, k,
+                1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _raw_stream(index))
+    if rc:
+        raise MQError("mq_route", rc)
     return ids, weights
 
 
 def expert_plan(ids, experts: int, stream=None) -> ExpertPlan:
     """The plan of ids int32 [T, k]. Ids outside [0, experts), such as -1 or another
     rank's experts, get no row."""
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.dtype is not torch.int32:
         raise ValueError("ids must be an int32 tensor [T, k]")
     T, k = ids.shape
-    device = ids.device
-    with _Launch(device, stream, ids) as at:
-        _check(ids, "ids", torch.int32, (T, k), device)
-        rows = plan_rows(T, k, experts)
-        plan = ExpertPlan(torch.empty(experts + 1, dtype=torch.int32, device=device),
-                          torch.empty(rows, dtype=torch.int32, device=device), torch.empty_like(ids))
-        _call("mq_expert_plan", ids.data_ptr(), T, k, experts, plan.offsets.data_ptr(), plan.row_token.data_ptr(),
-              plan.row_of.data_ptr(), at.stream)
-    return plan
+    index = ids.get_device()
+    if stream is not None or index < 0 or index != _current_device():
+        with _on(index, stream, ids):
+            return expert_plan(ids, experts)
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    rows = _plan_rows(T, k, experts)
+    if rows < 0:
+        raise ValueError(f"no plan for {T} tokens of {k} slots and {experts} experts")
+    offsets = _empty_strided_cuda((experts + 1,), (1,), torch.int32)
+    row_token = _empty_strided_cuda((rows,), (1,), torch.int32)
+    row_of = _empty_strided_cuda((T, k), (k, 1), torch.int32)
+    rc = _expert_plan(ids.data_ptr(), T, k, experts, offsets.data_ptr(), row_token.data_ptr(), row_of.data_ptr(),
+                      _raw_stream(index))
+    if rc:
+        raise MQError("mq_expert_plan", rc)
+    return ExpertPlan(offsets, row_token, row_of)
 
 
-def _plan(plan, device):
+def _plan(plan, index):
     """(T, k, experts, rows) of a plan, its tensors checked."""
     if not isinstance(plan, ExpertPlan):
         raise TypeError("plan must be an ExpertPlan (expert_plan)")
-    T, k = plan.row_of.shape
-    E = plan.offsets.numel() - 1
+    offsets, row_token, row_of = plan
+    T, k = row_of.shape
+    E = offsets.shape[0] - 1
     rows = plan_rows(T, k, E)
-    _check(plan.offsets, "plan.offsets", torch.int32, (E + 1,), device)
-    _check(plan.row_token, "plan.row_token", torch.int32, (rows,), device)
-    _check(plan.row_of, "plan.row_of", torch.int32, (T, k), device)
+    _check(offsets, "plan.offsets", torch.int32, (E + 1,), index)
+    _check(row_token, "plan.row_token", torch.int32, (rows,), index)
+    _check(row_of, "plan.row_of", torch.int32, (T, k), index)
     return T, k, E, rows
 
 
@@ -97,23 +119,27 @@ def mx_experts_up(x, w_gate: MX, w_up: MX, plan: ExpertPlan, out_dtype=torch.bfl
     """h [rows, I]: for each row of the plan silu(Q(x[t]) w_gate[e]^T) * (Q(x[t]) w_up[e]^T),
     zero for rows of no token. x [T, D]; w_gate, w_up: MX batches [experts, I, D]."""
     code = _input(x, "x", 2)
-    device = x.device
-    with _Launch(device, stream, x, w_gate, w_up, plan) as at:
-        T, k, E, rows = _plan(plan, device)
-        _mx(w_gate, "w_gate", device, E)
-        _mx(w_up, "w_up", device, E)
-        D, I = w_gate.cols, w_gate.rows
-        if (w_up.rows, w_up.cols) != (I, D):
-            raise ValueError(f"w_gate is {I} x {D}, w_up is {w_up.rows} x {w_up.cols}")
-        if x.shape != (T, D):
-            raise ValueError(f"x must be [{T}, {D}] for this plan and these weights, got {tuple(x.shape)}")
-        h = _output(h, "h", (rows, I), out_dtype if h is None else h.dtype, device)
-        need = _lib.mq_mx_experts_up_workspace_bytes(T, k, E, D, I)
-        work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-        _call("mq_mx_experts_up", x.data_ptr(), code, x.stride(0), T, k, E, D, I, plan.offsets.data_ptr(),
-              plan.row_token.data_ptr(), plan.row_of.data_ptr(), w_gate.codes.data_ptr(), w_gate.scales.data_ptr(),
-              w_up.codes.data_ptr(), w_up.scales.data_ptr(), h.data_ptr(), _TYPES[h.dtype],
-              None if work is None else work.data_ptr(), need, at.stream)
+    index = x.get_device()
+    if stream is not None or index < 0 or index != _current_device():
+        with _on(index, stream, x, w_gate, w_up, plan, h):
+            return mx_experts_up(x, w_gate, w_up, plan, out_dtype, h)
+    T, k, E, rows = _plan(plan, index)
+    _mx(w_gate, "w_gate", index, E)
+    _mx(w_up, "w_up", index, E)
+    D, I = w_gate.cols, w_gate.rows
+    if (w_up.rows, w_up.cols) != (I, D):
+        raise ValueError(f"w_gate is {I} x {D}, w_up is {w_up.rows} x {w_up.cols}")
+    if x.shape != (T, D):
+        raise ValueError(f"x must be [{T}, {D}] for this plan and these weights, got {tuple(x.shape)}")
+    h = _output(h, "h", (rows, I), out_dtype if h is None else h.dtype, index)
+    need = _up_workspace(T, k, E, D, I)
+    work = _empty_strided_cuda((need,), (1,), torch.uint8) if need else None
+    rc = _up(x.data_ptr(), code, x.stride(0), T, k, E, D, I, plan.offsets.data_ptr(), plan.row_token.data_ptr(),
+             plan.row_of.data_ptr(), w_gate.codes.data_ptr(), w_gate.scales.data_ptr(), w_up.codes.data_ptr(),
+             w_up.scales.data_ptr(), h.data_ptr(), _TYPES[h.dtype], work.data_ptr() if need else None, need,
+             _raw_stream(index))
+    if rc:
+        raise MQError("mq_mx_experts_up", rc)
     return h
 
 
@@ -121,19 +147,23 @@ def mx_experts_down(h, w_down: MX, plan: ExpertPlan, weights, out_dtype=torch.bf
     """y[t] = sum over slots j of weights[t, j] * (Q(h[row_of[t, j]]) w_down[e]^T), in the order
     of the slots. h [rows, I], weights fp32 [T, k], w_down: MX batch [experts, D, I]."""
     code = _input(h, "h", 2)
-    device = h.device
-    with _Launch(device, stream, h, w_down, plan, weights) as at:
-        T, k, E, rows = _plan(plan, device)
-        _mx(w_down, "w_down", device, E)
-        D, I = w_down.rows, w_down.cols
-        _check(h, "h", h.dtype, (rows, I), device)
-        _check(weights, "weights", torch.float32, (T, k), device)
-        y = _output(y, "y", (T, D), out_dtype if y is None else y.dtype, device)
-        need = _lib.mq_mx_experts_down_workspace_bytes(T, k, E, D, I)
-        work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-        _call("mq_mx_experts_down", h.data_ptr(), code, T, k, E, D, I, plan.offsets.data_ptr(), plan.row_of.data_ptr(),
-              weights.data_ptr(), w_down.codes.data_ptr(), w_down.scales.data_ptr(), y.data_ptr(), _TYPES[y.dtype],
-              None if work is None else work.data_ptr(), need, at.stream)
+    index = h.get_device()
+    if stream is not None or index < 0 or index != _current_device():
+        with _on(index, stream, h, w_down, plan, weights, y):
+            return mx_experts_down(h, w_down, plan, weights, out_dtype, y)
+    T, k, E, rows = _plan(plan, index)
+    _mx(w_down, "w_down", index, E)
+    D, I = w_down.rows, w_down.cols
+    _check(h, "h", h.dtype, (rows, I), index)
+    _check(weights, "weights", torch.float32, (T, k), index)
+    y = _output(y, "y", (T, D), out_dtype if y is None else y.dtype, index)
+    need = _down_workspace(T, k, E, D, I)
+    work = _empty_strided_cuda((need,), (1,), torch.uint8) if need else None
+    rc = _down(h.data_ptr(), code, T, k, E, D, I, plan.offsets.data_ptr(), plan.row_of.data_ptr(), weights.data_ptr(),
+               w_down.codes.data_ptr(), w_down.scales.data_ptr(), y.data_ptr(), _TYPES[y.dtype],
+               work.data_ptr() if need else None, need, _raw_stream(index))
+    if rc:
+        raise MQError("mq_mx_experts_down", rc)
     return y
 
 
