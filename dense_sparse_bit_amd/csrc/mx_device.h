@@ -46,6 +46,14 @@ template <> struct MxRaw8<float> {
         for (int i = 7; i > 0; --i) v[i] = v[i - 1];
         v[0] = x;
     }
+    __device__ void drop(int s) {                // the first s go, zeros follow the last
+#pragma unroll
+        for (int b = 4; b > 0; b >>= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = (s & b) ? (i + b < 8 ? v[i + b] : 0.0f) : v[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = s >= 8 ? 0.0f : v[i];
+    }
     __device__ uint32_t peak() const {           // fp32 bits of the largest magnitude
         uint32_t m = 0;
 #pragma unroll
@@ -68,6 +76,18 @@ template <typename T> struct MxRaw16 {
 #pragma unroll
         for (int i = 3; i > 0; --i) w[i] = w[i] << 16 | w[i - 1] >> 16;
         w[0] = w[0] << 16 | __builtin_bit_cast(unsigned short, x);
+    }
+    __device__ void drop(int s) {
+#pragma unroll
+        for (int b = 2; b > 0; b >>= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = (s & 2 * b) ? (i + b < 4 ? w[i + b] : 0) : w[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = (s & 1) ? w[i] >> 16 | (i < 3 ? w[i + 1] << 16 : 0) : w[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = s >= 8 ? 0 : w[i];
     }
     __device__ mx_u16x2 peak2() const {           // magnitudes compare as whole numbers
         mx_u16x2 m = __builtin_bit_cast(mx_u16x2, w[0] & 0x7fff7fffu);
@@ -128,6 +148,17 @@ __device__ inline MxRaw8<T> mx_load8(const T* p, int have) {
 #pragma clang loop unroll(disable)
         for (int i = have - 1; i >= 0; --i) r.push(p[i]);   // rare: kept small
     }
+    return r;
+}
+
+// The values k .. k + 7 of a row of K >= 8; those from `lim` <= K on (a multiple of 8, or
+// K) are zero. Always one whole load within the row, moved down where it had to start
+// earlier: no branch, so that the loads of several rows are in flight together.
+template <typename T>
+__device__ inline MxRaw8<T> mx_load8_tail(const T* row, int k, int K, int lim) {
+    const int at = min(k, K - 8), s = k < lim ? k - at : 8;
+    MxRaw8<T> r = mx_load8(row + at, 8);
+    r.drop(s);
     return r;
 }
 

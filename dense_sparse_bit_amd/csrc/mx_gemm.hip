@@ -65,26 +65,30 @@ __device__ __forceinline__ void rows_to_lds(const XT* x, int64_t stride, int K, 
         *reinterpret_cast<uint32_t*>(to + (lane >> 2) * kBlockPitch + (r & 15) * 16 + (lane & 3) * 4) = word;
         if ((lane & 3) == 0) to[16 * kBlockPitch + ((lane >> 2 & 3) * 16 + (r & 15)) * 4 + (lane >> 4)] = byte;
     };
-    if (g + kBatch <= end && (g + kBatch) * 128 <= K) {
+    auto all = [&](auto load) __attribute__((always_inline)) {
         MxRaw8<XT> v[RB];
 #pragma unroll
-        for (int i = 0; i < RB; ++i) v[i] = mx_load8(x + row_at(min(i, rows - 1)) * stride + k, 8);
+        for (int i = 0; i < RB; ++i) v[i] = load(min(i, rows - 1));
         between();
 #pragma unroll
         for (int i = 0; i < RB; ++i)
             if (RB == 1 || i < rows) put(i, v[i]);
         for (int r = RB; r < rows; r += RB) {
 #pragma unroll
-            for (int i = 0; i < RB; ++i) v[i] = mx_load8(x + row_at(min(r + i, rows - 1)) * stride + k, 8);
+            for (int i = 0; i < RB; ++i) v[i] = load(min(r + i, rows - 1));
 #pragma unroll
             for (int i = 0; i < RB; ++i)
                 if (r + i < rows) put(r + i, v[i]);
         }
+    };
+    const int lim = min(K, end * 128);
+    if ((g + kBatch) * 128 <= lim) {
+        all([&](int r) __attribute__((always_inline)) { return mx_load8(x + row_at(r) * stride + k, 8); });
+    } else if (K >= 8) {                                   // the end of the run or of the rows
+        all([&](int r) __attribute__((always_inline)) { return mx_load8_tail(x + row_at(r) * stride, k, K, lim); });
     } else {
-        // the end of the run or of the rows
         between();
-        const int have = min(K, end * 128) - k;
-        for (int r = 0; r < rows; ++r) put(r, mx_load8(x + row_at(r) * stride + k, have));
+        for (int r = 0; r < rows; ++r) put(r, mx_load8(x + row_at(r) * stride + k, K - k));
     }
 }
 
@@ -234,18 +238,26 @@ hipError_t few(const MxGemmArgs& a, hipStream_t st) {
     const unsigned rows = static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT));
     const int G = (a.K + 127) / 128;
     const int waves = G >= 32 ? 8 : (G >= 8 ? 4 : (G >= 4 ? 2 : 1));
-    const size_t lds = static_cast<size_t>(waves) * (kRowsLds > NT * 1024 ? kRowsLds : NT * 1024) * MT;
+    constexpr int kRowsBytes = __is_same(XT, MxReady) ? 0 : kRowsLds;
+    const size_t lds = static_cast<size_t>(waves) * (kRowsBytes > NT * 1024 ? kRowsBytes : NT * 1024) * MT;
     k_mx_few<XT, NT, MT, RB, GATED><<<dim3(cols, rows), 64 * waves, lds, st>>>(a);
     return hipGetLastError();
 }
 
-// rows: the most that a row tile can have
+// Rows that are quantized on the way: at most 16 a workgroup. RB (rows whose loads are in
+// flight together) follows their number; two column tiles a wave, which share the rows'
+// quantization, where there are enough tiles for two rounds of workgroups without.
+// Measured (K = 4096): 4 rows, N = 4096: RB 4 / 8: 4.1 / 4.5 us; 16 rows, one tile / two:
+// N = 4096 6.7 / 7.2 us, N = 14336 15.5 / 11.4 us.
 template <typename XT>
-hipError_t few_rows(const MxGemmArgs& a, int64_t rows, hipStream_t st) {
-    if (a.w2q) return rows == 1 ? few<XT, 2, 1, 1, true>(a, st) : few<XT, 2, 1, 8, true>(a, st);
+hipError_t few_raw(const MxGemmArgs& a, int64_t rows, hipStream_t st) {
+    if (a.w2q) {
+        if (rows == 1) return few<XT, 2, 1, 1, true>(a, st);
+        return rows <= 4 ? few<XT, 2, 1, 4, true>(a, st) : few<XT, 2, 1, 8, true>(a, st);
+    }
     if (rows == 1) return few<XT, 1, 1, 1, false>(a, st);
-    if (a.offsets || rows <= 16) return few<XT, 1, 1, 8, false>(a, st);
-    return few<XT, 2, 2, 16, false>(a, st);
+    if (rows <= 4) return few<XT, 1, 1, 4, false>(a, st);
+    return a.N > 8192 ? few<XT, 2, 1, 8, false>(a, st) : few<XT, 1, 1, 8, false>(a, st);
 }
 
 // The experts' down products of few tokens, each token by itself: workgroup (16 NT
@@ -328,6 +340,26 @@ __device__ inline mx_i4 load16(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
 }
 __device__ inline int load4(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
     return static_cast<int>(__builtin_amdgcn_raw_buffer_load_b32(r, lane_at, at, 0));
+}
+
+// Pieces of 32 rows in a row block, for `rows32` pieces in all and about `partial` more
+// that are not whole, over `cols` column blocks: the least time of
+//   rounds of 256 workgroups * (2.2 + 0.6 s + K / 128 (0.165 + 0.05 s)) us
+// for blocks of s pieces, a fit of one round's times from s = 1 (K = 4096: 9.3 us, 14336:
+// 26.6) to 6 (20.8, 58.2).
+int wide_pieces(int64_t rows32, int64_t partial, int64_t cols, int64_t K, double* time) {
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= kMaxSub; ++s) {
+        const int64_t n = ((rows32 + s - 1) / s + partial) * cols;
+        const double t = static_cast<double>((n + 255) / 256) * (2.2 + 0.6 * s + static_cast<double>((K + 127) / 128) * (0.165 + 0.05 * s));
+        if (s == 1 || t < least) {
+            least = t;
+            best = s;
+        }
+    }
+    if (time) *time = least;
+    return best;
 }
 
 // One wave's part of a tile of SUB * 32 rows: 64 columns (GATED: 32 of gate and 32 of
@@ -668,34 +700,37 @@ __global__ __launch_bounds__(1024) void k_mx_tiles(const int32_t* offsets, int E
 // a thread; a token's rows are read eight at a time.
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine(const float* rows, int64_t n_rows, const int32_t* row_of,
-                                                 const float* weights, int k, int pitch, int cols, int64_t d0, int64_t D, T* y) {
+                                                 const float* weights, int64_t T_, int k, int pitch, int cols, int64_t d0,
+                                                 int64_t D, T* y) {
     const int d = (blockIdx.y * 256 + threadIdx.x) * 4;
-    const int64_t t = blockIdx.x;
     if (d >= cols) return;
-    mx_f4 acc = {};
-    for (int j0 = 0; j0 < k; j0 += 8) {
-        mx_f4 r[8];
-        float w[8];
+    for (int64_t t = blockIdx.x; t < T_; t += gridDim.x) {
+        mx_f4 acc = {};
+        for (int j0 = 0; j0 < k; j0 += 8) {
+            mx_f4 r[8];
+            float w[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bool there = j0 + j < k;
-            const int p = there ? row_of[t * k + j0 + j] : -1;
-            w[j] = there ? weights[t * k + j0 + j] : 0.0f;
-            r[j] = mx_f4{0, 0, 0, 0};
-            if (p >= 0 && p < n_rows) r[j] = *reinterpret_cast<const mx_f4*>(rows + static_cast<int64_t>(p) * pitch + d);
+            for (int j = 0; j < 8; ++j) {
+                const bool there = j0 + j < k;
+                const int p = there ? row_of[t * k + j0 + j] : -1;
+                w[j] = there ? weights[t * k + j0 + j] : 0.0f;
+                r[j] = mx_f4{0, 0, 0, 0};
+                if (p >= 0 && p < n_rows) r[j] = *reinterpret_cast<const mx_f4*>(rows + static_cast<int64_t>(p) * pitch + d);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc += w[j] * r[j];
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc += w[j] * r[j];
+        mx_store4(y, sizeof(T) == 4 ? MQ_F32 : (__is_same(T, __bf16) ? MQ_BF16 : MQ_F16), t * D + d0 + d, cols - d,
+                  D % 4 == 0 && d0 % 4 == 0, acc[0], acc[1], acc[2], acc[3]);
     }
-    mx_store4(y, sizeof(T) == 4 ? MQ_F32 : (__is_same(T, __bf16) ? MQ_BF16 : MQ_F16), t * D + d0 + d, cols - d,
-              D % 4 == 0 && d0 % 4 == 0, acc[0], acc[1], acc[2], acc[3]);
 }
 
 template <typename T>
 hipError_t combine(const float* rows, int64_t n_rows, const int32_t* row_of, const float* weights, int64_t T_, int k,
                    int pitch, int cols, int64_t d0, int64_t D, void* y, hipStream_t st) {
-    k_combine<T><<<dim3(static_cast<unsigned>(T_), static_cast<unsigned>((cols + 1023) / 1024)), 256, 0, st>>>(
-        rows, n_rows, row_of, weights, k, pitch, cols, d0, D, static_cast<T*>(y));
+    const unsigned grid = static_cast<unsigned>(T_ < (1 << 20) ? T_ : 1 << 20);
+    k_combine<T><<<dim3(grid, static_cast<unsigned>((cols + 1023) / 1024)), 256, 0, st>>>(
+        rows, n_rows, row_of, weights, T_, k, pitch, cols, d0, D, static_cast<T*>(y));
     return hipGetLastError();
 }
 
@@ -708,12 +743,13 @@ hipError_t wide(const MxGemmArgs& a, hipStream_t st) {
     const int64_t ncol = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
     int blocks = 0, block_tiles = 0;
     if (!a.tiles) {
-        blocks = (rt + kBlockTiles - 1) / kBlockTiles;
-        block_tiles = ((rt + blocks - 1) / blocks + 1) / 2 * 2;
+        block_tiles = 2 * wide_pieces((rt + 1) / 2, 0, ncol, a.K, nullptr);
         blocks = (rt + block_tiles - 1) / block_tiles;
     }
     const int64_t n = a.tiles ? tiles_cap(a.M, a.E) : blocks;
-    const unsigned grid = static_cast<unsigned>((n * ncol + 7) / 8 * 8);
+    const int64_t want = (n * ncol + 7) / 8 * 8;
+    if (want >= int64_t(1) << 24) return hipErrorInvalidConfiguration;       // a grid holds 2^32 threads
+    const unsigned grid = static_cast<unsigned>(want);
     if (gated)
         k_mx_wide<T, true><<<grid, 256, 0, st>>>(a, blocks, block_tiles);
     else
@@ -723,15 +759,35 @@ hipError_t wide(const MxGemmArgs& a, hipStream_t st) {
 
 }  // namespace
 
-bool mx_few_rows(int64_t M, int64_t N, int64_t K) { return M <= 32; }
+int mx_plan(int64_t M, int64_t N, int64_t K) {
+    if (M <= 16) return kMxOneTile;
+    const double groups = static_cast<double>((K + 127) / 128), g = groups / 32, rows32 = static_cast<double>((M + 31) / 32);
+    const double u = rows32 * static_cast<double>((N + 15) / 16) / 256;       // workgroups of one column tile, in 256s
+    const double cost[3] = {2.4 + g + fmax(u, 1.0) * (0.5 + 1.15 * g),
+                            2.6 + 2.0 * g + fmax(u / 2, 1.0) * (0.4 + 1.9 * g),
+                            4.0 + 2.2 * g + fmax(u / 4, 0.7) * (0.6 + 2.6 * g)};
+    int best = 0;
+    for (int i = 1; i < 3; ++i)
+        if (cost[i] < cost[best]) best = i;
+    double wide;
+    wide_pieces(static_cast<int64_t>(rows32), 0, (N + 255) / 256, K, &wide);
+    return cost[best] < wide && rows32 <= 65535 ? best : kMxWide;
+}
 
-hipError_t launch_mx_few(const MxGemmArgs& a, hipStream_t st) {
-    const int64_t rows = a.offsets ? a.T : a.M;
-    if (!a.x) return few_rows<MxReady>(a, rows, st);
-    switch (a.x_dtype) {
-        case MQ_F32: return few_rows<float>(a, rows, st);
-        case MQ_BF16: return few_rows<__bf16>(a, rows, st);
-        default: return few_rows<_Float16>(a, rows, st);
+hipError_t launch_mx_few(const MxGemmArgs& a, int plan, hipStream_t st) {
+    if (a.x) {
+        const int64_t rows = a.offsets ? a.T : a.M;
+        switch (a.x_dtype) {
+            case MQ_F32: return few_raw<float>(a, rows, st);
+            case MQ_BF16: return few_raw<__bf16>(a, rows, st);
+            default: return few_raw<_Float16>(a, rows, st);
+        }
+    }
+    switch (plan) {
+        case kMxOneTile: return few<MxReady, 1, 1, 8, false>(a, st);
+        case 0: return few<MxReady, 1, 2, 8, false>(a, st);
+        case 1: return few<MxReady, 2, 2, 8, false>(a, st);
+        default: return few<MxReady, 4, 2, 8, false>(a, st);
     }
 }
 

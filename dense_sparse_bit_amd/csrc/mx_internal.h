@@ -85,11 +85,12 @@ struct PlanArgs {
 hipError_t launch_mx_quant(const MxQuantArgs& a, hipStream_t st);
 hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t B, int64_t R, int64_t K, void* y,
                              int y_dtype, hipStream_t st);
-// The product's kernel: split over K, with the rows quantized on the way where they are
-// not yet (M is the rows of a product, or of the busiest plan that could be), or tiles
-// of many rows.
-bool mx_few_rows(int64_t M, int64_t N, int64_t K);
-hipError_t launch_mx_few(const MxGemmArgs& a, hipStream_t st);
+// The kernel of a product of M rows: split over K with 16 rows a workgroup, or 32 rows and
+// one, two or four column tiles (0, 1, 2), or tiles of many rows.
+constexpr int kMxOneTile = -1, kMxWide = 3;
+int mx_plan(int64_t M, int64_t N, int64_t K);
+// a.x given: rows are quantized on the way (plan kMxOneTile, or rows of a plan's tiles)
+hipError_t launch_mx_few(const MxGemmArgs& a, int plan, hipStream_t st);
 // y[t] = sum over j of weights[t][j] * (Q(x[row_of[t][j]]) . w[expert of the row]), in one
 // launch, for few tokens (P: rows of x; k <= 32)
 hipError_t launch_mx_down_few(const MxGemmArgs& a, const int32_t* row_of, const float* weights, int k, int64_t P,

@@ -93,162 +93,164 @@ __global__ __launch_bounds__(64 * kTokens) void k_route(RouteArgs a) {
     extern __shared__ __align__(16) double lds[];     // (groups) keys, and scores where they are computed
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + wave;
-    if (t >= a.T) return;
-    const T* logits = static_cast<const T*>(a.logits) + t * a.stride_t;
-    const bool softmax = a.score == MQ_SCORE_SOFTMAX;
-    float x[V], bias[V];
-    bool fault = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = min(lane * V + i, a.E - 1);      // lanes past the last expert: its values, masked
-        x[i] = static_cast<float>(logits[e]);
-        bias[i] = BIAS ? a.bias[e] : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (lane * V + i >= a.E) x[i] = -INFINITY;
-        fault |= !(x[i] == x[i]) || (softmax && x[i] == INFINITY);
-    }
-    double sum = 1.0, base = 0.0;
-    double score[V];
-    if (softmax) {
-        float top = x[0];
-#pragma unroll
-        for (int i = 1; i < V; ++i) top = fmaxf(top, x[i]);
-        const uint32_t best = wave_max(ordered(top));
-        base = __uint_as_float(best ^ ((best >> 31) ? 0x80000000u : 0xffffffffu));
-        if (!(base > -INFINITY)) base = 0.0;
-        sum = 0.0;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + wave; t < a.T; t += static_cast<int64_t>(gridDim.x) * kTokens) {
+        const T* logits = static_cast<const T*>(a.logits) + t * a.stride_t;
+        const bool softmax = a.score == MQ_SCORE_SOFTMAX;
+        float x[V], bias[V];
+        bool fault = false;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            score[i] = exp(static_cast<double>(x[i]) - base);
-            sum += score[i];
+            const int e = min(lane * V + i, a.E - 1);      // lanes past the last expert: its values, masked
+            x[i] = static_cast<float>(logits[e]);
+            bias[i] = BIAS ? a.bias[e] : 0.0f;
         }
-        sum = wave_sum(sum);
-        if (!(sum > 0.0)) sum = 1.0;
-    }
-    auto score_of = [&](float v) __attribute__((always_inline)) -> double {
-        return softmax ? exp(static_cast<double>(v) - base) / sum : 1.0 / (1.0 + exp(-static_cast<double>(v)));
-    };
-    Key key[V];
-    if constexpr (BIAS) {
-        if (softmax) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) score[i] /= sum;
+        for (int i = 0; i < V; ++i) {
+            if (lane * V + i >= a.E) x[i] = -INFINITY;
+            fault |= !(x[i] == x[i]) || (softmax && x[i] == INFINITY);
+        }
+        double sum = 1.0, base = 0.0;
+        double score[V];
+        if (softmax) {
+            float top = x[0];
+#pragma unroll
+            for (int i = 1; i < V; ++i) top = fmaxf(top, x[i]);
+            const uint32_t best = wave_max(ordered(top));
+            base = __uint_as_float(best ^ ((best >> 31) ? 0x80000000u : 0xffffffffu));
+            if (!(base > -INFINITY)) base = 0.0;
+            sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                score[i] = exp(static_cast<double>(x[i]) - base);
+                sum += score[i];
+            }
+            sum = wave_sum(sum);
+            if (!(sum > 0.0)) sum = 1.0;
+        }
+        auto score_of = [&](float v) __attribute__((always_inline)) -> double {
+            return softmax ? exp(static_cast<double>(v) - base) / sum : 1.0 / (1.0 + exp(-static_cast<double>(v)));
+        };
+        Key key[V];
+        if constexpr (BIAS) {
+            if (softmax) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) score[i] /= sum;
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) score[i] = 1.0 / (1.0 + exp(-static_cast<double>(x[i])));
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const double v = x[i] == -INFINITY ? -HUGE_VAL : score[i] + static_cast<double>(bias[i]);
+                fault |= !(v == v);
+                key[i] = v == -HUGE_VAL ? 0 : ordered(v);
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) score[i] = 1.0 / (1.0 + exp(-static_cast<double>(x[i])));
+            for (int i = 0; i < V; ++i) key[i] = x[i] == -INFINITY ? 0 : ordered(x[i]);
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const double v = x[i] == -INFINITY ? -HUGE_VAL : score[i] + static_cast<double>(bias[i]);
-            fault |= !(v == v);
-            key[i] = v == -HUGE_VAL ? 0 : ordered(v);
+        float* weights = a.weights + t * a.k;
+        int32_t* ids = a.ids + t * a.k;
+        if (__any(fault)) {
+            // a NaN among the logits or biases: no expert, and weights that show it
+            if (lane < a.k) { ids[lane] = -1; weights[lane] = NAN; }
+            continue;
         }
-    } else {
+        if (a.top_groups < a.groups) {
+            // lane g weighs group g, whose experts it finds in LDS
+            const int per = a.E / a.groups;
+            const bool two = a.group_score == MQ_GROUP_TOP2;
+            double* mine = lds + wave * 64 * V;
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = x[i] == -INFINITY ? 0 : ordered(x[i]);
-    }
-    float* weights = a.weights + t * a.k;
-    int32_t* ids = a.ids + t * a.k;
-    if (__any(fault)) {
-        // a NaN among the logits or biases: no expert, and weights that show it
-        if (lane < a.k) { ids[lane] = -1; weights[lane] = NAN; }
-        return;
-    }
-    if (a.top_groups < a.groups) {
-        // lane g weighs group g, whose experts it finds in LDS
-        const int per = a.E / a.groups;
-        const bool two = a.group_score == MQ_GROUP_TOP2;
-        double* mine = lds + wave * 64 * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            double v = -HUGE_VAL;
-            if (key[i]) {
-                if constexpr (BIAS) v = score[i] + static_cast<double>(bias[i]);
-                else v = x[i];
+            for (int i = 0; i < V; ++i) {
+                double v = -HUGE_VAL;
+                if (key[i]) {
+                    if constexpr (BIAS) v = score[i] + static_cast<double>(bias[i]);
+                    else v = x[i];
+                }
+                mine[lane * V + i] = v;
             }
-            mine[lane * V + i] = v;
-        }
-        __builtin_amdgcn_wave_barrier();             // a wave's LDS accesses complete in order
-        double worth = -HUGE_VAL;
-        if (lane < a.groups) {
-            double first = -HUGE_VAL, second = -HUGE_VAL;
+            __builtin_amdgcn_wave_barrier();             // a wave's LDS accesses complete in order
+            double worth = -HUGE_VAL;
+            if (lane < a.groups) {
+                double first = -HUGE_VAL, second = -HUGE_VAL;
 #pragma unroll 4
-            for (int i = 0; i < per; ++i) {
-                const double v = mine[lane * per + i];
-                if (v > first) { second = first; first = v; } else if (v > second) second = v;
-            }
-            worth = first;
-            if (two && first > -HUGE_VAL) {
-                if constexpr (BIAS) {
-                    if (second > -HUGE_VAL) worth += second;
-                } else {
-                    worth = score_of(static_cast<float>(first)) + (second > -HUGE_VAL ? score_of(static_cast<float>(second)) : 0.0);
+                for (int i = 0; i < per; ++i) {
+                    const double v = mine[lane * per + i];
+                    if (v > first) { second = first; first = v; } else if (v > second) second = v;
+                }
+                worth = first;
+                if (two && first > -HUGE_VAL) {
+                    if constexpr (BIAS) {
+                        if (second > -HUGE_VAL) worth += second;
+                    } else {
+                        worth = score_of(static_cast<float>(first)) + (second > -HUGE_VAL ? score_of(static_cast<float>(second)) : 0.0);
+                    }
                 }
             }
-        }
-        const uint64_t wb = ordered(worth);
-        int rank = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const uint64_t other = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(wb >> 32), g))) << 32 |
-                                   static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(wb), g));
-            rank += other > wb || (other == wb && g < lane);
-        }
-        const uint64_t keep = __ballot(rank < a.top_groups);
-        const float share = 1.0f / per;
-#pragma unroll
-        for (int i = 0; i < V; ++i)                    // (e + 1/2) / per is never near a whole number
-            if (!(keep >> (static_cast<int>((lane * V + i + 0.5f) * share) & 63) & 1)) key[i] = 0;
-    }
-    int mine = -1;
-    double w = 0.0;
-    float logit = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-        Key best = key[0];
-        int at = 0;
-#pragma unroll
-        for (int i = 1; i < V; ++i)
-            if (key[i] > best) { best = key[i]; at = i; }
-        const int from = first_best(best);
-        if (from < 0) break;                           // no expert is left
-        const int i0 = __builtin_amdgcn_readlane(at, from);
-        if (lane == j) mine = from * V + i0;
-        // the chosen expert's logit (its score, where scores are computed)
-        double s = 0.0;
-        float l = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i == i0) {
-                if constexpr (BIAS) s = score[i];
-                l = x[i];
-                if (lane == from) key[i] = 0;
+            const uint64_t wb = ordered(worth);
+            int rank = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const uint64_t other = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(wb >> 32), g))) << 32 |
+                                       static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(wb), g));
+                rank += other > wb || (other == wb && g < lane);
             }
-        if constexpr (BIAS) {
-            const uint64_t b = __builtin_bit_cast(uint64_t, s);
-            const uint64_t r = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(b >> 32), from))) << 32 |
-                               static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(b), from));
-            if (lane == j) w = __builtin_bit_cast(double, r);
-        } else {
-            const float r = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(l)), from)));
-            if (lane == j) logit = r;
+            const uint64_t keep = __ballot(rank < a.top_groups);
+            const float share = 1.0f / per;
+#pragma unroll
+            for (int i = 0; i < V; ++i)                    // (e + 1/2) / per is never near a whole number
+                if (!(keep >> (static_cast<int>((lane * V + i + 0.5f) * share) & 63) & 1)) key[i] = 0;
         }
-    }
-    if constexpr (!BIAS) w = mine >= 0 ? score_of(logit) : 0.0;
-    if (a.renormalize) {
-        const double total = wave_sum(w);
-        w = total > 0.0 ? w / total : 0.0;
-    }
-    if (lane < a.k) {
-        ids[lane] = mine;
-        weights[lane] = static_cast<float>(w * static_cast<double>(a.scale));
+        int mine = -1;
+        double w = 0.0;
+        float logit = 0.0f;
+        for (int j = 0; j < a.k; ++j) {
+            Key best = key[0];
+            int at = 0;
+#pragma unroll
+            for (int i = 1; i < V; ++i)
+                if (key[i] > best) { best = key[i]; at = i; }
+            const int from = first_best(best);
+            if (from < 0) break;                           // no expert is left
+            const int i0 = __builtin_amdgcn_readlane(at, from);
+            if (lane == j) mine = from * V + i0;
+            // the chosen expert's logit (its score, where scores are computed)
+            double s = 0.0;
+            float l = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i == i0) {
+                    if constexpr (BIAS) s = score[i];
+                    l = x[i];
+                    if (lane == from) key[i] = 0;
+                }
+            if constexpr (BIAS) {
+                const uint64_t b = __builtin_bit_cast(uint64_t, s);
+                const uint64_t r = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(b >> 32), from))) << 32 |
+                                   static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(b), from));
+                if (lane == j) w = __builtin_bit_cast(double, r);
+            } else {
+                const float r = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(l)), from)));
+                if (lane == j) logit = r;
+            }
+        }
+        if constexpr (!BIAS) w = mine >= 0 ? score_of(logit) : 0.0;
+        if (a.renormalize) {
+            const double total = wave_sum(w);
+            w = total > 0.0 ? w / total : 0.0;
+        }
+        if (lane < a.k) {
+            ids[lane] = mine;
+            weights[lane] = static_cast<float>(w * static_cast<double>(a.scale));
+        }
     }
 }
 
 template <typename T, int V>
 hipError_t route(const RouteArgs& a, hipStream_t st) {
-    const unsigned grid = static_cast<unsigned>((a.T + kTokens - 1) / kTokens);
+    const int64_t wgs = (a.T + kTokens - 1) / kTokens;
+    const unsigned grid = static_cast<unsigned>(wgs < (1 << 22) ? wgs : 1 << 22);
     const size_t lds = a.top_groups < a.groups ? kTokens * 64 * V * sizeof(double) : 0;
     if (a.bias) k_route<T, V, true><<<grid, 64 * kTokens, lds, st>>>(a);
     else k_route<T, V, false><<<grid, 64 * kTokens, lds, st>>>(a);
