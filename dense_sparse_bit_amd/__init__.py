@@ -28,6 +28,12 @@ if not os.path.exists(LIB_PATH):
                       "(hipcc, gfx950). There is no fallback implementation.")
 
 _lib = C.CDLL(LIB_PATH)
+
+try:
+    from . import _binding  # noqa: E402  (csrc/binding.cpp; after torch and libmq.so, which it links to)
+except ImportError as e:
+    raise ImportError(f"{_PKG}/_binding.so is missing or does not load: build it with "
+                      "`python dense_sparse_bit_amd/_build.py`") from e
 _p, _i64, _int = C.c_void_p, C.c_int64, C.c_int
 
 _SIGS = {

@@ -1,16 +1,19 @@
-"""Build libmq.so (the HIP library) in-tree with hipcc for gfx950.
+"""Build libmq.so (the HIP library) in-tree with hipcc for gfx950, and _binding.so (the
+extension module that calls it) with g++.
 
     python dense_sparse_bit_amd/_build.py
 
 A standalone script (it imports nothing from the package, whose import needs the
 built library). Cross-compiles without a GPU. Objects go to
-dense_sparse_bit_amd/_build/, the shared library to dense_sparse_bit_amd/libmq.so.
+dense_sparse_bit_amd/_build/, the libraries to dense_sparse_bit_amd/.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -50,6 +53,24 @@ def _compile(name: str, flags: list) -> str:
     return out
 
 
+def _binding() -> str:
+    """The extension module: host code against torch's headers and libmq.so."""
+    spec = importlib.util.find_spec("torch")              # found, not imported
+    torch = os.path.dirname(spec.origin)
+    out = os.path.join(PKG, "_binding.so")
+    cmd = ["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", out + ".tmp",
+           f"-L{torch}/lib", "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10_hip", "-lc10", f"-L{PKG}", "-lmq",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stderr}")
+    os.replace(out + ".tmp", out)
+    return out
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
@@ -60,8 +81,9 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    binding = _binding()
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {binding}")
     return LIB
 
 

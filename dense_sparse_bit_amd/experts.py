@@ -6,8 +6,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import MQError, _lib
-from .mx import _TYPES, MX, _check, _current_device, _empty_strided_cuda, _input, _mx, _on, _output, _raw_stream
+from . import MQError, _binding, _lib
+from .mx import _TYPES, MX, _check, _current_device, _input, _mx, _on, _output, _raw_stream
 
 _SCORES = {"softmax": 0, "sigmoid": 1}        # MQ_SCORE_*
 _GROUP_SCORES = {"max": 0, "top2": 1}         # MQ_GROUP_*
@@ -22,6 +22,7 @@ class ExpertPlan(NamedTuple):
     row_of: torch.Tensor
 
 
+_binding.types(MX, ExpertPlan)
 _route, _plan_rows, _expert_plan = _lib.mq_route, _lib.mq_plan_rows, _lib.mq_expert_plan
 _up, _up_workspace = _lib.mq_mx_experts_up, _lib.mq_mx_experts_up_workspace_bytes
 _down, _down_workspace = _lib.mq_mx_experts_down, _lib.mq_mx_experts_down_workspace_bytes
@@ -43,6 +44,11 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
     ("max": a group's largest key, "top2": the sum of its two largest). Logits of -inf mask
     experts: slots that none is left for have id -1 and weight 0. A NaN gives ids -1 and
     weights NaN."""
+    if stream is None:
+        done = _binding.route(logits, k, _SCORES.get(score, -1), bias, groups, groups if top_groups is None else top_groups,
+                              _GROUP_SCORES.get(group_score, -1), renormalize, float(scale), ids, weights)
+        if done is not None:
+            return done
     code = _input(logits, "logits", 2)
     T, E = logits.shape
     score_code, group_code = _SCORES.get(score), _GROUP_SCORES.get(group_score)
@@ -62,11 +68,11 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
             return route(logits, k, score, bias, groups, top_groups, group_score, renormalize, scale, ids, weights)
     b = None if bias is None else _check(bias, "bias", torch.float32, (E,), index).data_ptr()
     if ids is None:
-        ids = _empty_strided_cuda((T, k), (k, 1), torch.int32)
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     else:
         _check(ids, "ids", torch.int32, (T, k), index)
     if weights is None:
-        weights = _empty_strided_cuda((T, k), (k, 1), torch.float32)
+        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
     else:
         _check(weights, "weights", torch.float32, (T, k), index)
     rc = _route(logits.data_ptr(), code, T, logits.stride(0), E, b, score_code, groups, top_groups, group_code, k,
@@ -79,6 +85,10 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
 def expert_plan(ids, experts: int, stream=None) -> ExpertPlan:
     """The plan of ids int32 [T, k]. Ids outside [0, experts), such as -1 or another
     rank's experts, get no row."""
+    if stream is None:
+        done = _binding.expert_plan(ids, experts)
+        if done is not None:
+            return done
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.dtype is not torch.int32:
         raise ValueError("ids must be an int32 tensor [T, k]")
     T, k = ids.shape
@@ -91,9 +101,9 @@ def expert_plan(ids, experts: int, stream=None) -> ExpertPlan:
     rows = _plan_rows(T, k, experts)
     if rows < 0:
         raise ValueError(f"no plan for {T} tokens of {k} slots and {experts} experts")
-    offsets = _empty_strided_cuda((experts + 1,), (1,), torch.int32)
-    row_token = _empty_strided_cuda((rows,), (1,), torch.int32)
-    row_of = _empty_strided_cuda((T, k), (k, 1), torch.int32)
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+    row_token = torch.empty(rows, dtype=torch.int32, device=ids.device)
+    row_of = torch.empty_like(ids)
     rc = _expert_plan(ids.data_ptr(), T, k, experts, offsets.data_ptr(), row_token.data_ptr(), row_of.data_ptr(),
                       _raw_stream(index))
     if rc:
@@ -118,6 +128,10 @@ def _plan(plan, index):
 def mx_experts_up(x, w_gate: MX, w_up: MX, plan: ExpertPlan, out_dtype=torch.bfloat16, h=None, stream=None):
     """h [rows, I]: for each row of the plan silu(Q(x[t]) w_gate[e]^T) * (Q(x[t]) w_up[e]^T),
     zero for rows of no token. x [T, D]; w_gate, w_up: MX batches [experts, I, D]."""
+    if stream is None:
+        done = _binding.experts_up(x, w_gate, w_up, plan, out_dtype, h)
+        if done is not None:
+            return done
     code = _input(x, "x", 2)
     index = x.get_device()
     if stream is not None or index < 0 or index != _current_device():
@@ -133,7 +147,7 @@ def mx_experts_up(x, w_gate: MX, w_up: MX, plan: ExpertPlan, out_dtype=torch.bfl
         raise ValueError(f"x must be [{T}, {D}] for this plan and these weights, got {tuple(x.shape)}")
     h = _output(h, "h", (rows, I), out_dtype if h is None else h.dtype, index)
     need = _up_workspace(T, k, E, D, I)
-    work = _empty_strided_cuda((need,), (1,), torch.uint8) if need else None
+    work = torch.empty(need, dtype=torch.uint8, device=plan.offsets.device) if need else None
     rc = _up(x.data_ptr(), code, x.stride(0), T, k, E, D, I, plan.offsets.data_ptr(), plan.row_token.data_ptr(),
              plan.row_of.data_ptr(), w_gate.codes.data_ptr(), w_gate.scales.data_ptr(), w_up.codes.data_ptr(),
              w_up.scales.data_ptr(), h.data_ptr(), _TYPES[h.dtype], work.data_ptr() if need else None, need,
@@ -146,6 +160,10 @@ def mx_experts_up(x, w_gate: MX, w_up: MX, plan: ExpertPlan, out_dtype=torch.bfl
 def mx_experts_down(h, w_down: MX, plan: ExpertPlan, weights, out_dtype=torch.bfloat16, y=None, stream=None):
     """y[t] = sum over slots j of weights[t, j] * (Q(h[row_of[t, j]]) w_down[e]^T), in the order
     of the slots. h [rows, I], weights fp32 [T, k], w_down: MX batch [experts, D, I]."""
+    if stream is None:
+        done = _binding.experts_down(h, w_down, plan, weights, out_dtype, y)
+        if done is not None:
+            return done
     code = _input(h, "h", 2)
     index = h.get_device()
     if stream is not None or index < 0 or index != _current_device():
@@ -158,7 +176,7 @@ def mx_experts_down(h, w_down: MX, plan: ExpertPlan, weights, out_dtype=torch.bf
     _check(weights, "weights", torch.float32, (T, k), index)
     y = _output(y, "y", (T, D), out_dtype if y is None else y.dtype, index)
     need = _down_workspace(T, k, E, D, I)
-    work = _empty_strided_cuda((need,), (1,), torch.uint8) if need else None
+    work = torch.empty(need, dtype=torch.uint8, device=plan.offsets.device) if need else None
     rc = _down(h.data_ptr(), code, T, k, E, D, I, plan.offsets.data_ptr(), plan.row_of.data_ptr(), weights.data_ptr(),
                w_down.codes.data_ptr(), w_down.scales.data_ptr(), y.data_ptr(), _TYPES[y.dtype],
                work.data_ptr() if need else None, need, _raw_stream(index))

@@ -1,7 +1,11 @@
 """Microscaled 4-bit matrices (include/mq.h): quantization, reading back, products.
 
 32 consecutive inputs of a row share a power-of-two scale, values are 4-bit floats. The
-functions check and marshal device tensors; all of the work runs in libmq.so.
+functions check and marshal device tensors; all of the work runs in libmq.so. A call
+with all as it should be, on the current device and stream, is done by the extension
+module _binding (csrc/binding.cpp), which costs the host about half of what the same
+steps cost in Python; the rest of each function tells what is wrong, or makes another
+device or stream current first.
 """
 from __future__ import annotations
 
@@ -9,20 +13,12 @@ from typing import NamedTuple
 
 import torch
 
-from . import MQError, _lib
+from . import MQError, _binding, _lib
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # MQ_F32, MQ_BF16, MQ_F16
 
-# What one call costs on the host decides the speed of the smallest ones: the current
-# device and stream are asked for without making objects of them, and outputs are
-# allocated through torch's shortest way (0.7 us against 1.6 us for torch.empty).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
-try:
-    from torch._C._dynamo.guards import _empty_strided_cuda
-except ImportError:
-    def _empty_strided_cuda(size, stride, dtype):
-        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
 
 
 class MX(NamedTuple):
@@ -85,19 +81,10 @@ def _mx(a, name, index, batch=None):
     return a
 
 
-def _new(shape, dtype):
-    """A contiguous tensor on the current device."""
-    stride, n = [], 1
-    for size in reversed(shape):
-        stride.append(n)
-        n *= size or 1
-    return _empty_strided_cuda(shape, tuple(reversed(stride)), dtype)
-
-
 def _output(y, name, shape, dtype, index):
     if y is None:
         _type(dtype, name)
-        return _empty_strided_cuda(shape, (shape[1] or 1, 1), dtype) if len(shape) == 2 else _new(shape, dtype)
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{index}")
     _type(y.dtype if isinstance(y, torch.Tensor) else dtype, name)
     _check(y, name, dtype, shape, index)
     if y.data_ptr() % 16:
@@ -131,6 +118,10 @@ def mx_quantize(x, out=None, stream=None) -> MX:
     """x [R, K] or [B, R, K] (fp32, bf16, fp16; the last axis contiguous, other strides
     free) to microscaled 4-bit. A block of 32 with a NaN or an infinity reads back as NaN.
     out: an MX of the same sizes to write to."""
+    if stream is None:
+        done = _binding.quantize(x, out)
+        if done is not None:
+            return done
     batched = isinstance(x, torch.Tensor) and x.dim() == 3
     code = _input(x, "x", 3 if batched else 2)
     shape = x.shape
@@ -144,11 +135,9 @@ def mx_quantize(x, out=None, stream=None) -> MX:
     if out is None:
         tiles, groups = (R + 15) // 16, (K + 127) // 128
         quads = (groups + 3) // 4
-        if batched:
-            out = MX(_new((shape[0], tiles, groups, 1024), torch.uint8), _new((shape[0], tiles, quads, 256), torch.uint8), R, K)
-        else:
-            out = MX(_empty_strided_cuda((tiles, groups, 1024), (groups * 1024, 1024, 1), torch.uint8),
-                     _empty_strided_cuda((tiles, quads, 256), (quads * 256, 256, 1), torch.uint8), R, K)
+        lead = (shape[0],) if batched else ()
+        out = MX(torch.empty(lead + (tiles, groups, 1024), dtype=torch.uint8, device=x.device),
+                 torch.empty(lead + (tiles, quads, 256), dtype=torch.uint8, device=x.device), R, K)
     else:
         if isinstance(out, MX) and (out.rows, out.cols) != (R, K):
             raise ValueError(f"out is {out.rows} x {out.cols}, x is {R} x {K}")
@@ -162,6 +151,10 @@ def mx_quantize(x, out=None, stream=None) -> MX:
 
 def mx_dequantize(a: MX, dtype=torch.float32, out=None, stream=None):
     """The values of a microscaled matrix (or batch), [(B,) R, K]."""
+    if stream is None:
+        done = _binding.dequantize(a, dtype, out)
+        if done is not None:
+            return done
     if not isinstance(a, MX):
         raise TypeError("a must be an MX matrix (mx_quantize)")
     codes, scales, R, K = a
@@ -182,6 +175,10 @@ def mx_dequantize(a: MX, dtype=torch.float32, out=None, stream=None):
 def mx_linear(x, w: MX, bias=None, out_dtype=torch.bfloat16, y=None, stream=None):
     """y = Q(x) w^T + bias: x [M, K] (fp32, bf16, fp16), quantized on the way, or an MX
     matrix; w an MX matrix [N, K]; bias fp32 [N]."""
+    if stream is None:
+        done = _binding.linear(x, w, bias, out_dtype, y)
+        if done is not None:
+            return done
     ready = isinstance(x, MX)
     if ready:
         index = x.codes.get_device()
@@ -207,7 +204,7 @@ def mx_linear(x, w: MX, bias=None, out_dtype=torch.bfloat16, y=None, stream=None
                    y.data_ptr(), _TYPES[y.dtype], _raw_stream(index))
     else:
         need = _linear_workspace(M, N, K)
-        work = _empty_strided_cuda((need,), (1,), torch.uint8) if need else None
+        work = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
         rc = _linear(x.data_ptr(), code, x.stride(0), w.codes.data_ptr(), w.scales.data_ptr(), M, N, K, b, y.data_ptr(),
                      _TYPES[y.dtype], work.data_ptr() if need else None, need, _raw_stream(index))
     if rc:
