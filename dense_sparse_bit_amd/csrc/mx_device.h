@@ -176,13 +176,6 @@ __device__ inline uint32_t mx_quant8(const MxRaw8<T>& v, int& byte) {
     return byte == 255 ? 0 : v.codes(mx_scale_value(byte));
 }
 
-// value of a 4-bit code: 0, 0.5, 1, 1.5, 2, 3, 4, 6 with the sign in bit 3
-__device__ inline float mx_code_value(uint32_t c) {
-    const uint32_t m = c & 7;
-    const float v = m < 4 ? 0.5f * m : (m < 6 ? m - 2.0f : 2.0f * m - 8.0f);
-    return c & 8 ? -v : v;
-}
-
 template <typename T>
 __device__ inline T mx_round(float v) { return static_cast<T>(v); }
 

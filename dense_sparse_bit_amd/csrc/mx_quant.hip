@@ -19,7 +19,8 @@ constexpr int kThreads = 256;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t stride_b, int64_t R, int64_t stride_r, int K,
                                                        uint8_t* codes, uint8_t* scales) {
-    __shared__ uint32_t lds_codes[1024];
+    constexpr int kRun = 16 * 4 + 4;                // words of a block's 16 rows, and 4 more: other banks
+    __shared__ __align__(16) uint32_t lds_codes[16 * kRun];
     __shared__ uint8_t lds_scales[256];
     const int G = (K + 127) / 128, G4 = (G + 3) / 4;
     const int64_t RT = (R + 15) / 16;
@@ -38,7 +39,7 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t strid
         for (int i = 0; i < 4; ++i) {
             const int row = 4 * wave + i;
             int byte;
-            lds_codes[((lane >> 2) * 16 + row) * 4 + (lane & 3)] = mx_quant8(v[i], byte);
+            lds_codes[(lane >> 2) * kRun + row * 4 + (lane & 3)] = mx_quant8(v[i], byte);
             // blocks beyond K hold zeros, so their byte is 0
             if ((lane & 3) == 0) lds_scales[(((lane >> 2) & 3) * 16 + row) * 4 + (lane >> 4)] = byte;
         }
@@ -46,7 +47,7 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t strid
         const int t = threadIdx.x;
         if (q * 4 + (t >> 6) < G)
             *reinterpret_cast<uint4*>(codes + ((b * RT + rt) * G + q * 4) * 1024 + t * 16) =
-                *reinterpret_cast<const uint4*>(&lds_codes[4 * t]);
+                *reinterpret_cast<const uint4*>(&lds_codes[(t >> 4) * kRun + (t & 15) * 4]);
         if (t < 64)
             *reinterpret_cast<uint32_t*>(scales + ((b * RT + rt) * G4 + q) * 256 + t * 4) =
                 *reinterpret_cast<const uint32_t*>(&lds_scales[4 * t]);
@@ -78,35 +79,61 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant_rows(const T* x, int64_t 
     }
 }
 
+// The way back, tile by tile as k_mx_quant: the codes of 16 rows x 512 inputs come in as
+// one run, change places in LDS (runs of 16 rows 16 bytes apart, so that a row's words
+// lie in different banks) and leave as rows, 16 bytes of bf16 a lane. The instruction's
+// value times scale is exact in fp32 and rounded once to T. Bound by the writes.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t R, int K,
                                                          T* y) {
+    constexpr int kRun = 16 * 4 + 4;                // words of a block's 16 rows, and 4 more
+    __shared__ __align__(16) uint32_t lds_codes[16 * kRun];
+    __shared__ uint32_t lds_scales[64];
     const int G = (K + 127) / 128, G4 = (G + 3) / 4;
     const int64_t RT = (R + 15) / 16, b = blockIdx.z;
-    const int k0 = (blockIdx.x * kThreads + threadIdx.x) * 8;
-    if (k0 >= K) return;
-    const int g = k0 >> 7, kc = (k0 >> 5) & 3;
-    for (int64_t r = blockIdx.y; r < R; r += gridDim.y) {
-        const int64_t rt = b * RT + (r >> 4);
-        const int lane = kc * 16 + static_cast<int>(r & 15);
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + ((rt * G + g) * 64 + lane) * 16 + ((k0 >> 3) & 3) * 4);
-        const int byte = scales[((rt * G4 + (g >> 2)) * 64 + lane) * 4 + (g & 3)];
-        T* out = y + (b * R + r) * K + k0;
-        T v[8];
+    const int q = blockIdx.x, t = threadIdx.x, wave = t >> 6, lane = t & 63;
+    const int k0 = q * 512 + 8 * lane, have = K - k0;
+    for (int64_t rt = blockIdx.y; rt < RT; rt += gridDim.y) {
+        if (q * 4 + wave < G)
+            *reinterpret_cast<uint4*>(&lds_codes[(t >> 4) * kRun + (t & 15) * 4]) =
+                *reinterpret_cast<const uint4*>(codes + ((b * RT + rt) * G + q * 4) * 1024 + t * 16);
+        if (t < 64) lds_scales[t] = *reinterpret_cast<const uint32_t*>(scales + ((b * RT + rt) * G4 + q) * 256 + t * 4);
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float f = byte == 255 ? __uint_as_float(0x7fc00000u) : ldexpf(mx_code_value(w >> (4 * i)), byte - 127);
-            v[i] = mx_round<T>(f);
-        }
-        if (K % 8 == 0) {
-            typedef T V8 __attribute__((ext_vector_type(8), aligned(16)));
-            V8 o;
+        for (int i = 0; i < 4; ++i) {
+            const int row = 4 * wave + i;
+            const int64_t r = rt * 16 + row;
+            if (r >= R || have <= 0) continue;
+            const uint32_t w = lds_codes[(lane >> 2) * kRun + row * 4 + (lane & 3)];
+            const int byte = lds_scales[(lane >> 2 & 3) * 16 + row] >> 8 * (lane >> 4) & 255;
+            const float scale = mx_scale_value(byte);
+            float v[8];
+            const mx_f2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 1),
+                        p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 3);
+            v[0] = p0[0]; v[1] = p0[1]; v[2] = p1[0]; v[3] = p1[1];
+            v[4] = p2[0]; v[5] = p2[1]; v[6] = p3[0]; v[7] = p3[1];
+            if (byte == 255) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = v[i];
-            *reinterpret_cast<V8*>(out) = o;
-        } else {
-            for (int i = 0; i < 8 && k0 + i < K; ++i) out[i] = v[i];
+                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(0x7fc00000u);
+            }
+            T* out = y + (b * R + r) * K + k0;
+            if (have >= 8) {
+                if constexpr (sizeof(T) == 4) {
+                    typedef float Out __attribute__((ext_vector_type(4), aligned(4)));
+                    *reinterpret_cast<Out*>(out) = Out{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<Out*>(out + 4) = Out{v[4], v[5], v[6], v[7]};
+                } else {
+                    typedef uint32_t Out __attribute__((ext_vector_type(4), aligned(2)));
+                    *reinterpret_cast<Out*>(out) = Out{mx_pack2<T>(v[0], v[1]), mx_pack2<T>(v[2], v[3]), mx_pack2<T>(v[4], v[5]),
+                                                       mx_pack2<T>(v[6], v[7])};
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < have) out[j] = mx_round<T>(v[j]);
+            }
         }
+        __syncthreads();
     }
 }
 
@@ -127,8 +154,8 @@ hipError_t quant(const MxQuantArgs& a, hipStream_t st) {
 
 template <typename T>
 hipError_t dequant(const uint8_t* codes, const uint8_t* scales, int64_t B, int64_t R, int64_t K, void* y, hipStream_t st) {
-    const dim3 grid(static_cast<unsigned>((K + kThreads * 8 - 1) / (kThreads * 8)),
-                    static_cast<unsigned>(R < 32768 ? R : 32768), static_cast<unsigned>(B));
+    const int64_t RT = mx_row_tiles(R);
+    const dim3 grid(static_cast<unsigned>(mx_quads(K)), static_cast<unsigned>(RT < 32768 ? RT : 32768), static_cast<unsigned>(B));
     k_mx_dequant<T><<<grid, kThreads, 0, st>>>(codes, scales, R, static_cast<int>(K), static_cast<T*>(y));
     return hipGetLastError();
 }
