@@ -37,6 +37,11 @@ int check_product(int64_t M, int64_t N, int64_t K) {
     return MQ_OK;
 }
 
+// the up products find a token's quantized row by a 32-bit offset
+int check_row_offsets(int64_t T, int64_t D) {
+    return mq::mx_row_codes_size(T, D) > int64_t(0xffffffff) ? MQ_ERR_UNSUPPORTED : MQ_OK;
+}
+
 int check_slots(int64_t T, int64_t k, int64_t E) {
     if (T < 0 || k <= 0 || E <= 0) return MQ_ERR_INVALID_ARG;
     if (E > MQ_MAX_EXPERTS || T > kMaxSlots / k) return MQ_ERR_UNSUPPORTED;
@@ -243,7 +248,7 @@ int mq_expert_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t*
 }
 
 size_t mq_mx_experts_up_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I) {
-    if (check_slots(T, k, E) || check_product(T * k, I, D) || few_tokens(T, k)) return 0;
+    if (check_slots(T, k, E) || check_product(T * k, I, D) || check_row_offsets(T, D) || few_tokens(T, k)) return 0;
     const int64_t P = mq::plan_rows(T, k, E);
     return row_bytes(T, D) + tiles_bytes(P, E);
 }
@@ -253,7 +258,8 @@ int mq_mx_experts_up(const void* x, int x_dtype, int64_t stride_t, int64_t T, in
                      const uint8_t* gate_s, const uint8_t* up_q, const uint8_t* up_s, void* h, int h_dtype,
                      void* workspace, size_t workspace_bytes, void* stream) {
     int rc = check_slots(T, k, E);
-    if (rc || (rc = check_product(mq::plan_rows(T, k, E), I, D)) || (rc = check_matrix(E, I, D))) return rc;
+    if (rc || (rc = check_product(mq::plan_rows(T, k, E), I, D)) || (rc = check_matrix(E, I, D)) || (rc = check_row_offsets(T, D)))
+        return rc;
     if (bad_type(x_dtype) || bad_type(h_dtype) || stride_t < 0) return MQ_ERR_INVALID_ARG;
     if (T == 0) return MQ_OK;
     if (!x || off(x, type_size(x_dtype)) || !h || off(h, 16)) return MQ_ERR_INVALID_ARG;

@@ -10,6 +10,7 @@
 
 namespace mq {
 
+typedef int mx_i2 __attribute__((ext_vector_type(2)));
 typedef int mx_i4 __attribute__((ext_vector_type(4)));
 typedef int mx_i8 __attribute__((ext_vector_type(8)));
 typedef float mx_f4 __attribute__((ext_vector_type(4)));

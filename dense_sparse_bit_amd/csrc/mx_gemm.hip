@@ -324,15 +324,17 @@ hipError_t down_few(const MxGemmArgs& a, const int32_t* row_of, const float* wei
 
 // ------------------------------------------------------------------- many rows
 template <int S> struct Phase { static constexpr int value = S; };
-constexpr int kMaxSub = 6;                    // 32-row pieces of a row block
+constexpr int kMaxSub = 4;                    // 32-row pieces of a row block
 constexpr int kBlockTiles = 2 * kMaxSub;      // its 16-row tiles
+constexpr int kScaleBytes = 512 * kMaxSub;    // its rows' scales for four steps
+constexpr int kOutBytes = 32 * (64 * 4 + 16); // a wave's results on their way out: 32 rows, 16 B apart in the banks
 
 __device__ inline __amdgpu_buffer_rsrc_t buffer(const void* base, int64_t bytes) {
     // wave-uniform by construction; said so here, or every load becomes a loop over lanes
     const uint64_t p = reinterpret_cast<uint64_t>(base);
     const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p));
     const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p >> 32));
-    const int n = __builtin_amdgcn_readfirstlane(static_cast<int>(bytes < 0 ? 0 : (bytes < 0x7fffffff ? bytes : 0x7fffffff)));
+    const int n = __builtin_amdgcn_readfirstlane(static_cast<int>(bytes < 0 ? 0 : (bytes < 0xffffffff ? bytes : 0xffffffff)));
     return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(static_cast<uint64_t>(hi) << 32 | lo), 0, n, 0x00020000);
 }
 __device__ inline mx_i4 load16(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
@@ -342,17 +344,19 @@ __device__ inline int load4(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
     return static_cast<int>(__builtin_amdgcn_raw_buffer_load_b32(r, lane_at, at, 0));
 }
 
-// Pieces of 32 rows in a row block, for `rows32` pieces in all and about `partial` more
-// that are not whole, over `cols` column blocks: the least time of
-//   rounds of 256 workgroups * (2.2 + 0.6 s + K / 128 (0.165 + 0.05 s)) us
-// for blocks of s pieces, a fit of one round's times from s = 1 (K = 4096: 9.3 us, 14336:
-// 26.6) to 6 (20.8, 58.2).
-int wide_pieces(int64_t rows32, int64_t partial, int64_t cols, int64_t K, double* time) {
+// Pieces of 32 rows in a row block, for `rows32` pieces in all over `cols` column blocks:
+// the least time of n workgroups of s pieces each, two to a CU. Measured in us (K = 1024,
+// 4096, 14336): a round of 512 takes from 6.2, 15.4, 50 (s = 1) to 12.4, 34.8, 104 (s = 4),
+// one of at most 256, alone on their CUs, from 5.3, 11.7, 30 to 11.5, 21.6, 57. Rounds
+// after the first run into one another; the last one's end costs about 0.15 of one.
+int wide_pieces(int64_t rows32, int64_t cols, int64_t K, double* time) {
+    const double g = static_cast<double>((K + 127) / 128);
     int best = 1;
     double least = 0.0;
     for (int s = 1; s <= kMaxSub; ++s) {
-        const int64_t n = ((rows32 + s - 1) / s + partial) * cols;
-        const double t = static_cast<double>((n + 255) / 256) * (2.2 + 0.6 * s + static_cast<double>((K + 127) / 128) * (0.165 + 0.05 * s));
+        const int64_t n = (rows32 + s - 1) / s * cols;
+        const double round = 2.0 + 0.8 * s + g * (0.255 + 0.157 * s), alone = 2.0 + 1.4 * s + g * (0.155 + 0.07 * s);
+        const double t = n <= 256 ? alone : (n <= 512 ? round : (static_cast<double>(n) / 512 + 0.15) * round);
         if (s == 1 || t < least) {
             least = t;
             best = s;
@@ -363,10 +367,11 @@ int wide_pieces(int64_t rows32, int64_t partial, int64_t cols, int64_t K, double
 }
 
 // One wave's part of a tile of SUB * 32 rows: 64 columns (GATED: 32 of gate and 32 of
-// up). Its weights go from memory straight to registers, three steps of 128 inputs
-// ahead (the layout is the instruction's own); the rows, which the four waves share, go
-// through four LDS stages, one barrier a step. Reads beyond the operands' ends give zero
-// (buffer loads with the operands' sizes).
+// up). Its weights go from memory straight to registers, two steps of 128 inputs ahead
+// (the layout is the instruction's own); the rows and their scales, which the four waves
+// share, go through four LDS stages, one barrier a step. Reads beyond the operands' ends
+// give zero (buffer loads with the operands' sizes). Two workgroups share a CU: one's
+// products fill the other's barriers, first loads and stores.
 template <typename T, int SUB, bool GATED>
 __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int rt0, int n16, int e, int col16) {
     constexpr int XL = (SUB + 1) / 2;                // 16-row tiles that a wave fetches a step
@@ -390,22 +395,23 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
     const __amdgpu_buffer_rsrc_t w2sr = GATED ? buffer(a.w2s + first * G4 * 256, static_cast<int64_t>(have) * G4 * 256) : wsr;
     const int pair1 = GATED ? 0 : 2 * G * 1024, spair1 = GATED ? 0 : 2 * G4 * 256;
     // rows: tiles in the weights' layout, or (GATED) rows of their own, picked by token:
-    const int G2 = (G + 1) / 2;
-    const __amdgpu_buffer_rsrc_t xr = buffer(a.xq + static_cast<int64_t>(GATED ? 0 : rt0) * G * 1024, static_cast<int64_t>(n16) * G * 1024);
-    const __amdgpu_buffer_rsrc_t xsr = buffer(a.xs + static_cast<int64_t>(GATED ? 0 : rt0) * G4 * 256, static_cast<int64_t>(n16) * G4 * 256);
-    const uint8_t* xrow[2][GATED ? XL : 1];
-    const uint8_t* xsrow[GATED ? SUB : 1];
-    if constexpr (GATED) {
-        auto token = [&](int r) __attribute__((always_inline)) -> int64_t {       // of no row: token 0's, never written
-            const int t = r < n16 * 16 ? a.row_token[rt0 * 16 + r] : 0;
-            return static_cast<unsigned>(t) < static_cast<unsigned>(a.T) ? t : 0;
-        };
+    const int pitch = (G + 1) / 2 * 128;
+    const __amdgpu_buffer_rsrc_t xr = GATED ? buffer(a.xq, static_cast<int64_t>(a.T) * pitch)
+                                            : buffer(a.xq + static_cast<int64_t>(rt0) * G * 1024, static_cast<int64_t>(n16) * G * 1024);
+    const __amdgpu_buffer_rsrc_t xsr = GATED ? buffer(a.xs, static_cast<int64_t>(a.T) * G4 * 16)
+                                             : buffer(a.xs + static_cast<int64_t>(rt0) * G4 * 256, static_cast<int64_t>(n16) * G4 * 256);
+    auto token = [&](int r) __attribute__((always_inline)) -> uint32_t {          // of no row: token 0's, never written
+        const int t = r < n16 * 16 ? a.row_token[rt0 * 16 + r] : 0;
+        return static_cast<uint32_t>(t) < static_cast<uint32_t>(a.T) ? t : 0;
+    };
+    uint32_t xat[2][XL], xsat;                       // this lane's places in xr and xsr
 #pragma unroll
-        for (int p = 0; p < 2 * XL; ++p)
-            xrow[p / XL][p % XL] = a.xq + token((p % XL * 4 + wave) * 16 + 8 * (p / XL) + (lane >> 3)) * G2 * 128 + (lane & 7) * 16;
-#pragma unroll
-        for (int i = 0; i < SUB; ++i) xsrow[i] = a.xs + token(32 * i + (lane & 31)) * G4 * 16 + (lane >> 5) * 4;
-    }
+    for (int p = 0; p < 2 * XL; ++p)
+        xat[p / XL][p % XL] = GATED ? token((p % XL * 4 + wave) * 16 + 8 * (p / XL) + (lane >> 3)) * pitch + (lane & 7) * 16
+                                    : (p % XL * 4 + wave) * G * 1024 + lane * 16;
+    // a quad of steps' scales, 8 bytes a thread
+    if constexpr (GATED) xsat = token(threadIdx.x >> 1) * G4 * 16 + (threadIdx.x & 1) * 8;
+    else xsat = (threadIdx.x >> 5) * G4 * 256 + (threadIdx.x & 31) * 8;
 
     mx_i4 W[4][2][2];                                // [step % 4][column pair][half]
     // The scalar part of an offset stays within the buffer (the range check subtracts
@@ -419,8 +425,8 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
     // read 128 bytes of a row: a whole line, where one step's 64 were half of one).
     mx_i4 X[2][XL];
     auto load_x = [&](int step, int s, int i) __attribute__((always_inline)) {     // step: the pair's first
-        if constexpr (GATED) return *reinterpret_cast<const mx_i4*>(xrow[s][i] + min(step, (G - 1) & ~1) * 64);
-        else return load16(xr, (i * 4 + wave) * G * 1024 + lane * 16, min(step + s, G - 1) * 1024);
+        if constexpr (GATED) return load16(xr, xat[s][i], min(step, (G - 1) & ~1) * 64);
+        else return load16(xr, xat[0][i], min(step + s, G - 1) * 1024);
     };
     auto store_x = [&](int stage, int s, int i, mx_i4 x) __attribute__((always_inline)) {   // stage: the pair's first
         uint8_t* to = lds + (i * 4 + wave) * kTile;
@@ -428,18 +434,24 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
         else to += (stage + s) * kStage + lane * 16;
         *reinterpret_cast<mx_i4*>(to) = x;
     };
-    int sw[2][2], sx[SUB][2], swn[2][2], sxn[SUB][2];
-    auto load_s = [&](int quad, int (&w)[2][2], int (&x)[SUB][2]) __attribute__((always_inline)) {
+    // The rows' scales: a word of four steps' bytes for each block % 4 and row, in two
+    // buffers that take turns by quads of steps.
+    uint8_t* scales = lds + 4 * kStage;
+    mx_i2 XS;
+    auto load_xs = [&](int quad) __attribute__((always_inline)) {
+        const int q = min(quad, G4 - 1);
+        return __builtin_bit_cast(mx_i2, __builtin_amdgcn_raw_buffer_load_b64(xsr, xsat, q * (GATED ? 16 : 256), 0));
+    };
+    auto store_xs = [&](int at, mx_i2 v) __attribute__((always_inline)) {
+        *reinterpret_cast<mx_i2*>(scales + at + threadIdx.x * 8) = v;
+    };
+    int sw[2][2], swn[2][2];
+    auto load_s = [&](int quad, int (&w)[2][2]) __attribute__((always_inline)) {
         const int q = min(quad, G4 - 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             w[0][h] = load4(wsr, scale_pair + h * 128, q * 256);
             w[1][h] = load4(w2sr, scale_pair + spair1 + h * 128, q * 256);
-#pragma unroll
-            for (int i = 0; i < SUB; ++i) {
-                if constexpr (GATED) x[i][h] = *reinterpret_cast<const int*>(xsrow[i] + q * 16 + h * 8);
-                else x[i][h] = load4(xsr, scale_pair + h * 128, (2 * i * G4 + q) * 256);
-            }
         }
     };
     mx_f16 acc[SUB][2] = {};
@@ -454,81 +466,93 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
                 for (int i = 0; i < SUB; ++i) acc[i][j][r] = b;
             }
     }
+    // Fragment q of a step: half q / SUB of piece q % SUB, and its scales. All first halves
+    // come before the second ones: products that add to the same sums are 2 SUB apart
+    // (two apart, the instructions alone run at 5.9 PFLOP/s, eight apart at 6.5).
+    struct Fragment { mx_i4 c; int s; };
     const uint8_t* xl = lds + (lane >> 4 & 1) * kTile + (lane >> 5) * kBlock + (lane & 15) * 16;
-    auto read = [&](int stage, int i, mx_i4 (&f)[2]) __attribute__((always_inline)) {
-        f[0] = *reinterpret_cast<const mx_i4*>(xl + stage * kStage + 2 * i * kTile);
-        f[1] = *reinterpret_cast<const mx_i4*>(xl + stage * kStage + 2 * i * kTile + 2 * kBlock);
+    const uint8_t* sl = scales + (GATED ? (lane & 31) * 16 + (lane >> 5) * 4 : (lane >> 4 & 1) * 256 + (lane >> 5) * 64 + (lane & 15) * 4);
+    auto read = [&](int stage, int at, int q) __attribute__((always_inline)) {
+        const int i = q % SUB, h = q / SUB;
+        return Fragment{*reinterpret_cast<const mx_i4*>(xl + stage * kStage + 2 * i * kTile + 2 * h * kBlock),
+                        *reinterpret_cast<const int*>(sl + at + i * 512 + h * (GATED ? 8 : 128))};
     };
     // Step g (S = g % 4): the products of group g. Even steps: rows of g + 2 and g + 3 enter
     // LDS (the barrier before step g + 1 shows them to it, which reads its successor's
-    // first pieces), those of g + 4 and g + 5 leave memory; weights of g + 3 do in each. Pieces are read two products
-    // ahead, across the step's end. The scheduling barriers keep each piece's products
-    // with its reads: left alone, the compiler moves all reads of four steps, and their
-    // waits, before the first product.
-    constexpr int kAhead = SUB < 2 ? SUB : 2;
-    mx_i4 F[kAhead][2];
+    // first pieces), those of g + 4 and g + 5 leave memory; weights of g + 2 do in each.
+    // In step 2 the next quad's scales enter LDS. Fragments are read kAhead ahead, across
+    // the step's end. The scheduling barriers keep each fragment's products with its reads:
+    // left alone, the compiler moves all reads of four steps, and their waits, before the
+    // first product.
+    constexpr int NF = 2 * SUB, kAhead = SUB < 2 ? 2 : 3;
+    Fragment F[kAhead];
+    int now = 0;                                     // the quad's scale buffer
     auto step = [&](auto phase, int g) __attribute__((always_inline)) {
         constexpr int S = decltype(phase)::value;
-        mx_i4 f[SUB + kAhead][2];
+        Fragment f[NF + kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) { f[i][0] = F[i][0]; f[i][1] = F[i][1]; }
+        for (int q = 0; q < kAhead; ++q) f[q] = F[q];
 #pragma unroll
-        for (int i = 0; i < SUB; ++i) {
-            // the step's loads are spread over its pieces: issued together by four waves
+        for (int q = 0; q < NF; ++q) {
+            // the step's loads are spread over its products: issued together by four waves
             // that just left a barrier, they hold up the products behind them
 #pragma unroll
             for (int p = 0; p < 4; ++p)
-                if (p * SUB / 4 == i) W[(S + 3) & 3][p >> 1][p & 1] = load_w(g + 3, p);
+                if (p * NF / 4 == q) W[(S + 2) & 3][p >> 1][p & 1] = load_w(g + 2, p);
             if (!(S & 1)) {
 #pragma unroll
                 for (int p = 0; p < 2 * XL; ++p)
-                    if (SUB - 1 - p * SUB / (2 * XL) == i) {
+                    if (NF - 1 - p * NF / (2 * XL) == q) {
                         store_x((S + 2) & 3, p / XL, p % XL, X[p / XL][p % XL]);
                         X[p / XL][p % XL] = load_x(g + 4, p / XL, p % XL);
                     }
             }
-            if (i + kAhead < SUB) read(S, i + kAhead, f[i + kAhead]);
-            else read((S + 1) & 3, i + kAhead - SUB, f[i + kAhead]);
+            if (S == 2 && q == 0) {
+                store_xs(now ^ kScaleBytes, XS);
+                XS = load_xs((g >> 2) + 2);
+            }
+            f[q + kAhead] = q + kAhead < NF ? read(S, now, q + kAhead)
+                                            : read((S + 1) & 3, S == 3 ? now ^ kScaleBytes : now, q + kAhead - NF);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<S>(W[S][j][h], f[i][h], acc[i][j], sw[j][h], sx[i][h]);
+            for (int j = 0; j < 2; ++j)
+                acc[q % SUB][j] = mfma32<S>(W[S][j][q / SUB], f[q].c, acc[q % SUB][j], sw[j][q / SUB], f[q].s);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) { F[i][0] = f[SUB + i][0]; F[i][1] = f[SUB + i][1]; }
+        for (int q = 0; q < kAhead; ++q) F[q] = f[NF + q];
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
     };
 #pragma unroll
     for (int p = 0; p < 2 * XL; ++p) X[p / XL][p % XL] = load_x(0, p / XL, p % XL);
+    XS = load_xs(0);
 #pragma unroll
     for (int p = 0; p < 4; ++p) W[0][p >> 1][p & 1] = load_w(0, p);
-    load_s(0, sw, sx);
+    load_s(0, sw);
 #pragma unroll
-    for (int p = 0; p < 8; ++p) W[1 + p / 4][p >> 1 & 1][p & 1] = load_w(1 + p / 4, p & 3);
+    for (int p = 0; p < 4; ++p) W[1][p >> 1][p & 1] = load_w(1, p);
 #pragma unroll
     for (int p = 0; p < 2 * XL; ++p) {
         store_x(0, p / XL, p % XL, X[p / XL][p % XL]);
         X[p / XL][p % XL] = load_x(2, p / XL, p % XL);
     }
+    store_xs(0, XS);
+    XS = load_xs(1);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) read(0, i, F[i]);
+    for (int q = 0; q < kAhead; ++q) F[q] = read(0, 0, q);
     int g = 0;
     for (; g + 4 <= G; g += 4) {
-        load_s((g >> 2) + 1, swn, sxn);
+        load_s((g >> 2) + 1, swn);
         step(Phase<0>{}, g);
         step(Phase<1>{}, g + 1);
         step(Phase<2>{}, g + 2);
         step(Phase<3>{}, g + 3);
+        now ^= kScaleBytes;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < 2; ++j) sw[j][h] = swn[j][h];
-#pragma unroll
-            for (int i = 0; i < SUB; ++i) sx[i][h] = sxn[i][h];
-        }
     }
     if (g < G) {
         step(Phase<0>{}, g);
@@ -544,8 +568,8 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
     constexpr int kPer = 16 / sizeof(T);                         // columns of a lane's 16 bytes
     constexpr int kLanes = kWaveCols / kPer;                     // lanes of a row
     constexpr int kRound = 64 / kLanes;                          // rows of a store
-    static_assert(32 * kPitch <= kBlockTiles * 1024);
-    uint8_t* tile = lds + wave * kBlockTiles * 1024;             // every wave is past the last barrier
+    static_assert(32 * kPitch <= kOutBytes);
+    uint8_t* tile = lds + wave * kOutBytes;                      // every wave is past the last barrier
     const int n = col16 * 16 + (lane & (kLanes - 1)) * kPer;
     const int rows = min(n16 * 16, a.M - rt0 * 16);
     T* y = static_cast<T*>(a.y) + static_cast<int64_t>(rt0) * 16 * a.ldy;
@@ -613,8 +637,10 @@ __device__ inline void zero_rows(const MxGemmArgs& a, int rt0, int n16, int n0, 
 // dies in turn, so each die takes a run of neighbouring tiles: they share rows and
 // weights in its L2.
 template <typename T, bool GATED>
-__global__ __launch_bounds__(256) void k_mx_wide(MxGemmArgs a, int blocks, int block_tiles) {
-    __shared__ __align__(16) uint8_t lds[4 * kBlockTiles * (GATED ? 1280 : 1024) + (GATED ? 64 : 0)];
+__global__ __launch_bounds__(256, 2) void k_mx_wide(MxGemmArgs a, int blocks, int block_tiles) {
+    constexpr int kStages = 4 * kBlockTiles * (GATED ? 1280 : 1024) + (GATED ? 64 : 0) + 2 * kScaleBytes;
+    static_assert(kStages >= 4 * kOutBytes);
+    __shared__ __align__(16) uint8_t lds[kStages];
     constexpr int kCols = GATED ? 128 : 256;
     const int ncol = (a.N + kCols - 1) / kCols;
     const int count = a.tiles ? a.tiles[0] : blocks;
@@ -642,9 +668,7 @@ __global__ __launch_bounds__(256) void k_mx_wide(MxGemmArgs a, int blocks, int b
         case 1: wide_tile<T, 1, GATED>(a, lds, rt0, n16, e, col16); break;
         case 2: wide_tile<T, 2, GATED>(a, lds, rt0, n16, e, col16); break;
         case 3: wide_tile<T, 3, GATED>(a, lds, rt0, n16, e, col16); break;
-        case 4: wide_tile<T, 4, GATED>(a, lds, rt0, n16, e, col16); break;
-        case 5: wide_tile<T, 5, GATED>(a, lds, rt0, n16, e, col16); break;
-        default: wide_tile<T, 6, GATED>(a, lds, rt0, n16, e, col16); break;
+        default: wide_tile<T, 4, GATED>(a, lds, rt0, n16, e, col16); break;
     }
 }
 
@@ -743,7 +767,7 @@ hipError_t wide(const MxGemmArgs& a, hipStream_t st) {
     const int64_t ncol = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
     int blocks = 0, block_tiles = 0;
     if (!a.tiles) {
-        block_tiles = 2 * wide_pieces((rt + 1) / 2, 0, ncol, a.K, nullptr);
+        block_tiles = 2 * wide_pieces((rt + 1) / 2, ncol, a.K, nullptr);
         blocks = (rt + block_tiles - 1) / block_tiles;
     }
     const int64_t n = a.tiles ? tiles_cap(a.M, a.E) : blocks;
@@ -770,7 +794,7 @@ int mx_plan(int64_t M, int64_t N, int64_t K) {
     for (int i = 1; i < 3; ++i)
         if (cost[i] < cost[best]) best = i;
     double wide;
-    wide_pieces(static_cast<int64_t>(rows32), 0, (N + 255) / 256, K, &wide);
+    wide_pieces(static_cast<int64_t>(rows32), (N + 255) / 256, K, &wide);
     return cost[best] < wide && rows32 <= 65535 ? best : kMxWide;
 }
 
