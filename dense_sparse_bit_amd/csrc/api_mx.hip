@@ -83,6 +83,10 @@ mq::MxQuantArgs rows_of(const void* x, int dtype, int64_t R, int64_t stride, int
     return a;
 }
 
+mq::MxTilesArgs blocks_of(const int32_t* offsets, int64_t E, int64_t P, int32_t* tiles) {
+    return {offsets, static_cast<int>(E), static_cast<int>(P / 16), tiles, static_cast<int>(mq::mx_tiles_cap(P, E))};
+}
+
 size_t row_bytes(int64_t R, int64_t K) {
     return round16(mq::mx_row_codes_size(R, K)) + round16(mq::mx_row_scales_size(R, K));
 }
@@ -290,8 +294,8 @@ int mq_mx_experts_up(const void* x, int x_dtype, int64_t stride_t, int64_t T, in
     a.tiles = reinterpret_cast<int32_t*>(xs + round16(mq::mx_row_scales_size(T, D)));
     mq::MxQuantArgs q = rows_of(x, x_dtype, T, stride_t, D, xq, xs);
     q.by_row = true;
+    q.plan = blocks_of(offsets, E, P, a.tiles);
     if (mq::launch_mx_quant(q, st) != hipSuccess) return MQ_ERR_HIP;
-    if (mq::launch_mx_tiles(offsets, a.E, P, a.tiles, st) != hipSuccess) return MQ_ERR_HIP;
     return status_of(mq::launch_mx_wide(a, st));
 }
 
@@ -344,8 +348,9 @@ int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t
         a.xq = hq;
         a.xs = hs;
         a.tiles = reinterpret_cast<int32_t*>(hs + round16(mq::mx_scales_size(P, I)));
-        if (mq::launch_mx_quant(rows_of(h, h_dtype, P, I, I, hq, hs), st) != hipSuccess) return MQ_ERR_HIP;
-        if (mq::launch_mx_tiles(offsets, a.E, P, a.tiles, st) != hipSuccess) return MQ_ERR_HIP;
+        mq::MxQuantArgs q = rows_of(h, h_dtype, P, I, I, hq, hs);
+        q.plan = blocks_of(offsets, E, P, a.tiles);
+        if (mq::launch_mx_quant(q, st) != hipSuccess) return MQ_ERR_HIP;
     }
     for (int64_t d = 0; d < D; d += step) {
         a.N = static_cast<int>(D - d < step ? D - d : step);

@@ -324,8 +324,7 @@ hipError_t down_few(const MxGemmArgs& a, const int32_t* row_of, const float* wei
 
 // ------------------------------------------------------------------- many rows
 template <int S> struct Phase { static constexpr int value = S; };
-constexpr int kMaxSub = 4;                    // 32-row pieces of a row block
-constexpr int kBlockTiles = 2 * kMaxSub;      // its 16-row tiles
+constexpr int kMaxSub = kBlockTiles / 2;      // 32-row pieces of a row block
 constexpr int kScaleBytes = 512 * kMaxSub;    // its rows' scales for four steps
 constexpr int kOutBytes = 32 * (64 * 4 + 16); // a wave's results on their way out: 32 rows, 16 B apart in the banks
 
@@ -672,54 +671,6 @@ __global__ __launch_bounds__(256, 2) void k_mx_wide(MxGemmArgs a, int blocks, in
     }
 }
 
-// Row blocks of a plan: each expert's rows in blocks of at most kBlockTiles 16-row
-// tiles, of even sizes; then the rows after the last expert's, with expert -1.
-// tiles: [0] their number, then (expert, first 16-row tile, 16-row tiles, 0) each.
-__global__ __launch_bounds__(1024) void k_mx_tiles(const int32_t* offsets, int E, int P16, int32_t* tiles, int cap) {
-    __shared__ int last[1024 + 1];             // blocks up to and with expert e
-    __shared__ int wave_sum[16];
-    const int tid = threadIdx.x, lane = tid & 63;
-    int from = 0, to = 0;
-    if (tid <= E) {
-        from = min(max(offsets[tid] >> 4, 0), P16);
-        to = tid < E ? min(max(offsets[tid + 1] >> 4, 0), P16) : P16;
-    }
-    int n = to > from ? (to - from + kBlockTiles - 1) / kBlockTiles : 0;
-    for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(n, o);
-        if (lane >= o) n += v;
-    }
-    if (lane == 63) wave_sum[tid >> 6] = n;
-    __syncthreads();
-    for (int w = 0; w < (tid >> 6); ++w) n += wave_sum[w];
-    last[tid] = n;
-    // E = 1024: the rows after the last expert's have no thread of their own
-    if (tid == 1023) {
-        const int rest = E == 1024 ? max(0, P16 - min(max(offsets[1024] >> 4, 0), P16)) : 0;
-        last[1024] = n + (rest + kBlockTiles - 1) / kBlockTiles;
-    }
-    __syncthreads();
-    const int count = min(last[1024], cap);
-    if (tid == 0) tiles[0] = count;
-    for (int i = tid; i < count; i += 1024) {
-        int lo = 0, hi = 1024;                  // first e with last[e] > i
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (last[mid] > i) hi = mid; else lo = mid + 1;
-        }
-        const int f = min(max(offsets[lo] >> 4, 0), P16);
-        const int l = lo < E ? min(max(offsets[lo + 1] >> 4, 0), P16) : P16;
-        const int c = l - f, before = lo ? last[lo - 1] : 0;
-        const int parts = (c + kBlockTiles - 1) / kBlockTiles, j = i - before;
-        // pieces of 32 rows are whole; the parts differ by one piece at most
-        const int pieces = (c + 1) / 2;
-        const int p0 = static_cast<int>(static_cast<int64_t>(pieces) * j / parts);
-        const int p1 = static_cast<int>(static_cast<int64_t>(pieces) * (j + 1) / parts);
-        int4* at = reinterpret_cast<int4*>(tiles + 4 + 4 * i);
-        *at = make_int4(lo < E ? lo : -1, f + 2 * p0, min(2 * p1, c) - 2 * p0, 0);
-    }
-}
-
 // y[t][d0 + d] = sum over j of weights[t][j] * rows[row_of[t][j]][d], d < cols. Four columns
 // a thread; a token's rows are read eight at a time.
 template <typename T>
@@ -758,8 +709,6 @@ hipError_t combine(const float* rows, int64_t n_rows, const int32_t* row_of, con
     return hipGetLastError();
 }
 
-int64_t tiles_cap(int64_t P, int64_t E) { return P / 16 / kBlockTiles + E + 2; }
-
 template <typename T>
 hipError_t wide(const MxGemmArgs& a, hipStream_t st) {
     const int rt = (a.M + 15) / 16;
@@ -770,7 +719,7 @@ hipError_t wide(const MxGemmArgs& a, hipStream_t st) {
         block_tiles = 2 * wide_pieces((rt + 1) / 2, ncol, a.K, nullptr);
         blocks = (rt + block_tiles - 1) / block_tiles;
     }
-    const int64_t n = a.tiles ? tiles_cap(a.M, a.E) : blocks;
+    const int64_t n = a.tiles ? mx_tiles_cap(a.M, a.E) : blocks;
     const int64_t want = (n * ncol + 7) / 8 * 8;
     if (want >= int64_t(1) << 24) return hipErrorInvalidConfiguration;       // a grid holds 2^32 threads
     const unsigned grid = static_cast<unsigned>(want);
@@ -830,13 +779,6 @@ hipError_t launch_mx_wide(const MxGemmArgs& a, hipStream_t st) {
         case MQ_BF16: return wide<__bf16>(a, st);
         default: return wide<_Float16>(a, st);
     }
-}
-
-int64_t mx_tiles_size(int64_t P, int64_t E) { return 4 + 4 * tiles_cap(P, E); }
-
-hipError_t launch_mx_tiles(const int32_t* offsets, int E, int64_t P, int32_t* tiles, hipStream_t st) {
-    k_mx_tiles<<<1, 1024, 0, st>>>(offsets, E, static_cast<int>(P / 16), tiles, static_cast<int>(tiles_cap(P, E)));
-    return hipGetLastError();
 }
 
 hipError_t launch_combine(const float* rows, int64_t n_rows, const int32_t* row_of, const float* weights, int64_t T,

@@ -29,6 +29,20 @@ inline int64_t plan_rows(int64_t T, int64_t k, int64_t E) {
 inline int64_t mx_row_codes_size(int64_t R, int64_t K) { return R * ((mx_groups(K) + 1) / 2) * 128; }
 inline int64_t mx_row_scales_size(int64_t R, int64_t K) { return R * mx_quads(K) * 16; }
 
+// Row blocks of an expert plan, for launch_mx_wide: each expert's rows in blocks of at most
+// kBlockTiles 16-row tiles, of even sizes; then the rows after the last expert's, with
+// expert -1. tiles: [0] their number, then (expert, first 16-row tile, 16-row tiles, 0)
+// each.
+constexpr int kBlockTiles = 8;
+inline int64_t mx_tiles_cap(int64_t P, int64_t E) { return P / 16 / kBlockTiles + E + 2; }
+inline int64_t mx_tiles_size(int64_t P, int64_t E) { return 4 + 4 * mx_tiles_cap(P, E); }
+struct MxTilesArgs {
+    const int32_t* offsets;          // of a plan of P16 16-row tiles; null: no tiles are wanted
+    int E, P16;
+    int32_t* tiles;
+    int cap;
+};
+
 // x[b][r][c] of a strided matrix, as it is read by the quantizer. by_row (B = 1): the
 // row by row layout.
 struct MxQuantArgs {
@@ -39,6 +53,7 @@ struct MxQuantArgs {
     bool by_row;
     uint8_t* codes;
     uint8_t* scales;
+    MxTilesArgs plan;                // row blocks that the launch makes too
 };
 
 // Y = X W^T over microscaled operands. Dense: M x N outputs. With offsets (expert
@@ -59,7 +74,7 @@ struct MxGemmArgs {
     const int32_t* offsets;
     const int32_t* row_token;        // x's row of each of the plan's rows (x given), and which rows are live
     int E, T;
-    int32_t* tiles;                  // row blocks of the plan (launch_mx_tiles)
+    int32_t* tiles;                  // row blocks of the plan (MxTilesArgs)
 };
 
 struct RouteArgs {
@@ -96,9 +111,6 @@ hipError_t launch_mx_few(const MxGemmArgs& a, int plan, hipStream_t st);
 hipError_t launch_mx_down_few(const MxGemmArgs& a, const int32_t* row_of, const float* weights, int k, int64_t P,
                               hipStream_t st);
 hipError_t launch_mx_wide(const MxGemmArgs& a, hipStream_t st);
-// Row blocks of a plan of P rows, for launch_mx_wide; entries of `tiles`.
-int64_t mx_tiles_size(int64_t P, int64_t E);
-hipError_t launch_mx_tiles(const int32_t* offsets, int E, int64_t P, int32_t* tiles, hipStream_t st);
 hipError_t launch_route(const RouteArgs& a, hipStream_t st);
 hipError_t launch_plan(const PlanArgs& a, hipStream_t st);
 // y[t][d0 + d] = sum over j of weights[t][j] * rows[row_of[t][j]][d], d < cols (fp32 rows,

@@ -11,6 +11,54 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Row blocks of a plan (mx_internal.h), by one workgroup: thread t counts the blocks of the
+// entries 4t .. 4t + 3 (experts, and one for the rows after the last's), whose sums give
+// each entry its place. It goes with the quantization of the rows, which takes longer:
+// a launch of its own took 5 us.
+constexpr int kTilesLds = 1024 + kThreads / 64 + 1;
+__device__ void mx_tiles(const MxTilesArgs& p, int* lds) {
+    int* const last = lds;                     // blocks up to and with entry i; then waves' sums
+    const int tid = threadIdx.x, lane = tid & 63;
+    auto start = [&](int e) { return min(max(p.offsets[e] >> 4, 0), p.P16); };
+    auto end = [&](int e) { return e < p.E ? start(e + 1) : p.P16; };
+    int n[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = 4 * tid + i, c = e <= p.E ? end(e) - start(e) : 0;
+        n[i] = sum += c > 0 ? (c + kBlockTiles - 1) / kBlockTiles : 0;
+    }
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 63) lds[1024 + (tid >> 6)] = sum;
+    __syncthreads();
+    sum -= n[3];
+    for (int w = 0; w < (tid >> 6); ++w) sum += lds[1024 + w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) last[4 * tid + i] = sum + n[i];
+    __syncthreads();
+    // 1024 experts: the rows after the last one's have no thread of their own
+    const int rest = p.E == 1024 ? p.P16 - start(1024) : 0;
+    const int experts = last[1023], count = min(experts + (rest + kBlockTiles - 1) / kBlockTiles, p.cap);
+    if (tid == 0) p.tiles[0] = count;
+    for (int i = tid; i < count; i += kThreads) {
+        int lo = 0, hi = 1024;                  // first e with last[e] > i
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (last[mid] > i) hi = mid; else lo = mid + 1;
+        }
+        const int f = start(lo), c = end(lo) - f, before = lo ? last[lo - 1] : 0;
+        const int parts = (c + kBlockTiles - 1) / kBlockTiles, j = i - before;
+        // pieces of 32 rows are whole; the parts differ by one piece at most
+        const int pieces = (c + 1) / 2;
+        const int p0 = static_cast<int>(static_cast<int64_t>(pieces) * j / parts);
+        const int p1 = static_cast<int>(static_cast<int64_t>(pieces) * (j + 1) / parts);
+        *reinterpret_cast<int4*>(p.tiles + 4 + 4 * i) = make_int4(lo < p.E ? lo : -1, f + 2 * p0, min(2 * p1, c) - 2 * p0, 0);
+    }
+    __syncthreads();
+}
+
 // One workgroup: 16 rows x 512 inputs (four code tiles, one scale entry per lane).
 // Wave w reads rows 4w .. 4w + 3, 1 KB of bf16 at a time; lane l holds inputs
 // 8l .. 8l + 7, four lanes a block. Codes and scales go through LDS, because a tile
@@ -18,7 +66,7 @@ constexpr int kThreads = 256;
 // 256 B runs.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t stride_b, int64_t R, int64_t stride_r, int K,
-                                                       uint8_t* codes, uint8_t* scales) {
+                                                       uint8_t* codes, uint8_t* scales, MxTilesArgs plan) {
     constexpr int kRun = 16 * 4 + 4;                // words of a block's 16 rows, and 4 more: other banks
     __shared__ __align__(16) uint32_t lds_codes[16 * kRun];
     __shared__ uint8_t lds_scales[256];
@@ -28,6 +76,8 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t strid
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int k0 = q * 512 + 8 * lane;
     const int64_t b = blockIdx.z;
+    static_assert(16 * kRun >= kTilesLds);
+    if (plan.offsets && (blockIdx.x | blockIdx.y) == 0) mx_tiles(plan, reinterpret_cast<int*>(lds_codes));
     for (int64_t rt = blockIdx.y; rt < RT; rt += gridDim.y) {
         MxRaw8<T> v[4];
 #pragma unroll
@@ -60,7 +110,9 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t strid
 constexpr int kRows = 4;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_mx_quant_rows(const T* x, int64_t R, int64_t stride_r, int K, uint8_t* codes,
-                                                            uint8_t* scales) {
+                                                            uint8_t* scales, MxTilesArgs plan) {
+    __shared__ int lds[kTilesLds];
+    if (plan.offsets && (blockIdx.x | blockIdx.y) == 0) mx_tiles(plan, lds);
     const int G = (K + 127) / 128, G2 = (G + 1) / 2, G4 = (G + 3) / 4;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * kRows;
@@ -144,10 +196,10 @@ hipError_t quant(const MxQuantArgs& a, hipStream_t st) {
     const T* x = static_cast<const T*>(a.x);
     if (a.by_row) {
         const dim3 grid(static_cast<unsigned>((a.R + 4 * kRows - 1) / (4 * kRows)), quads);
-        k_mx_quant_rows<T><<<grid, kThreads, 0, st>>>(x, a.R, a.stride_r, a.K, a.codes, a.scales);
+        k_mx_quant_rows<T><<<grid, kThreads, 0, st>>>(x, a.R, a.stride_r, a.K, a.codes, a.scales, a.plan);
     } else {
         const dim3 grid(quads, static_cast<unsigned>(RT < 32768 ? RT : 32768), static_cast<unsigned>(a.B));
-        k_mx_quant<T><<<grid, kThreads, 0, st>>>(x, a.stride_b, a.R, a.stride_r, a.K, a.codes, a.scales);
+        k_mx_quant<T><<<grid, kThreads, 0, st>>>(x, a.stride_b, a.R, a.stride_r, a.K, a.codes, a.scales, a.plan);
     }
     return hipGetLastError();
 }
