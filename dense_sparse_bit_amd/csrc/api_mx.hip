@@ -92,9 +92,10 @@ size_t row_bytes(int64_t R, int64_t K) {
 }
 
 // Whether a product quantizes its rows on the way. It saves a launch (about 3 us) and
-// costs each workgroup the whole matrix of rows: at 16 rows and K = 4096 both ways take
-// 6.5 us, at K = 14336 18 against 12 us.
-bool on_the_way(int64_t M, int64_t K) { return M <= 16 && M * K <= 1 << 17; }
+// costs each workgroup the whole matrix of rows. Measured, on the way / apart, in us:
+// 16 rows, 4096 x 4096: 6.9 / 7.6, N = 14336: 13.2 / 13.8, N = 4096, K = 14336: 20 / 14.8;
+// N = 28672, K = 8192: 8 rows 28.8 / 31.9, 16 rows 37 / 31.7.
+bool on_the_way(int64_t M, int64_t N, int64_t K) { return M <= 16 && M * K <= 1 << 17 && M * K <= (int64_t(1) << 31) / N; }
 
 hipError_t launch_product(const mq::MxGemmArgs& a, hipStream_t st) {
     const int plan = mq::mx_plan(a.M, a.N, a.K);
@@ -167,7 +168,7 @@ int mq_mx_gemm(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const ui
 }
 
 size_t mq_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    return check_product(M, N, K) || on_the_way(M, K) ? 0 : mx_bytes(M, K);
+    return check_product(M, N, K) || on_the_way(M, N, K) ? 0 : mx_bytes(M, K);
 }
 
 int mq_mx_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* wq, const uint8_t* ws, int64_t M,
@@ -182,7 +183,7 @@ int mq_mx_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* wq
     const hipStream_t st = static_cast<hipStream_t>(stream);
     mq::MxGemmArgs a = product(nullptr, nullptr, wq, ws, M, N, K, y, y_dtype);
     a.bias = bias;
-    if (on_the_way(M, K)) {
+    if (on_the_way(M, N, K)) {
         a.x = x;
         a.x_dtype = x_dtype;
         a.stride_x = stride_m;
