@@ -307,6 +307,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     } catch (const No&) {
     } catch (const std::exception&) {              // no device, no memory: the long way says so
     }
+    PyErr_Clear();                                 // an operand's own error: the long way meets it again
     Py_RETURN_NONE;
 }
 

@@ -208,6 +208,33 @@ def test_rows_beyond_32_bit_offsets_are_refused():
 
 
 @pytest.mark.gpu
+def test_refusals_on_the_device(mq):
+    """Every refusal has its own error, an operand's included, and launches nothing."""
+    import torch
+    x = torch.randn(4, 64, device="cuda")
+    w = mq.mx_quantize(torch.randn(20, 64, device="cuda"))
+    ids, _ = mq.route(x, 2)
+    plan = mq.expert_plan(ids, 64)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        mq.route(x, 2, renormalize=torch.zeros(2))
+    for error, call in (
+            (ValueError, lambda: mq.route(x, 65)), (ValueError, lambda: mq.route(x, 2, score="sum")),
+            (ValueError, lambda: mq.route(x, 2, bias=torch.zeros(63, device="cuda"))),
+            (TypeError, lambda: mq.route(x.double(), 2)), (ValueError, lambda: mq.route(x.t(), 2)),
+            (mq.MQError, lambda: mq.route(x, 40)), (ValueError, lambda: mq.expert_plan(ids.long(), 64)),
+            (ValueError, lambda: mq.expert_plan(ids, 0)), (ValueError, lambda: mq.expert_plan(ids.t(), 64)),
+            (TypeError, lambda: mq.mx_quantize(x.double())), (ValueError, lambda: mq.mx_quantize(x.t())),
+            (ValueError, lambda: mq.mx_quantize(x[:, :0])), (ValueError, lambda: mq.mx_linear(x[:, :63], w)),
+            (ValueError, lambda: mq.mx_linear(x.cpu(), w)), (TypeError, lambda: mq.mx_linear(x, w, out_dtype=torch.int8)),
+            (ValueError, lambda: mq.mx_linear(x, w, y=torch.empty(4, 19, device="cuda"))),
+            (ValueError, lambda: mq.mx_linear(x, w._replace(rows=40))), (TypeError, lambda: mq.mx_dequantize(x)),
+            (TypeError, lambda: mq.mx_experts_up(x, w, w, ids)), (ValueError, lambda: mq.mx_experts_up(x, w, w, plan))):
+        with pytest.raises(error):
+            call()
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
 def test_example():
     """The layer against plain fp32 over the same quantized values: bf16 rounds h before its
     second quantization, where a change of half a step can move a code by one; the result is
