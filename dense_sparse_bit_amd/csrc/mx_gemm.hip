@@ -325,7 +325,11 @@ hipError_t down_few(const MxGemmArgs& a, const int32_t* row_of, const float* wei
 // ------------------------------------------------------------------- many rows
 template <int S> struct Phase { static constexpr int value = S; };
 constexpr int kMaxSub = kBlockTiles / 2;      // 32-row pieces of a row block
-constexpr int kScaleBytes = 512 * kMaxSub;    // its rows' scales for four steps
+// Its rows' scales for four steps: words of four bytes, one for each block % 4 and row;
+// blocks are a row block and 32 words apart, so that neighbouring rows' words, and with
+// them two blocks', lie in different banks.
+constexpr int kScaleBlock = 128 * kMaxSub + 128;
+constexpr int kScaleBytes = 4 * kScaleBlock;
 constexpr int kOutBytes = 32 * (64 * 4 + 16); // a wave's results on their way out: 32 rows, 16 B apart in the banks
 
 __device__ inline __amdgpu_buffer_rsrc_t buffer(const void* base, int64_t bytes) {
@@ -433,16 +437,23 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
         else to += (stage + s) * kStage + lane * 16;
         *reinterpret_cast<mx_i4*>(to) = x;
     };
-    // The rows' scales: a word of four steps' bytes for each block % 4 and row, in two
-    // buffers that take turns by quads of steps.
+    // The rows' scales, in two buffers that take turns by quads of steps. A thread brings two
+    // words: two rows' of one block (GATED: two blocks' of one row).
     uint8_t* scales = lds + 4 * kStage;
     mx_i2 XS;
     auto load_xs = [&](int quad) __attribute__((always_inline)) {
         const int q = min(quad, G4 - 1);
         return __builtin_bit_cast(mx_i2, __builtin_amdgcn_raw_buffer_load_b64(xsr, xsat, q * (GATED ? 16 : 256), 0));
     };
+    uint8_t* const scales_to = scales + (GATED ? (threadIdx.x & 1) * 2 * kScaleBlock + (threadIdx.x >> 1) * 4
+                                               : (threadIdx.x >> 3 & 3) * kScaleBlock + (threadIdx.x >> 5) * 64 + (threadIdx.x & 7) * 8);
     auto store_xs = [&](int at, mx_i2 v) __attribute__((always_inline)) {
-        *reinterpret_cast<mx_i2*>(scales + at + threadIdx.x * 8) = v;
+        if constexpr (GATED) {
+            *reinterpret_cast<int*>(scales_to + at) = v[0];
+            *reinterpret_cast<int*>(scales_to + at + kScaleBlock) = v[1];
+        } else {
+            *reinterpret_cast<mx_i2*>(scales_to + at) = v;
+        }
     };
     int sw[2][2], swn[2][2];
     auto load_s = [&](int quad, int (&w)[2][2]) __attribute__((always_inline)) {
@@ -470,11 +481,11 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
     // (two apart, the instructions alone run at 5.9 PFLOP/s, eight apart at 6.5).
     struct Fragment { mx_i4 c; int s; };
     const uint8_t* xl = lds + (lane >> 4 & 1) * kTile + (lane >> 5) * kBlock + (lane & 15) * 16;
-    const uint8_t* sl = scales + (GATED ? (lane & 31) * 16 + (lane >> 5) * 4 : (lane >> 4 & 1) * 256 + (lane >> 5) * 64 + (lane & 15) * 4);
+    const uint8_t* sl = scales + (lane >> 5) * kScaleBlock + (lane & 31) * 4;
     auto read = [&](int stage, int at, int q) __attribute__((always_inline)) {
         const int i = q % SUB, h = q / SUB;
         return Fragment{*reinterpret_cast<const mx_i4*>(xl + stage * kStage + 2 * i * kTile + 2 * h * kBlock),
-                        *reinterpret_cast<const int*>(sl + at + i * 512 + h * (GATED ? 8 : 128))};
+                        *reinterpret_cast<const int*>(sl + at + i * 128 + h * 2 * kScaleBlock)};
     };
     // Step g (S = g % 4): the products of group g. Even steps: rows of g + 2 and g + 3 enter
     // LDS (the barrier before step g + 1 shows them to it, which reads its successor's
