@@ -13,8 +13,8 @@ constexpr int kThreads = 256;
 
 // Row blocks of a plan (mx_internal.h), by one workgroup: thread t counts the blocks of the
 // entries 4t .. 4t + 3 (experts, and one for the rows after the last's), whose sums give
-// each entry its place. It goes with the quantization of the rows, which takes longer:
-// a launch of its own took 5 us.
+// each entry its place. It goes with the quantization of the rows, which takes longer: a
+// launch of its own took 5 us.
 constexpr int kTilesLds = 1024 + kThreads / 64 + 1;
 __device__ void mx_tiles(const MxTilesArgs& p, int* lds) {
     int* const last = lds;                     // blocks up to and with entry i; then waves' sums
@@ -77,8 +77,12 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant(const T* x, int64_t strid
     const int k0 = q * 512 + 8 * lane;
     const int64_t b = blockIdx.z;
     static_assert(16 * kRun >= kTilesLds);
-    if (plan.offsets && (blockIdx.x | blockIdx.y) == 0) mx_tiles(plan, reinterpret_cast<int*>(lds_codes));
-    for (int64_t rt = blockIdx.y; rt < RT; rt += gridDim.y) {
+    const int first = plan.offsets ? 1 : 0;         // workgroups (0, 0): the plan's row blocks alone
+    if (static_cast<int>(blockIdx.y) < first) {
+        if (blockIdx.x == 0) mx_tiles(plan, reinterpret_cast<int*>(lds_codes));
+        return;
+    }
+    for (int64_t rt = blockIdx.y - first; rt < RT; rt += gridDim.y - first) {
         MxRaw8<T> v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -112,10 +116,14 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void k_mx_quant_rows(const T* x, int64_t R, int64_t stride_r, int K, uint8_t* codes,
                                                             uint8_t* scales, MxTilesArgs plan) {
     __shared__ int lds[kTilesLds];
-    if (plan.offsets && (blockIdx.x | blockIdx.y) == 0) mx_tiles(plan, lds);
+    const int first = plan.offsets ? 1 : 0;         // workgroups (0, 0): the plan's row blocks alone
+    if (static_cast<int>(blockIdx.x) < first) {
+        if (blockIdx.y == 0) mx_tiles(plan, lds);
+        return;
+    }
     const int G = (K + 127) / 128, G2 = (G + 1) / 2, G4 = (G + 3) / 4;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * kRows;
+    const int64_t r0 = (static_cast<int64_t>(blockIdx.x - first) * 4 + wave) * kRows;
     const int q = blockIdx.y, k0 = q * 512 + 8 * lane;
     MxRaw8<T> v[kRows];
 #pragma unroll
@@ -194,11 +202,12 @@ hipError_t quant(const MxQuantArgs& a, hipStream_t st) {
     const int64_t RT = mx_row_tiles(a.R);
     const int quads = static_cast<int>(mx_quads(a.K));
     const T* x = static_cast<const T*>(a.x);
+    const unsigned first = a.plan.offsets ? 1 : 0;     // workgroups for the plan's row blocks
     if (a.by_row) {
-        const dim3 grid(static_cast<unsigned>((a.R + 4 * kRows - 1) / (4 * kRows)), quads);
+        const dim3 grid(static_cast<unsigned>((a.R + 4 * kRows - 1) / (4 * kRows)) + first, quads);
         k_mx_quant_rows<T><<<grid, kThreads, 0, st>>>(x, a.R, a.stride_r, a.K, a.codes, a.scales, a.plan);
     } else {
-        const dim3 grid(quads, static_cast<unsigned>(RT < 32768 ? RT : 32768), static_cast<unsigned>(a.B));
+        const dim3 grid(quads, static_cast<unsigned>(RT < 32768 ? RT : 32768) + first, static_cast<unsigned>(a.B));
         k_mx_quant<T><<<grid, kThreads, 0, st>>>(x, a.stride_b, a.R, a.stride_r, a.K, a.codes, a.scales, a.plan);
     }
     return hipGetLastError();
