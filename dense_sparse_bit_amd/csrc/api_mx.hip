@@ -102,12 +102,20 @@ hipError_t launch_product(const mq::MxGemmArgs& a, hipStream_t st) {
     return plan == mq::kMxWide ? mq::launch_mx_wide(a, st) : mq::launch_mx_few(a, plan, st);
 }
 
-// Whether the experts of a batch meet few rows each: at most two row tiles.
-bool few_tokens(int64_t T, int64_t k) { return T <= 32 && k <= 1024; }
-// Whether the down products go token by token.
+// Whether the up products split K, quantizing on the way, instead of taking tiles of many
+// rows. Measured, split / tiles, in us: 64 experts of 4096 x 1024, 8 a token: 1 token 6.8 /
+// 16.3, 8 30.7 / 32.6, 16 30.7 / 32.9, 24 38.1 / 35.5; 8 experts of 4096 x 4096, 2 a token:
+// 1 token 6.7 / 15.5, 16 24.9 / 24.8, 24 29.7 / 26.7.
+bool few_tokens(int64_t T, int64_t k) { return T <= 16 && k <= 1024; }
+// Whether the down products go token by token. As above, by token / tiles: 1 token 6.0 /
+// 13.5, 4 13.8 / 20.3, 8 25.1 / 25.1, 16 44.3 / 25.3; 5.3 / 15.3, 14.2 / 18.7, 21.2 / 18.6,
+// 37.8 / 19.4; 128 experts of 2048 x 768, 8 a token: 5.8 / 12.5, 8.0 / 13.2, 13.5 / 15.9,
+// 24.2 / 20.1.
 bool one_by_one(int64_t T, int64_t k) { return T <= 8 && k <= 32; }
-// Columns of the down products that are made, and summed, at a time: even parts of at
-// most kDownBytes of fp32 rows.
+// Columns of the down products that are made, and summed, at a time: even parts of at most
+// kDownBytes of fp32 rows, which the last-level cache (256 MB) holds. Measured (4096 tokens,
+// 8 of 64 experts, 4096 columns), in us: parts of 50 MB 378, 100 344, 140 316, 200 317,
+// 300 328, all at once 340.
 constexpr int64_t kDownBytes = int64_t(200) << 20;
 int64_t down_cols(int64_t P, int64_t D) {
     const int64_t parts = (P * D * 4 + kDownBytes - 1) / kDownBytes;
@@ -304,7 +312,7 @@ size_t mq_mx_experts_down_workspace_bytes(int64_t T, int64_t k, int64_t E, int64
     if (check_slots(T, k, E) || check_product(T * k, D, I) || one_by_one(T, k)) return 0;
     const int64_t P = mq::plan_rows(T, k, E);
     const size_t rows = round16(P * down_cols(P, D) * 4);
-    return few_tokens(T, k) ? rows : rows + mx_bytes(P, I) + tiles_bytes(P, E);
+    return rows + mx_bytes(P, I) + tiles_bytes(P, E);
 }
 
 int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t E, int64_t D, int64_t I,
@@ -338,25 +346,18 @@ int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t
     a.E = static_cast<int>(E);
     a.T = static_cast<int>(T);
     a.ldy = static_cast<int>(step);
-    const bool few = few_tokens(T, k);
-    if (few) {
-        a.x = h;
-        a.x_dtype = h_dtype;
-        a.stride_x = I;
-    } else {
-        uint8_t* hq = static_cast<uint8_t*>(workspace) + round16(P * step * 4);
-        uint8_t* hs = hq + round16(mq::mx_codes_size(P, I));
-        a.xq = hq;
-        a.xs = hs;
-        a.tiles = reinterpret_cast<int32_t*>(hs + round16(mq::mx_scales_size(P, I)));
-        mq::MxQuantArgs q = rows_of(h, h_dtype, P, I, I, hq, hs);
-        q.plan = blocks_of(offsets, E, P, a.tiles);
-        if (mq::launch_mx_quant(q, st) != hipSuccess) return MQ_ERR_HIP;
-    }
+    uint8_t* hq = static_cast<uint8_t*>(workspace) + round16(P * step * 4);
+    uint8_t* hs = hq + round16(mq::mx_codes_size(P, I));
+    a.xq = hq;
+    a.xs = hs;
+    a.tiles = reinterpret_cast<int32_t*>(hs + round16(mq::mx_scales_size(P, I)));
+    mq::MxQuantArgs q = rows_of(h, h_dtype, P, I, I, hq, hs);
+    q.plan = blocks_of(offsets, E, P, a.tiles);
+    if (mq::launch_mx_quant(q, st) != hipSuccess) return MQ_ERR_HIP;
     for (int64_t d = 0; d < D; d += step) {
         a.N = static_cast<int>(D - d < step ? D - d : step);
         a.w_tile0 = static_cast<int>(d / 16);
-        if ((few ? mq::launch_mx_few(a, mq::kMxOneTile, st) : mq::launch_mx_wide(a, st)) != hipSuccess) return MQ_ERR_HIP;
+        if (mq::launch_mx_wide(a, st) != hipSuccess) return MQ_ERR_HIP;
         if (mq::launch_combine(rows, P, row_of, weights, T, static_cast<int>(k), static_cast<int>(step), a.N, d, D, y, y_dtype,
                                st) != hipSuccess)
             return MQ_ERR_HIP;

@@ -169,9 +169,9 @@ __global__ __launch_bounds__(512) void k_mx_few(MxGemmArgs a) {
     const int row0 = blockIdx.y * 16 * MT, ct = blockIdx.x * NC;
     int rows = min(16 * MT, a.M - row0), e = 0, token = 0;
     uint64_t alive = ~0ull;                            // which of the rows have a token
-    if (a.offsets) {
+    if constexpr (GATED) {
         // (MT = 1) lane l % 16 is row l % 16 of the plan's tile
-        token = a.row_token ? a.row_token[row0 + (lane & 15)] : 0;
+        token = a.row_token[row0 + (lane & 15)];
         alive = __ballot(static_cast<unsigned>(token) < static_cast<unsigned>(a.T)) & 0xffff;
         e = __builtin_amdgcn_readfirstlane(expert_of(a.offsets, a.E, row0));
         if (e < 0) alive = 0;
@@ -183,21 +183,19 @@ __global__ __launch_bounds__(512) void k_mx_few(MxGemmArgs a) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const int c = GATED ? j >> 1 : j;
-            const int64_t tile = static_cast<int64_t>(e) * a.w_tiles + a.w_tile0 + (ct + c < n_tiles ? ct + c : n_tiles - 1);
+            const int64_t tile = static_cast<int64_t>(e) * n_tiles + (ct + c < n_tiles ? ct + c : n_tiles - 1);
             w[j] = ((GATED && (j & 1)) ? a.w2q : a.wq) + tile * G * 1024 + lane * 16;
             ws[j] = ((GATED && (j & 1)) ? a.w2s : a.ws) + tile * G4 * 256 + lane * 4;
         }
-        const bool gather = a.row_token && a.x;
         auto row_at = [&](int i) __attribute__((always_inline)) -> int64_t {
-            if (!gather) return row0 + i;
+            if (!GATED) return row0 + i;
             const int t = __builtin_amdgcn_readlane(token, i & 15);
             return static_cast<unsigned>(t) < static_cast<unsigned>(a.T) ? t : 0;
         };
         const int g0 = static_cast<int>(static_cast<int64_t>(G) * wave / waves);
         const int end = static_cast<int>(static_cast<int64_t>(G) * (wave + 1) / waves);
         if constexpr (__is_same(XT, MxReady)) {
-            auto here = [&](int i) __attribute__((always_inline)) -> int64_t { return row0 + i; };
-            few_run<XT, NT, MT, RB>(a, w, ws, rows, here, g0, end, nullptr, acc);
+            few_run<XT, NT, MT, RB>(a, w, ws, rows, row_at, g0, end, nullptr, acc);
         } else {
             few_run<XT, NT, MT, RB>(a, w, ws, rows, row_at, g0, end, lds + wave * MT * kRowsLds, acc);
         }
@@ -760,7 +758,7 @@ int mx_plan(int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_mx_few(const MxGemmArgs& a, int plan, hipStream_t st) {
     if (a.x) {
-        const int64_t rows = a.offsets ? a.T : a.M;
+        const int64_t rows = a.w2q ? a.T : a.M;
         switch (a.x_dtype) {
             case MQ_F32: return few_raw<float>(a, rows, st);
             case MQ_BF16: return few_raw<__bf16>(a, rows, st);
