@@ -157,7 +157,9 @@ __device__ __forceinline__ void few_run(const MxGemmArgs& a, const uint8_t* cons
 
 // One workgroup: 16 MT rows x NT column tiles of 16 (GATED: NT / 2 of each matrix), its
 // waves each a run of K; the partial sums are added through LDS in the order of the
-// waves.
+// waves. Bound by the weights' read where there are enough of them: one row of 8192 x 28672
+// takes 25 us (5 TB/s), of 14336 x 4096 8.5 us; of 4096 x 4096 4.2 us, most of it the latency
+// of a launch, the rows' quantization and one batch of loads.
 template <typename XT, int NT, int MT, int RB, bool GATED>
 __global__ __launch_bounds__(512) void k_mx_few(MxGemmArgs a) {
     constexpr int NC = GATED ? NT / 2 : NT;
@@ -235,6 +237,8 @@ hipError_t few(const MxGemmArgs& a, hipStream_t st) {
     const unsigned cols = static_cast<unsigned>(((a.N + 15) / 16 + NC - 1) / NC);
     const unsigned rows = static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT));
     const int G = (a.K + 127) / 128;
+    // A wave has at least two groups, from four waves on. Eight waves or four from K = 4096 on:
+    // 4.2 / 4.4 us (1 x 4096 x 4096), 8.5 / 8.9 (N = 14336); sixteen change nothing.
     const int waves = G >= 32 ? 8 : (G >= 8 ? 4 : (G >= 4 ? 2 : 1));
     constexpr int kRowsBytes = __is_same(XT, MxReady) ? 0 : kRowsLds;
     const size_t lds = static_cast<size_t>(waves) * (kRowsBytes > NT * 1024 ? kRowsBytes : NT * 1024) * MT;
@@ -262,7 +266,8 @@ hipError_t few_raw(const MxGemmArgs& a, int64_t rows, hipStream_t st) {
 // columns, token), a wave for each slot (of up to kDownWaves; fewer slots: several waves
 // split a slot's K). The slots' sums meet in LDS and are added in their order, so the
 // rows need no memory of their own and no second launch. Experts that tokens share are
-// read once a token: for few tokens there are few of those.
+// read once a token: for few tokens there are few of those. One token, 8 experts of 4096 x
+// 1024: 6.0 us, bound by the chain of loads (slot's row, its expert, the row, the weights).
 constexpr int kDownWaves = 16;
 
 template <typename XT, int NT>
@@ -372,7 +377,12 @@ int wide_pieces(int64_t rows32, int64_t cols, int64_t K, double* time) {
 // (the layout is the instruction's own); the rows and their scales, which the four waves
 // share, go through four LDS stages, one barrier a step. Reads beyond the operands' ends
 // give zero (buffer loads with the operands' sizes). Two workgroups share a CU: one's
-// products fill the other's barriers, first loads and stores.
+// products fill the other's barriers, first loads and stores (against one workgroup of 192
+// rows a CU, whose waves have twice the registers: 32768 x 4096 x 1024 97 / 124 us, 8192^3
+// 262 / 286, 2048 x 17408 x 5120 106 / 105).
+// Measured: 8192^3 4.2 PFLOP/s, where products fed from registers reach 6.6 on such codes.
+// The matrix units are busy for half the cycles, LDS for a third; with all codes alike the
+// same products run at 5.3, so the clock that the power leaves is a good part of it.
 template <typename T, int SUB, bool GATED>
 __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int rt0, int n16, int e, int col16) {
     constexpr int XL = (SUB + 1) / 2;                // 16-row tiles that a wave fetches a step
@@ -681,7 +691,8 @@ __global__ __launch_bounds__(256, 2) void k_mx_wide(MxGemmArgs a, int blocks, in
 }
 
 // y[t][d0 + d] = sum over j of weights[t][j] * rows[row_of[t][j]][d], d < cols. Four columns
-// a thread; a token's rows are read eight at a time.
+// a thread; a token's rows are read eight at a time. Bound by that read: 201 MB of rows in
+// 40 us, 134 MB in 24.
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine(const float* rows, int64_t n_rows, const int32_t* row_of,
                                                  const float* weights, int64_t T_, int k, int pitch, int cols, int64_t d0,

@@ -86,7 +86,8 @@ __device__ inline int first_best(uint64_t key) {
 // with their bias, in 64 bits; else the logits themselves, and only the chosen experts'
 // scores are computed (softmax: and the sum). A key of 0 is a masked expert. Bound by
 // the latency of k rounds of a maximum over the wave: lane moves in the vector unit keep
-// a round near 200 cycles (through LDS permutes, 64-bit values: 1500).
+// a round near 200 cycles (through LDS permutes, 64-bit values: 1500). One token of 128
+// experts: 3.5 us; 4096 tokens of 256 in 8 groups, sigmoid and bias: 11.7 us.
 template <typename T, int V, bool BIAS>
 __global__ __launch_bounds__(64 * kTokens) void k_route(RouteArgs a) {
     using Key = typename std::conditional<BIAS, uint64_t, uint32_t>::type;
@@ -370,7 +371,9 @@ __device__ void plan_tail(const PlanArgs& a, int64_t end) {
 }
 
 // One launch: workgroup b counts the ids of all slots, and of those before its own 1024,
-// which it then places. The ids are read once a workgroup, from L2.
+// which it then places. The ids are read once a workgroup, from L2, and counted by LDS
+// atomics (whose order changes nothing), which take most of the time: 8 slots 4.1 us, 32768
+// slots of 256 experts 8.2 us.
 __global__ __launch_bounds__(kPlanThreads) void k_plan(PlanArgs a) {
     __shared__ PlanLds s;
     const int tid = threadIdx.x;
