@@ -752,19 +752,30 @@ hipError_t wide(const MxGemmArgs& a, hipStream_t st) {
 
 }  // namespace
 
+// The least of the ways' costs, fits of measured times (us) in rounds of 256 workgroups:
+// 16 rows and one column tile a workgroup, 32 rows and one, two or four, and tiles of many
+// rows (the fourth way's workgroups are two to a CU by their LDS, so it goes by whole rounds
+// of 512). Few workgroups of the last take a third of a us or more for a step of K: the
+// latency of weights that no cache holds. Over 110 sizes (10 to 800 rows, K = 512 to 14336)
+// the choice is within 13% of the fastest way, 0.5% on average. E.g. (in this order) 64 x 1024 x 4096: 3.9, 4.4,
+// 6.0, 7.7, 11.0; 256 x 4096 x 14336: 66.7, 53.1, 41.6, 33.6, 47.0; 96 x 14336 x 4096: 27.2, 23.0,
+// 20.9, 21.6, 16.4.
 int mx_plan(int64_t M, int64_t N, int64_t K) {
     if (M <= 16) return kMxOneTile;
-    const double groups = static_cast<double>((K + 127) / 128), g = groups / 32, rows32 = static_cast<double>((M + 31) / 32);
-    const double u = rows32 * static_cast<double>((N + 15) / 16) / 256;       // workgroups of one column tile, in 256s
-    const double cost[3] = {2.4 + g + fmax(u, 1.0) * (0.5 + 1.15 * g),
-                            2.6 + 2.0 * g + fmax(u / 2, 1.0) * (0.4 + 1.9 * g),
-                            4.0 + 2.2 * g + fmax(u / 4, 0.7) * (0.6 + 2.6 * g)};
+    const int64_t rows16 = (M + 15) / 16, rows32 = (M + 31) / 32, tiles = (N + 15) / 16;
+    const double g = static_cast<double>((K + 127) / 128) / 32;
+    const double v = static_cast<double>(rows16 * tiles) / 256, u = static_cast<double>(rows32 * tiles) / 256;
+    const double cost[4] = {0.65 + 0.53 * g + fmax(v, 1.0) * (0.73 + 0.83 * g),
+                            2.3 + 0.6 * g + fmax(u, 1.0) * (0.58 + 1.49 * g),
+                            2.53 + 1.7 * g + fmax(u / 2, 1.0) * (0.77 + 2.12 * g),
+                            3.91 + 2.5 * g + (u <= 8 ? fmax(u / 4, 0.75) : 2 * ceil(u / 8)) * (0.35 + 3.45 * g)};
     int best = 0;
-    for (int i = 1; i < 3; ++i)
+    for (int i = 1; i < 4; ++i)
         if (cost[i] < cost[best]) best = i;
     double wide;
-    wide_pieces(static_cast<int64_t>(rows32), (N + 255) / 256, K, &wide);
-    return cost[best] < wide && rows32 <= 65535 ? best : kMxWide;
+    wide_pieces(rows32, (N + 255) / 256, K, &wide);
+    wide = fmax(wide, 2.0 + 0.37 * 32 * g);
+    return cost[best] < wide && rows16 <= 65535 ? best + kMxOneTile : kMxWide;
 }
 
 hipError_t launch_mx_few(const MxGemmArgs& a, int plan, hipStream_t st) {
