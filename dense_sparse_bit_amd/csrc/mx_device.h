@@ -163,6 +163,16 @@ __device__ inline MxRaw8<T> mx_load8_tail(const T* row, int k, int K, int lim) {
     return r;
 }
 
+// Between LDS accesses of a wave's lanes where one lane's stores are another's loads, or the
+// other way round. A wave's LDS accesses complete in the order of its instructions, so the
+// fences cost none of their own; they keep the compiler, which sees one lane, from moving
+// an access across. (The wave barrier alone orders no memory accesses.)
+__device__ __forceinline__ void mx_wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // max over the four lanes of a block
 __device__ inline uint32_t mx_quad_max(uint32_t m) {
     m = max(m, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xB1, 0xf, 0xf, true)));

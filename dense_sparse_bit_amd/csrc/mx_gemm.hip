@@ -137,9 +137,9 @@ __device__ __forceinline__ void few_run(const MxGemmArgs& a, const uint8_t* cons
 #pragma unroll
                     for (int j = 0; j < NT; ++j) acc[j][i] = mfma16(wc[u][j], c[u][i], acc[j][i], wb[u][j], b[u][i]);
         } else {
-            __builtin_amdgcn_wave_barrier();               // the last batch's reads come first
+            mx_wave_sync();                                // the last batch's reads come first
             rows_to_lds<XT, RB>(static_cast<const XT*>(a.x), a.stride_x, a.K, rows, row_at, g, end, lds, load_w);
-            __builtin_amdgcn_wave_barrier();               // a wave's LDS accesses complete in order
+            mx_wave_sync();
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 const uint8_t* from = lds + i * kRowsLds;
@@ -602,7 +602,7 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
             const int m = 32 * i + (lane & 31);
             live = m < rows && static_cast<unsigned>(a.row_token[rt0 * 16 + m]) < static_cast<unsigned>(a.T);
         }
-        __builtin_amdgcn_wave_barrier();                         // a wave's LDS accesses complete in order
+        mx_wave_sync();                                          // the last piece's reads come first
 #pragma unroll
         for (int j = 0; j < (GATED ? 1 : 2); ++j) {
 #pragma unroll
@@ -620,7 +620,7 @@ __device__ __forceinline__ void wide_tile(const MxGemmArgs& a, uint8_t* lds, int
                     *reinterpret_cast<uint2*>(to) = make_uint2(mx_pack2<T>(v[0], v[1]), mx_pack2<T>(v[2], v[3]));
             }
         }
-        __builtin_amdgcn_wave_barrier();
+        mx_wave_sync();
         if (vec) {
 #pragma unroll
             for (int s = 0; s < 32 / kRound; ++s) {

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(64 * kTokens) void k_route(RouteArgs a) {
             const int shift = a.groups > 1 ? __builtin_clz(a.groups - 1) - 26 : 6, run = 1 << shift;
             const int group = lane >> shift;
             double* mine = lds + wave * 64 * V;
-            __builtin_amdgcn_wave_barrier();
+            mx_wave_sync();                              // the last token's reads come first
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 double v = -HUGE_VAL;
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(64 * kTokens) void k_route(RouteArgs a) {
                 }
                 mine[lane * V + i] = v;
             }
-            __builtin_amdgcn_wave_barrier();             // a wave's LDS accesses complete in order
+            mx_wave_sync();
             double first = -HUGE_VAL, second = -HUGE_VAL;
             if (group < a.groups) {
 #pragma unroll 4
