@@ -83,13 +83,19 @@ const at::Tensor& input(const Here& here, PyObject* o, int64_t dims) {
     return t;
 }
 
+// One of the public named tuples, with all of its items (a tuple type's instance can be made
+// with fewer, by tuple.__new__): only then are they read without a check each.
+bool whole(PyObject* o, const PyTypeObject* type, Py_ssize_t items) {
+    return Py_TYPE(o) == type && PyTuple_GET_SIZE(o) == items;
+}
+
 struct Matrix {
     const uint8_t *codes, *scales;
     int64_t rows, cols;
 };
 
 Matrix matrix(const Here& here, PyObject* o, int64_t batch = -1) {
-    need(Py_TYPE(o) == mx_type);
+    need(whole(o, mx_type, 4));
     Matrix m;
     m.rows = integer(PyTuple_GET_ITEM(o, 2));
     m.cols = integer(PyTuple_GET_ITEM(o, 3));
@@ -169,7 +175,7 @@ PyObject* quantize(PyObject* const* a) {
 // dequantize(a, dtype, out)
 PyObject* dequantize(PyObject* const* a) {
     const Here here;
-    need(Py_TYPE(a[0]) == mx_type);
+    need(whole(a[0], mx_type, 4));
     const at::Tensor& c = tensor(PyTuple_GET_ITEM(a[0], 0));
     const bool batched = c.dim() == 4;
     const int64_t B = batched ? c.size(0) : 1;
@@ -250,7 +256,7 @@ struct Plan {
 };
 
 Plan plan(const Here& here, PyObject* o) {
-    need(Py_TYPE(o) == plan_type);
+    need(whole(o, plan_type, 3));
     const at::Tensor &offsets = tensor(PyTuple_GET_ITEM(o, 0)), &row_of = tensor(PyTuple_GET_ITEM(o, 2));
     need(row_of.dim() == 2 && offsets.dim() == 1);
     Plan p;

@@ -113,7 +113,7 @@ def expert_plan(ids, experts: int, stream=None) -> ExpertPlan:
 
 def _plan(plan, index):
     """(T, k, experts, rows) of a plan, its tensors checked."""
-    if not isinstance(plan, ExpertPlan):
+    if not isinstance(plan, ExpertPlan) or len(plan) != 3:
         raise TypeError("plan must be an ExpertPlan (expert_plan)")
     offsets, row_token, row_of = plan
     T, k = row_of.shape

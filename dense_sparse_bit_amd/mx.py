@@ -66,11 +66,16 @@ def _check(t, name, dtype, shape, index):
     raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
+def _whole(a, name):
+    """The items of an MX, all of them."""
+    if not isinstance(a, MX) or len(a) != 4:
+        raise TypeError(f"{name} must be an MX matrix (mx_quantize)")
+    return a
+
+
 def _mx(a, name, index, batch=None):
     """A microscaled operand: its tensors have the sizes its rows and cols ask for."""
-    if not isinstance(a, MX):
-        raise TypeError(f"{name} must be an MX matrix (mx_quantize)")
-    codes, scales, rows, cols = a
+    codes, scales, rows, cols = _whole(a, name)
     tiles, groups = (rows + 15) // 16, (cols + 127) // 128
     if batch is None:
         _check(codes, f"{name}.codes", torch.uint8, (tiles, groups, 1024), index)
@@ -139,7 +144,7 @@ def mx_quantize(x, out=None, stream=None) -> MX:
         out = MX(torch.empty(lead + (tiles, groups, 1024), dtype=torch.uint8, device=x.device),
                  torch.empty(lead + (tiles, quads, 256), dtype=torch.uint8, device=x.device), R, K)
     else:
-        if isinstance(out, MX) and (out.rows, out.cols) != (R, K):
+        if _whole(out, "out")[2:] != (R, K):
             raise ValueError(f"out is {out.rows} x {out.cols}, x is {R} x {K}")
         _mx(out, "out", index, shape[0] if batched else None)
     rc = _quantize(x.data_ptr(), code, shape[0] if batched else 1, x.stride(0) if batched else 0, R, x.stride(-2), K,
@@ -155,9 +160,7 @@ def mx_dequantize(a: MX, dtype=torch.float32, out=None, stream=None):
         done = _binding.dequantize(a, dtype, out)
         if done is not None:
             return done
-    if not isinstance(a, MX):
-        raise TypeError("a must be an MX matrix (mx_quantize)")
-    codes, scales, R, K = a
+    codes, scales, R, K = _whole(a, "a")
     index = codes.get_device()
     if stream is not None or index < 0 or index != _current_device():
         with _on(index, stream, a, out):
@@ -181,7 +184,7 @@ def mx_linear(x, w: MX, bias=None, out_dtype=torch.bfloat16, y=None, stream=None
             return done
     ready = isinstance(x, MX)
     if ready:
-        index = x.codes.get_device()
+        index = _whole(x, "x").codes.get_device()
     else:
         code = _input(x, "x", 2)
         index = x.get_device()

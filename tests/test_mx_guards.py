@@ -25,3 +25,34 @@ def test_lanes_hand_lds_over_through_fences(source):
     calls = re.findall(r"__builtin_amdgcn_(\w+)\(([^)]*)\)", helper)
     assert calls == [("fence", '__ATOMIC_RELEASE, "wavefront", "local"'), ("wave_barrier", ""),
                      ("fence", '__ATOMIC_ACQUIRE, "wavefront", "local"')]
+
+
+def _short_operands(mq, device):
+    """Instances of the public tuples with too few items, where each call takes one."""
+    import torch
+    zeros = lambda *shape, dtype=torch.float32: torch.zeros(*shape, dtype=dtype, device=device)
+    x, h, weights = zeros(4, 64), zeros(32, 64), zeros(4, 2)
+    plan = mq.ExpertPlan(*(zeros(*shape, dtype=torch.int32) for shape in ((3,), (32,), (4, 2))))
+    w = mq.MX(zeros(1, 1, 1024, dtype=torch.uint8), zeros(1, 1, 256, dtype=torch.uint8), 16, 64)
+    e = mq.MX(zeros(2, 1, 1, 1024, dtype=torch.uint8), zeros(2, 1, 1, 256, dtype=torch.uint8), 16, 64)
+    for n in range(4):
+        a = tuple.__new__(mq.MX, w[:n])
+        yield from ((lambda a=a: mq.mx_dequantize(a)), (lambda a=a: mq.mx_linear(a, w)))
+        if device == "cpu":                      # the rest comes after checks that host tensors do not pass
+            continue
+        yield from ((lambda a=a: mq.mx_linear(x, a)), (lambda a=a: mq.mx_quantize(x, out=a)),
+                    (lambda a=a: mq.mx_experts_up(x, a, e, plan)), (lambda a=a: mq.mx_experts_up(x, e, a, plan)),
+                    (lambda a=a: mq.mx_experts_down(h, a, plan, weights)))
+        if n < 3:
+            p = tuple.__new__(mq.ExpertPlan, plan[:n])
+            yield from ((lambda p=p: mq.mx_experts_up(x, e, e, p)), (lambda p=p: mq.mx_experts_down(h, e, p, weights)))
+
+
+@pytest.mark.parametrize("device", ["cpu", pytest.param("cuda", marks=pytest.mark.gpu)])
+def test_tuples_with_items_missing_are_refused(mq, device):
+    import torch
+    if device == "cpu" and torch.cuda.is_available():
+        pytest.skip("the host's own order of checks, where no GPU is visible")
+    for call in _short_operands(mq, device):
+        with pytest.raises(TypeError, match="must be an"):
+            call()
