@@ -358,8 +358,8 @@ int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t
         a.N = static_cast<int>(D - d < step ? D - d : step);
         a.w_tile0 = static_cast<int>(d / 16);
         if (mq::launch_mx_wide(a, st) != hipSuccess) return MQ_ERR_HIP;
-        if (mq::launch_combine(rows, P, row_of, weights, T, static_cast<int>(k), static_cast<int>(step), a.N, d, D, y, y_dtype,
-                               st) != hipSuccess)
+        if (mq::launch_combine(rows, P, offsets + E, row_of, weights, T, static_cast<int>(k), static_cast<int>(step), a.N, d, D,
+                               y, y_dtype, st) != hipSuccess)
             return MQ_ERR_HIP;
     }
     return MQ_OK;

@@ -690,15 +690,17 @@ __global__ __launch_bounds__(256, 2) void k_mx_wide(MxGemmArgs a, int blocks, in
     }
 }
 
-// y[t][d0 + d] = sum over j of weights[t][j] * rows[row_of[t][j]][d], d < cols. Four columns
+// y[t][d0 + d] = sum over j of weights[t][j] * rows[row_of[t][j]][d], d < cols, rows before
+// *end (the last expert's end). Four columns
 // a thread; a token's rows are read eight at a time. Bound by that read: 201 MB of rows in
 // 40 us, 134 MB in 24.
 template <typename T>
-__global__ __launch_bounds__(256) void k_combine(const float* rows, int64_t n_rows, const int32_t* row_of,
+__global__ __launch_bounds__(256) void k_combine(const float* rows, int64_t n_rows, const int32_t* end, const int32_t* row_of,
                                                  const float* weights, int64_t T_, int k, int pitch, int cols, int64_t d0,
                                                  int64_t D, T* y) {
     const int d = (blockIdx.y * 256 + threadIdx.x) * 4;
     if (d >= cols) return;
+    const int live = *end < n_rows ? *end : static_cast<int>(n_rows);      // no product wrote the rows from here on
     for (int64_t t = blockIdx.x; t < T_; t += gridDim.x) {
         mx_f4 acc = {};
         for (int j0 = 0; j0 < k; j0 += 8) {
@@ -710,7 +712,7 @@ __global__ __launch_bounds__(256) void k_combine(const float* rows, int64_t n_ro
                 const int p = there ? row_of[t * k + j0 + j] : -1;
                 w[j] = there ? weights[t * k + j0 + j] : 0.0f;
                 r[j] = mx_f4{0, 0, 0, 0};
-                if (p >= 0 && p < n_rows) r[j] = *reinterpret_cast<const mx_f4*>(rows + static_cast<int64_t>(p) * pitch + d);
+                if (p >= 0 && p < live) r[j] = *reinterpret_cast<const mx_f4*>(rows + static_cast<int64_t>(p) * pitch + d);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc += w[j] * r[j];
@@ -721,11 +723,11 @@ __global__ __launch_bounds__(256) void k_combine(const float* rows, int64_t n_ro
 }
 
 template <typename T>
-hipError_t combine(const float* rows, int64_t n_rows, const int32_t* row_of, const float* weights, int64_t T_, int k,
-                   int pitch, int cols, int64_t d0, int64_t D, void* y, hipStream_t st) {
+hipError_t combine(const float* rows, int64_t n_rows, const int32_t* end, const int32_t* row_of, const float* weights,
+                   int64_t T_, int k, int pitch, int cols, int64_t d0, int64_t D, void* y, hipStream_t st) {
     const unsigned grid = static_cast<unsigned>(T_ < (1 << 20) ? T_ : 1 << 20);
     k_combine<T><<<dim3(grid, static_cast<unsigned>((cols + 1023) / 1024)), 256, 0, st>>>(
-        rows, n_rows, row_of, weights, T_, k, pitch, cols, d0, D, static_cast<T*>(y));
+        rows, n_rows, end, row_of, weights, T_, k, pitch, cols, d0, D, static_cast<T*>(y));
     return hipGetLastError();
 }
 
@@ -812,12 +814,12 @@ hipError_t launch_mx_wide(const MxGemmArgs& a, hipStream_t st) {
     }
 }
 
-hipError_t launch_combine(const float* rows, int64_t n_rows, const int32_t* row_of, const float* weights, int64_t T,
-                          int k, int pitch, int cols, int64_t d0, int64_t D, void* y, int y_dtype, hipStream_t st) {
+hipError_t launch_combine(const float* rows, int64_t n_rows, const int32_t* end, const int32_t* row_of, const float* weights,
+                          int64_t T, int k, int pitch, int cols, int64_t d0, int64_t D, void* y, int y_dtype, hipStream_t st) {
     switch (y_dtype) {
-        case MQ_F32: return combine<float>(rows, n_rows, row_of, weights, T, k, pitch, cols, d0, D, y, st);
-        case MQ_BF16: return combine<__bf16>(rows, n_rows, row_of, weights, T, k, pitch, cols, d0, D, y, st);
-        default: return combine<_Float16>(rows, n_rows, row_of, weights, T, k, pitch, cols, d0, D, y, st);
+        case MQ_F32: return combine<float>(rows, n_rows, end, row_of, weights, T, k, pitch, cols, d0, D, y, st);
+        case MQ_BF16: return combine<__bf16>(rows, n_rows, end, row_of, weights, T, k, pitch, cols, d0, D, y, st);
+        default: return combine<_Float16>(rows, n_rows, end, row_of, weights, T, k, pitch, cols, d0, D, y, st);
     }
 }
 

@@ -114,8 +114,8 @@ hipError_t launch_mx_wide(const MxGemmArgs& a, hipStream_t st);
 hipError_t launch_route(const RouteArgs& a, hipStream_t st);
 hipError_t launch_plan(const PlanArgs& a, hipStream_t st);
 // y[t][d0 + d] = sum over j of weights[t][j] * rows[row_of[t][j]][d], d < cols (fp32 rows,
-// a multiple of 4 apart)
-hipError_t launch_combine(const float* rows, int64_t n_rows, const int32_t* row_of, const float* weights, int64_t T,
-                          int k, int pitch, int cols, int64_t d0, int64_t D, void* y, int y_dtype, hipStream_t st);
+// a multiple of 4 apart; those from *end on, on the device, are no rows)
+hipError_t launch_combine(const float* rows, int64_t n_rows, const int32_t* end, const int32_t* row_of, const float* weights,
+                          int64_t T, int k, int pitch, int cols, int64_t d0, int64_t D, void* y, int y_dtype, hipStream_t st);
 
 }  // namespace mq

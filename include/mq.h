@@ -416,7 +416,8 @@ int mq_expert_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t*
  *   h[p][i] = silu(g) * u,  g = Q(x[t]) . gate[e][i],  u = Q(x[t]) . up[e][i]
  * with silu(g) = g / (1 + exp(-g)); rows of no token are zero. x: [T][D] (row stride
  * stride_t), gate and up: E matrices I x D, h: [mq_plan_rows][I]. The plan is
- * mq_expert_plan's; entries of it out of range are taken as "no row".
+ * mq_expert_plan's; entries of row_token and row_of out of range (rows from offsets[E] on
+ * among them) are taken as "no row".
  * T * ceil(D / 256) * 128 < 2^32.
  */
 size_t mq_mx_experts_up_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I);

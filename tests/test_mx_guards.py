@@ -56,3 +56,35 @@ def test_tuples_with_items_missing_are_refused(mq, device):
     for call in _short_operands(mq, device):
         with pytest.raises(TypeError, match="must be an"):
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [4, 40])
+def test_rows_past_the_last_experts_are_no_rows(mq, T):
+    """A slot whose row lies after the last expert's adds zero, token by token and in row
+    blocks alike, whatever the workspace held before."""
+    import torch
+    E, k, D, I = 4, 2, 72, 96
+    g = torch.Generator(device="cuda").manual_seed(T)
+    ids = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    plan = mq.expert_plan(ids, E)
+    rows = plan.row_token.numel()
+    assert int(plan.offsets[E]) < rows
+    w = mq.mx_quantize(torch.randn(E, D, I, generator=g, device="cuda"))
+    h = torch.randn(rows, I, generator=g, device="cuda")
+    weights = torch.rand(T, k, generator=g, device="cuda")
+    lib, stream = mq.lib(), torch.cuda.current_stream().cuda_stream
+    need = lib.mq_mx_experts_down_workspace_bytes(T, k, E, D, I)
+    results = []
+    for row in (rows - 1, int(plan.offsets[E]), -1):
+        row_of = plan.row_of.clone()
+        row_of[T // 2, 1] = row
+        work = torch.full((need + 16,), 255, dtype=torch.uint8, device="cuda")          # NaN in fp32
+        y = torch.empty(T, D, device="cuda")
+        assert lib.mq_mx_experts_down(h.data_ptr(), 0, T, k, E, D, I, plan.offsets.data_ptr(), row_of.data_ptr(),
+                                      weights.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), y.data_ptr(), 0,
+                                      work.data_ptr(), need, stream) == 0
+        torch.cuda.synchronize()
+        results.append(y)
+    assert torch.isfinite(results[2]).all()
+    assert torch.equal(results[0], results[2]) and torch.equal(results[1], results[2])
