@@ -48,6 +48,14 @@ int check_slots(int64_t T, int64_t k, int64_t E) {
     return MQ_OK;
 }
 
+// sizes of the experts' products of T tokens: N outputs of K inputs a row and expert
+int check_experts(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
+    const int rc = check_slots(T, k, E);
+    if (rc) return rc;
+    const int product = check_product(mq::plan_rows(T, k, E), N, K);
+    return product ? product : check_matrix(E, N, K);
+}
+
 size_t round16(int64_t n) { return static_cast<size_t>((n + 15) / 16 * 16); }
 
 // codes, then scales, of an R x K matrix in a workspace
@@ -261,7 +269,7 @@ int mq_expert_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t*
 }
 
 size_t mq_mx_experts_up_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I) {
-    if (check_slots(T, k, E) || check_product(T * k, I, D) || check_row_offsets(T, D) || few_tokens(T, k)) return 0;
+    if (check_experts(T, k, E, I, D) || check_row_offsets(T, D) || few_tokens(T, k)) return 0;
     const int64_t P = mq::plan_rows(T, k, E);
     return row_bytes(T, D) + tiles_bytes(P, E);
 }
@@ -270,9 +278,8 @@ int mq_mx_experts_up(const void* x, int x_dtype, int64_t stride_t, int64_t T, in
                      const int32_t* offsets, const int32_t* row_token, const int32_t* row_of, const uint8_t* gate_q,
                      const uint8_t* gate_s, const uint8_t* up_q, const uint8_t* up_s, void* h, int h_dtype,
                      void* workspace, size_t workspace_bytes, void* stream) {
-    int rc = check_slots(T, k, E);
-    if (rc || (rc = check_product(mq::plan_rows(T, k, E), I, D)) || (rc = check_matrix(E, I, D)) || (rc = check_row_offsets(T, D)))
-        return rc;
+    int rc = check_experts(T, k, E, I, D);
+    if (rc || (rc = check_row_offsets(T, D))) return rc;
     if (bad_type(x_dtype) || bad_type(h_dtype) || stride_t < 0) return MQ_ERR_INVALID_ARG;
     if (T == 0) return MQ_OK;
     if (!x || off(x, type_size(x_dtype)) || !h || off(h, 16)) return MQ_ERR_INVALID_ARG;
@@ -309,7 +316,7 @@ int mq_mx_experts_up(const void* x, int x_dtype, int64_t stride_t, int64_t T, in
 }
 
 size_t mq_mx_experts_down_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t I) {
-    if (check_slots(T, k, E) || check_product(T * k, D, I) || one_by_one(T, k)) return 0;
+    if (check_experts(T, k, E, D, I) || one_by_one(T, k)) return 0;
     const int64_t P = mq::plan_rows(T, k, E);
     const size_t rows = round16(P * down_cols(P, D) * 4);
     return rows + mx_bytes(P, I) + tiles_bytes(P, E);
@@ -318,8 +325,8 @@ size_t mq_mx_experts_down_workspace_bytes(int64_t T, int64_t k, int64_t E, int64
 int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t E, int64_t D, int64_t I,
                        const int32_t* offsets, const int32_t* row_of, const float* weights, const uint8_t* wq,
                        const uint8_t* ws, void* y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
-    int rc = check_slots(T, k, E);
-    if (rc || (rc = check_product(mq::plan_rows(T, k, E), D, I)) || (rc = check_matrix(E, D, I))) return rc;
+    int rc = check_experts(T, k, E, D, I);
+    if (rc) return rc;
     if (bad_type(h_dtype) || bad_type(y_dtype)) return MQ_ERR_INVALID_ARG;
     if (T == 0) return MQ_OK;
     if (!h || off(h, type_size(h_dtype)) || !y || off(y, 16)) return MQ_ERR_INVALID_ARG;

@@ -88,3 +88,22 @@ def test_rows_past_the_last_experts_are_no_rows(mq, T):
         results.append(y)
     assert torch.isfinite(results[2]).all()
     assert torch.equal(results[0], results[2]) and torch.equal(results[1], results[2])
+
+
+def test_no_workspace_for_calls_that_are_refused(mq):
+    """The sizes of a workspace go by the checks of the call that takes it: a program learns
+    of a refusal before it allocates. 2^24 slots make more than 2^24 rows of a plan."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("host-only argument checks run where no GPU is visible")
+    lib, p = mq.lib(), 0x10000
+    up = lambda T, k, E, D, I: lib.mq_mx_experts_up(p, 1, D, T, k, E, D, I, p, p, p, p, p, p, p, p, 1, None, 0, None)
+    down = lambda T, k, E, D, I: lib.mq_mx_experts_down(p, 1, T, k, E, D, I, p, p, p, p, p, p, 1, None, 0, None)
+    for T, k, E, D, I in ((1 << 21, 8, 1024, 512, 256), (1 << 24, 1, 2, 64, 64), (100, 4, 1024, 1 << 20, 1 << 11),
+                          (100, 4, 1024, 1 << 11, 1 << 20), (100, 0, 8, 64, 64), (100, 4, 8, 0, 64), (100, 4, 8, 64, 0)):
+        assert up(T, k, E, D, I) < 0 and down(T, k, E, D, I) < 0
+        assert lib.mq_mx_experts_up_workspace_bytes(T, k, E, D, I) == 0, (T, k, E, D, I)
+        assert lib.mq_mx_experts_down_workspace_bytes(T, k, E, D, I) == 0, (T, k, E, D, I)
+    # refused for the missing workspace alone
+    assert up(100, 4, 8, 64, 64) == -1 and lib.mq_mx_experts_up_workspace_bytes(100, 4, 8, 64, 64) > 0
+    assert down(100, 4, 8, 64, 64) == -1 and lib.mq_mx_experts_down_workspace_bytes(100, 4, 8, 64, 64) > 0
