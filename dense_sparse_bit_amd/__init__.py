@@ -13,7 +13,9 @@ Packed tensors use the library's device layouts (include/mq.h): xq is
 from __future__ import annotations
 
 import ctypes as C
+import importlib
 import os
+import warnings
 
 import torch  # loads torch's HIP runtime first, so libmq.so binds to the same one
 
@@ -29,11 +31,15 @@ if not os.path.exists(LIB_PATH):
 
 _lib = C.CDLL(LIB_PATH)
 
+# The short way from Python to the microscaled and routing calls (csrc/binding.cpp), which is
+# tied to one Python and one torch. It links to torch and libmq.so, so it comes after both.
 try:
-    from . import _binding  # noqa: E402  (csrc/binding.cpp; after torch and libmq.so, which it links to)
+    _binding = importlib.import_module("._binding", __name__)
 except ImportError as e:
-    raise ImportError(f"{_PKG}/_binding.so is missing or does not load: build it with "
-                      "`python dense_sparse_bit_amd/_build.py`") from e
+    _binding = None
+    warnings.warn(f"_binding.so is missing or does not load ({e}): the microscaled and routing calls go through "
+                  "ctypes, at about twice the host's time. Build it with `python dense_sparse_bit_amd/_build.py`.",
+                  RuntimeWarning, stacklevel=2)
 _p, _i64, _int = C.c_void_p, C.c_int64, C.c_int
 
 _SIGS = {

@@ -54,11 +54,16 @@ def _compile(name: str, flags: list) -> str:
 
 
 def _binding() -> str:
-    """The extension module: host code against torch's headers and libmq.so."""
+    """The extension module: host code against torch's headers and libmq.so. It holds the
+    versions that it is built for, and does not load with others."""
     spec = importlib.util.find_spec("torch")              # found, not imported
     torch = os.path.dirname(spec.origin)
+    spec = importlib.util.spec_from_file_location("_torch_version", os.path.join(torch, "version.py"))
+    version = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(version)
     out = os.path.join(PKG, "_binding.so")
     cmd = ["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f'-DMQ_TORCH_VERSION="{version.__version__}"',
            "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"),
            "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", out + ".tmp",
@@ -66,6 +71,8 @@ def _binding() -> str:
            "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
+        if os.path.exists(out):
+            os.remove(out)                                # it was built for another libmq.so
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stderr}")
     os.replace(out + ".tmp", out)
     return out

@@ -18,7 +18,13 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <string.h>
+
 #include "../../include/mq.h"
+
+#define MQ_TEXT_(x) #x
+#define MQ_TEXT(x) MQ_TEXT_(x)
+#define MQ_PYTHON_VERSION MQ_TEXT(PY_MAJOR_VERSION) "." MQ_TEXT(PY_MINOR_VERSION) "."
 
 namespace {
 
@@ -349,4 +355,26 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "short way to the libra
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+// Objects of this Python and this torch are read by their layout in memory, so the module
+// does not load with others than it was built for.
+PyMODINIT_FUNC PyInit__binding() {
+    const char* const python = Py_GetVersion();                       // "major.minor.micro ..."
+    const size_t n = sizeof(MQ_PYTHON_VERSION) - 1;
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+    PyObject* text = version ? PyObject_Str(version) : nullptr;
+    const char* const now = text ? PyUnicode_AsUTF8(text) : nullptr;
+    PyObject* made = nullptr;
+    if (now) {
+        if (strncmp(python, MQ_PYTHON_VERSION, n) == 0 && strcmp(now, MQ_TORCH_VERSION) == 0) {
+            made = PyModule_Create(&module);
+        } else {
+            PyErr_Format(PyExc_ImportError, "built for Python " MQ_PYTHON_VERSION "x and torch " MQ_TORCH_VERSION ", this is torch %s",
+                         now);
+        }
+    }
+    Py_XDECREF(text);
+    Py_XDECREF(version);
+    Py_XDECREF(torch);
+    return made;
+}

@@ -22,7 +22,8 @@ class ExpertPlan(NamedTuple):
     row_of: torch.Tensor
 
 
-_binding.types(MX, ExpertPlan)
+if _binding is not None:
+    _binding.types(MX, ExpertPlan)
 _route, _plan_rows, _expert_plan = _lib.mq_route, _lib.mq_plan_rows, _lib.mq_expert_plan
 _up, _up_workspace = _lib.mq_mx_experts_up, _lib.mq_mx_experts_up_workspace_bytes
 _down, _down_workspace = _lib.mq_mx_experts_down, _lib.mq_mx_experts_down_workspace_bytes
@@ -44,7 +45,7 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
     ("max": a group's largest key, "top2": the sum of its two largest). Logits of -inf mask
     experts: slots that none is left for have id -1 and weight 0. A NaN gives ids -1 and
     weights NaN."""
-    if stream is None:
+    if stream is None and _binding is not None:
         done = _binding.route(logits, k, _SCORES.get(score, -1), bias, groups, groups if top_groups is None else top_groups,
                               _GROUP_SCORES.get(group_score, -1), renormalize, float(scale), ids, weights)
         if done is not None:
@@ -85,7 +86,7 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
 def expert_plan(ids, experts: int, stream=None) -> ExpertPlan:
     """The plan of ids int32 [T, k]. Ids outside [0, experts), such as -1 or another
     rank's experts, get no row."""
-    if stream is None:
+    if stream is None and _binding is not None:
         done = _binding.expert_plan(ids, experts)
         if done is not None:
             return done
@@ -128,7 +129,7 @@ def _plan(plan, index):
 def mx_experts_up(x, w_gate: MX, w_up: MX, plan: ExpertPlan, out_dtype=torch.bfloat16, h=None, stream=None):
     """h [rows, I]: for each row of the plan silu(Q(x[t]) w_gate[e]^T) * (Q(x[t]) w_up[e]^T),
     zero for rows of no token. x [T, D]; w_gate, w_up: MX batches [experts, I, D]."""
-    if stream is None:
+    if stream is None and _binding is not None:
         done = _binding.experts_up(x, w_gate, w_up, plan, out_dtype, h)
         if done is not None:
             return done
@@ -160,7 +161,7 @@ def mx_experts_up(x, w_gate: MX, w_up: MX, plan: ExpertPlan, out_dtype=torch.bfl
 def mx_experts_down(h, w_down: MX, plan: ExpertPlan, weights, out_dtype=torch.bfloat16, y=None, stream=None):
     """y[t] = sum over slots j of weights[t, j] * (Q(h[row_of[t, j]]) w_down[e]^T), in the order
     of the slots. h [rows, I], weights fp32 [T, k], w_down: MX batch [experts, D, I]."""
-    if stream is None:
+    if stream is None and _binding is not None:
         done = _binding.experts_down(h, w_down, plan, weights, out_dtype, y)
         if done is not None:
             return done

@@ -5,7 +5,7 @@ functions check and marshal device tensors; all of the work runs in libmq.so. A 
 with all as it should be, on the current device and stream, is done by the extension
 module _binding (csrc/binding.cpp), which costs the host about half of what the same
 steps cost in Python; the rest of each function tells what is wrong, or makes another
-device or stream current first.
+device or stream current first. Where the module is not there, it does all calls.
 """
 from __future__ import annotations
 
@@ -123,7 +123,7 @@ def mx_quantize(x, out=None, stream=None) -> MX:
     """x [R, K] or [B, R, K] (fp32, bf16, fp16; the last axis contiguous, other strides
     free) to microscaled 4-bit. A block of 32 with a NaN or an infinity reads back as NaN.
     out: an MX of the same sizes to write to."""
-    if stream is None:
+    if stream is None and _binding is not None:
         done = _binding.quantize(x, out)
         if done is not None:
             return done
@@ -156,7 +156,7 @@ def mx_quantize(x, out=None, stream=None) -> MX:
 
 def mx_dequantize(a: MX, dtype=torch.float32, out=None, stream=None):
     """The values of a microscaled matrix (or batch), [(B,) R, K]."""
-    if stream is None:
+    if stream is None and _binding is not None:
         done = _binding.dequantize(a, dtype, out)
         if done is not None:
             return done
@@ -178,7 +178,7 @@ def mx_dequantize(a: MX, dtype=torch.float32, out=None, stream=None):
 def mx_linear(x, w: MX, bias=None, out_dtype=torch.bfloat16, y=None, stream=None):
     """y = Q(x) w^T + bias: x [M, K] (fp32, bf16, fp16), quantized on the way, or an MX
     matrix; w an MX matrix [N, K]; bias fp32 [N]."""
-    if stream is None:
+    if stream is None and _binding is not None:
         done = _binding.linear(x, w, bias, out_dtype, y)
         if done is not None:
             return done

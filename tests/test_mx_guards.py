@@ -3,6 +3,8 @@ a wave's LDS accesses, operands that are no whole tuples, plans and sizes at the
 a machine without the extension module."""
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 
@@ -107,3 +109,62 @@ def test_no_workspace_for_calls_that_are_refused(mq):
     # refused for the missing workspace alone
     assert up(100, 4, 8, 64, 64) == -1 and lib.mq_mx_experts_up_workspace_bytes(100, 4, 8, 64, 64) > 0
     assert down(100, 4, 8, 64, 64) == -1 and lib.mq_mx_experts_down_workspace_bytes(100, 4, 8, 64, 64) > 0
+
+
+def _python(code):
+    return subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300,
+                          env={**os.environ, "HIP_VISIBLE_DEVICES": "-1"})
+
+
+WITHOUT = "import sys; sys.modules['dense_sparse_bit_amd._binding'] = None; "
+
+
+def test_package_without_the_extension_module():
+    """The package imports, says so, and passes its host tests."""
+    r = _python(WITHOUT + "import dense_sparse_bit_amd as mq; assert mq._binding is None; import pytest; "
+                "sys.exit(pytest.main(['-q', '-x', '-p', 'no:cacheprovider', '-m', 'not gpu', "
+                "'tests/test_abi.py', 'tests/test_mx_abi.py']))")
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "RuntimeWarning: _binding.so is missing" in r.stderr, r.stderr
+
+
+def test_extension_module_of_another_torch_is_not_loaded(mq):
+    if mq._binding is None:
+        pytest.skip("no extension module here")
+    r = _python("import torch; torch.__version__ = '9.9'; import dense_sparse_bit_amd as mq; assert mq._binding is None")
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "RuntimeWarning" in r.stderr and "this is torch 9.9" in r.stderr, r.stderr
+    r = _python("import dense_sparse_bit_amd as mq; assert mq._binding is not None")
+    assert r.returncode == 0 and "RuntimeWarning" not in r.stderr, r.stdout + r.stderr
+
+
+@pytest.mark.gpu
+def test_the_long_way_gives_the_same_bits(mq, monkeypatch):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1)
+    draw = lambda *shape: torch.randn(*shape, generator=g, device="cuda")
+    E, k, D, I = 8, 2, 200, 96
+    x, w, bias, router = draw(40, D), draw(64, D), draw(64), draw(40, E)
+    wg, wu, wd = draw(E, I, D), draw(E, I, D), draw(E, D, I)
+
+    def calls():
+        for T in (40, 3, 0):
+            a = mq.mx_quantize(x[:T])
+            b = mq.mx_quantize(wg)
+            yield from (*a[:2], *b[:2], mq.mx_dequantize(a, dtype=torch.float16), mq.mx_dequantize(b))
+            q = mq.mx_quantize(w, out=mq.mx_quantize(w))
+            yield from (mq.mx_linear(x[:T], q, bias=bias), mq.mx_linear(a, q, out_dtype=torch.float32),
+                        mq.mx_linear(x[:T], q, y=torch.empty(T, 64, device="cuda", dtype=torch.float16)))
+            ids, weights = mq.route(router[:T], k, score="sigmoid", groups=4, top_groups=2, group_score="top2", scale=1.5)
+            plan = mq.expert_plan(ids, E)
+            yield from (ids, weights, *plan)
+            up, down = (mq.mx_quantize(wg), mq.mx_quantize(wu)), mq.mx_quantize(wd)
+            h = mq.mx_experts_up(x[:T], *up, plan, out_dtype=torch.float32)
+            yield from (h, mq.mx_experts_down(h, down, plan, weights), mq.mx_experts(x[:T], *up, down, plan, weights))
+
+    assert mq._binding is not None
+    short = list(calls())
+    for module in ("mx", "experts"):
+        monkeypatch.setattr(sys.modules[f"dense_sparse_bit_amd.{module}"], "_binding", None)
+    for i, (a, b) in enumerate(zip(short, calls(), strict=True)):
+        assert torch.equal(a, b) and a.dtype == b.dtype, i
