@@ -186,8 +186,9 @@ def mx_experts_down(h, w_down: MX, plan: ExpertPlan, weights, out_dtype=torch.bf
     return y
 
 
-def mx_experts(x, w_gate: MX, w_up: MX, w_down: MX, plan: ExpertPlan, weights, out_dtype=torch.bfloat16, stream=None):
-    """A mixture's feed-forward layer of x [T, D]: mx_experts_up (its result in bf16), then
+def mx_experts(x, w_gate: MX, w_up: MX, w_down: MX, plan: ExpertPlan, weights, out_dtype=torch.bfloat16, stream=None,
+               h_dtype=torch.bfloat16):
+    """A mixture's feed-forward layer of x [T, D]: mx_experts_up (its result in h_dtype), then
     mx_experts_down."""
-    h = mx_experts_up(x, w_gate, w_up, plan, stream=stream)
+    h = mx_experts_up(x, w_gate, w_up, plan, out_dtype=h_dtype, stream=stream)
     return mx_experts_down(h, w_down, plan, weights, out_dtype=out_dtype, stream=stream)

@@ -168,3 +168,26 @@ def test_the_long_way_gives_the_same_bits(mq, monkeypatch):
         monkeypatch.setattr(sys.modules[f"dense_sparse_bit_amd.{module}"], "_binding", None)
     for i, (a, b) in enumerate(zip(short, calls(), strict=True)):
         assert torch.equal(a, b) and a.dtype == b.dtype, i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 50])
+def test_layer_rounds_h_to_the_type_asked_for(mq, T):
+    """mx_experts is mx_experts_up and mx_experts_down with h in h_dtype; bf16 by default."""
+    import torch
+    E, k, D, I = 4, 2, 136, 80
+    g = torch.Generator(device="cuda").manual_seed(T)
+    draw = lambda *shape: torch.randn(*shape, generator=g, device="cuda")
+    x, w = draw(T, D), [mq.mx_quantize(draw(*s)) for s in ((E, I, D), (E, I, D), (E, D, I))]
+    ids, weights = mq.route(draw(T, E), k)
+    plan = mq.expert_plan(ids, E)
+    layer = lambda **kw: mq.mx_experts(x, *w, plan, weights, out_dtype=torch.float32, **kw)
+    results = {}
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        h = mq.mx_experts_up(x, *w[:2], plan, out_dtype=dtype)
+        results[dtype] = mq.mx_experts_down(h, w[2], plan, weights, out_dtype=torch.float32)
+        assert torch.equal(layer(h_dtype=dtype), results[dtype]), dtype
+    assert torch.equal(layer(), results[torch.bfloat16])
+    assert not torch.equal(results[torch.bfloat16], results[torch.float32])
+    with pytest.raises(TypeError, match="float32, bfloat16 or float16"):
+        layer(h_dtype=torch.int32)
