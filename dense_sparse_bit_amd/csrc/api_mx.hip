@@ -120,14 +120,21 @@ bool few_tokens(int64_t T, int64_t k) { return T <= 16 && k <= 1024; }
 // 37.8 / 19.4; 128 experts of 2048 x 768, 8 a token: 5.8 / 12.5, 8.0 / 13.2, 13.5 / 15.9,
 // 24.2 / 20.1.
 bool one_by_one(int64_t T, int64_t k) { return T <= 8 && k <= 32; }
-// Columns of the down products that are made, and summed, at a time: even parts of at most
-// kDownBytes of fp32 rows, which the last-level cache (256 MB) holds. Measured (4096 tokens,
-// 8 of 64 experts, 4096 columns), in us: parts of 50 MB 378, 100 344, 140 316, 200 317,
-// 300 328, all at once 340.
+// Columns of the down products that are made, and summed, at a time: even parts, in whole
+// blocks of 256 columns, of at most kDownBytes of fp32 rows, which the last-level cache
+// (256 MB) holds. Where that is less than two blocks (from 102401 rows on) the cache no
+// longer helps, and narrow parts cost more launches: parts of at most 1024 columns then,
+// which also keep the workspace below that of all at once. Measured (8 of 64 experts, 4096
+// columns), in us, parts of 256 / 512 / 1024 / 1536 / 2048 / all at once: 4096 tokens (33728
+// rows) 529 / 403 / 328 / 319 / 325 / 335, 10000 847 / 769 / 770 / 790 / 773 / 767, 16384
+// (132032) 1260 / 1340 / 1276 / 1291 / 1250 / 1233, 32768 2795 / 2601 / 2510 / 2528 / 2450 /
+// 2434, 65536 5275 / 5043 / 4885 / 4920 / 4812 / 4871.
 constexpr int64_t kDownBytes = int64_t(200) << 20;
 int64_t down_cols(int64_t P, int64_t D) {
-    const int64_t parts = (P * D * 4 + kDownBytes - 1) / kDownBytes;
-    const int64_t cols = ((D + parts - 1) / (parts ? parts : 1) + 255) / 256 * 256;
+    const int64_t fit = P ? kDownBytes / (P * 4) / 256 * 256 : D + 255;
+    const int64_t most = fit >= 512 ? fit : 1024;
+    const int64_t parts = (D + most - 1) / most;
+    const int64_t cols = ((D + parts - 1) / parts + 255) / 256 * 256;
     return cols < D ? cols : (D + 3) / 4 * 4;
 }
 size_t tiles_bytes(int64_t P, int64_t E) { return round16(mq::mx_tiles_size(P, E) * 4); }

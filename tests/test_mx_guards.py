@@ -191,3 +191,42 @@ def test_layer_rounds_h_to_the_type_asked_for(mq, T):
     assert not torch.equal(results[torch.bfloat16], results[torch.float32])
     with pytest.raises(TypeError, match="float32, bfloat16 or float16"):
         layer(h_dtype=torch.int32)
+
+
+def _fp32_rows(mq, T, k, E, D, I):
+    """Bytes of a down product's workspace that hold fp32 rows."""
+    lib = mq.lib()
+    round16 = lambda n: -(-n // 16) * 16
+    P = lib.mq_plan_rows(T, k, E)
+    rest = round16(lib.mq_mx_codes_bytes(P, I)) + round16(lib.mq_mx_scales_bytes(P, I)) + \
+        round16(4 * (4 + 4 * (P // 16 // 8 + E + 2)))
+    return P, lib.mq_mx_experts_down_workspace_bytes(T, k, E, D, I) - rest
+
+
+@pytest.mark.parametrize("D", [72, 1000, 2880, 4096, 5120, 7168])
+def test_rows_of_down_products_stay_within_their_bound(mq, D):
+    """Parts of at most 200 MiB, as long as two blocks of 256 columns take no more; then of at
+    most 1024 columns. Never more columns than there are."""
+    seen = set()
+    for T in (9, 17, 300, 3000, 4096, 6000, 8192, 10000, 12500, 16384, 20000, 32768, 65536, 200000):
+        P, rows = _fp32_rows(mq, T, 8, 64, D, 256)
+        assert 0 < rows <= (P * -(-D // 4) * 4 + 3) * 4
+        small = P * 512 * 4 <= 200 << 20
+        assert rows <= (200 << 20 if small else P * 1024 * 4), (T, P, rows)
+        seen.add(small)
+    assert seen == {True, False}
+
+
+@pytest.mark.gpu
+def test_down_products_of_more_rows_than_a_part_of_the_cache_holds(mq):
+    """More than 102400 rows: two parts of at most 1024 columns, the second a shorter one."""
+    import numpy as np
+    import torch
+    from tests.test_mx_large import _check_layer
+    T, k, E, D, I = 14000, 8, 8, 1101, 40
+    rng = np.random.default_rng(5)
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    ids[rng.random((T, k)) < 0.02] = -1
+    P, rows = _fp32_rows(mq, T, k, E, D, I)
+    assert P > 102400 and rows == P * 768 * 4
+    _check_layer(mq, ids, E, D, I, torch.bfloat16, "bf16", [0, 1, 6999, 13998, 13999])
