@@ -69,6 +69,7 @@ _SIGS.update({
     "mq_mx_quantize": [_p, _int, _i64, _i64, _i64, _i64, _i64, _p, _p, _p],
     "mq_mx_dequantize": [_p, _p, _i64, _i64, _i64, _p, _int, _p],
     "mq_mx_gemm": [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _int, _p],
+    "mq_mx_gemm_way": [_i64, _i64, _i64],
     "mq_mx_linear": [_p, _int, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _int, _p, C.c_size_t, _p],
     "mq_route": [_p, _int, _i64, _i64, _i64, _p, _int, _i64, _i64, _int, _i64, _int, C.c_float, _p, _p, _p],
     "mq_expert_plan": [_p, _i64, _i64, _i64, _p, _p, _p, _p],

@@ -190,6 +190,13 @@ int mq_mx_gemm(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const ui
     return status_of(launch_product(a, st));
 }
 
+int mq_mx_gemm_way(int64_t M, int64_t N, int64_t K) {
+    const int rc = check_product(M, N, K);
+    if (rc) return rc;
+    const int plan = mq::mx_plan(M, N, K);
+    return plan == mq::kMxWide ? 3 + mq::mx_wide_pieces(M, N, K) : plan - mq::kMxOneTile;
+}
+
 size_t mq_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     return check_product(M, N, K) || on_the_way(M, N, K) ? 0 : mx_bytes(M, K);
 }

@@ -738,7 +738,7 @@ hipError_t wide(const MxGemmArgs& a, hipStream_t st) {
     const int64_t ncol = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
     int blocks = 0, block_tiles = 0;
     if (!a.tiles) {
-        block_tiles = 2 * wide_pieces((rt + 1) / 2, ncol, a.K, nullptr);
+        block_tiles = 2 * mx_wide_pieces(a.M, a.N, a.K);
         blocks = (rt + block_tiles - 1) / block_tiles;
     }
     const int64_t n = a.tiles ? mx_tiles_cap(a.M, a.E) : blocks;
@@ -779,6 +779,8 @@ int mx_plan(int64_t M, int64_t N, int64_t K) {
     wide = fmax(wide, 2.0 + 0.37 * 32 * g);
     return cost[best] < wide && rows16 <= 65535 ? best + kMxOneTile : kMxWide;
 }
+
+int mx_wide_pieces(int64_t M, int64_t N, int64_t K) { return wide_pieces((M + 31) / 32, (N + 255) / 256, K, nullptr); }
 
 hipError_t launch_mx_few(const MxGemmArgs& a, int plan, hipStream_t st) {
     if (a.x) {

@@ -104,6 +104,8 @@ hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_
 // one, two or four column tiles (0, 1, 2), or tiles of many rows.
 constexpr int kMxOneTile = -1, kMxWide = 3;
 int mx_plan(int64_t M, int64_t N, int64_t K);
+// 32-row pieces of a row block of such tiles
+int mx_wide_pieces(int64_t M, int64_t N, int64_t K);
 // a.x given: rows are quantized on the way (plan kMxOneTile, or rows of a plan's tiles)
 hipError_t launch_mx_few(const MxGemmArgs& a, int plan, hipStream_t st);
 // y[t] = sum over j of weights[t][j] * (Q(x[row_of[t][j]]) . w[expert of the row]), in one

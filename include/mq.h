@@ -363,6 +363,12 @@ int mq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t B, int
 int mq_mx_gemm(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* ws, int64_t M, int64_t N,
                int64_t K, const float* bias, void* y, int y_dtype, void* stream);
 
+/* The way that such a product takes: 0: K split over a workgroup's waves, 16 rows and 16
+ * columns a workgroup; 1, 2, 3: the same with 32 rows and 16, 32, 64 columns; 4 .. 7: tiles of
+ * 32, 64, 96, 128 rows and 256 columns. A status below 0 outside the supported sizes. The
+ * ways give the same sums in another order of additions. */
+int mq_mx_gemm_way(int64_t M, int64_t N, int64_t K);
+
 /* The same from unquantized activations x [M][K] (row stride stride_m): the bits of
  * mq_mx_quantize followed by mq_mx_gemm. workspace: device scratch of at least
  * mq_mx_linear_workspace_bytes, 16-byte aligned (may be NULL where that is 0). */
