@@ -105,3 +105,35 @@ def test_nan_stays_in_its_rows_and_columns(mq, T):
     want = torch.zeros_like(y, dtype=torch.bool)
     want[:, 9] = torch.from_numpy((ids == 3).any(1)).cuda()
     assert torch.equal(torch.isnan(y), want)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_silu_over_its_range(mq, T):
+    """silu(g) u for every half of a whole number g in [-120, 120], with gate and up exact, as
+    fp32: relative error at most (1.25 |g| + 8) 2^-24 (the exponential's argument is rounded;
+    then an exponential, a sum, a reciprocal and two products of a unit or half of one), and
+    below g = -87, where the value leaves fp32's normal range, 2^-119."""
+    import torch
+    gates = np.arange(-240, 241) / 2
+    I, D = len(gates), 32
+    w = np.zeros((I, D))
+    w[:, 0], w[:, 1] = 4, -4                                    # a peak of 4 or 6: a scale of 1
+    for i, g in enumerate(gates):
+        left, at = abs(g), 2
+        while left > 0:
+            w[i, at] = next(v for v in (6, 4, 3, 2, 1.5, 1, 0.5) if v <= left)
+            left -= w[i, at]
+            at += 1
+        w[i, 2:] *= np.sign(g)
+    assert (w.sum(1) == gates).all()
+    x = torch.ones(T, D, device="cuda")
+    gate = torch.from_numpy(w).float().cuda()[None]
+    up = torch.zeros(1, I, D, device="cuda")
+    up[:, :, 0] = 1.0
+    gate_q, up_q = mq.mx_quantize(gate), mq.mx_quantize(up)
+    assert torch.equal(mq.mx_dequantize(gate_q), gate) and torch.equal(mq.mx_dequantize(up_q), up)
+    plan = mq.expert_plan(torch.zeros(T, 1, dtype=torch.int32, device="cuda"), 1)
+    h = mq.mx_experts_up(x, gate_q, up_q, plan, out_dtype=torch.float32)[:T].double().cpu().numpy()
+    want = gates / (1 + np.exp(-gates))
+    tol = np.where(gates < -87, 2.0 ** -119, (1.25 * np.abs(gates) + 8) * 2.0 ** -24 * np.abs(want))
+    assert (np.abs(h - want) <= tol).all()
