@@ -102,7 +102,9 @@ size_t row_bytes(int64_t R, int64_t K) {
 // Whether a product quantizes its rows on the way. It saves a launch (about 3 us) and
 // costs each workgroup the whole matrix of rows. Measured, on the way / apart, in us:
 // 16 rows, 4096 x 4096: 6.9 / 7.6, N = 14336: 13.2 / 13.8, N = 4096, K = 14336: 20 / 14.8;
-// N = 28672, K = 8192: 8 rows 28.8 / 31.9, 16 rows 37 / 31.7.
+// N = 28672, K = 8192: 8 rows 28.8 / 31.9, 16 rows 37 / 31.7. Where K leaves a wave a batch and
+// part of one the rows cost it twice, which the rule does not see: N = 17408, K = 5120, on
+// weights that no cache holds, 8 rows 20.7 / 20.7, 10 25.4 / 20.9, 16 28.7 / 21.0.
 bool on_the_way(int64_t M, int64_t N, int64_t K) { return M <= 16 && M * K <= 1 << 17 && M * K <= (int64_t(1) << 31) / N; }
 
 hipError_t launch_product(const mq::MxGemmArgs& a, hipStream_t st) {
@@ -113,12 +115,13 @@ hipError_t launch_product(const mq::MxGemmArgs& a, hipStream_t st) {
 // Whether the up products split K, quantizing on the way, instead of taking tiles of many
 // rows. Measured, split / tiles, in us: 64 experts of 4096 x 1024, 8 a token: 1 token 6.8 /
 // 16.3, 8 30.7 / 32.6, 16 30.7 / 32.9, 24 38.1 / 35.5; 8 experts of 4096 x 4096, 2 a token:
-// 1 token 6.7 / 15.5, 16 24.9 / 24.8, 24 29.7 / 26.7.
+// 1 token 6.7 / 15.5, 16 24.9 / 24.8, 24 29.7 / 26.7. (All up to 4096 columns.)
 bool few_tokens(int64_t T, int64_t k) { return T <= 16 && k <= 1024; }
 // Whether the down products go token by token. As above, by token / tiles: 1 token 6.0 /
 // 13.5, 4 13.8 / 20.3, 8 25.1 / 25.1, 16 44.3 / 25.3; 5.3 / 15.3, 14.2 / 18.7, 21.2 / 18.6,
 // 37.8 / 19.4; 128 experts of 2048 x 768, 8 a token: 5.8 / 12.5, 8.0 / 13.2, 13.5 / 15.9,
-// 24.2 / 20.1.
+// 24.2 / 20.1. So 8 tokens lose 14% where experts are few and large, and win as much where
+// they are many and small.
 bool one_by_one(int64_t T, int64_t k) { return T <= 8 && k <= 32; }
 // Columns of the down products that are made, and summed, at a time: even parts, in whole
 // blocks of 256 columns, of at most kDownBytes of fp32 rows, which the last-level cache

@@ -157,9 +157,12 @@ __device__ __forceinline__ void few_run(const MxGemmArgs& a, const uint8_t* cons
 
 // One workgroup: 16 MT rows x NT column tiles of 16 (GATED: NT / 2 of each matrix), its
 // waves each a run of K; the partial sums are added through LDS in the order of the
-// waves. Bound by the weights' read where there are enough of them: one row of 8192 x 28672
-// takes 25 us (5 TB/s), of 14336 x 4096 8.5 us; of 4096 x 4096 4.2 us, most of it the latency
-// of a launch, the rows' quantization and one batch of loads.
+// waves. Bound by the weights' read where there are enough of them, in us, on weights that no
+// cache holds / that the last-level cache does: one row of 28672 x 8192 23.6 (5.3 TB/s) / 20.8,
+// 14336 x 4096 8.4 / 5.6, 17408 x 5120 12.9 / 10.6; of 4096 x 4096 4.7 / 3.6, most of it the
+// latency of a launch, the rows' quantization and one batch of loads. Sixteen quantized rows
+// of 28672 x 8192 30.2 (4.1 TB/s), of 17408 x 5120 17.5 (2.7 TB/s: eight waves have five groups
+// each, so every second batch is mostly repeats).
 template <typename XT, int NT, int MT, int RB, bool GATED>
 __global__ __launch_bounds__(512) void k_mx_few(MxGemmArgs a) {
     constexpr int NC = GATED ? NT / 2 : NT;
@@ -758,8 +761,8 @@ hipError_t wide(const MxGemmArgs& a, hipStream_t st) {
 // 16 rows and one column tile a workgroup, 32 rows and one, two or four, and tiles of many
 // rows (the fourth way's workgroups are two to a CU by their LDS, so it goes by whole rounds
 // of 512). Few workgroups of the last take a third of a us or more for a step of K: the
-// latency of weights that no cache holds. Over 110 sizes (10 to 800 rows, K = 512 to 14336)
-// the choice is within 13% of the fastest way, 0.5% on average. E.g. (in this order) 64 x 1024 x 4096: 3.9, 4.4,
+// latency of weights that no cache holds. Over the 110 sizes that the fits were made of (10 to
+// 800 rows, K = 512 to 14336) the choice is within 13% of the fastest way, 0.6% on average. E.g. (in this order) 64 x 1024 x 4096: 3.9, 4.4,
 // 6.0, 7.7, 11.0; 256 x 4096 x 14336: 66.7, 53.1, 41.6, 33.6, 47.0; 96 x 14336 x 4096: 27.2, 23.0,
 // 20.9, 21.6, 16.4.
 int mx_plan(int64_t M, int64_t N, int64_t K) {

@@ -84,10 +84,12 @@ __device__ inline int first_best(uint64_t key) {
 // One wave per token; lane l holds the experts V l .. V l + V - 1, so that the first
 // lane, and in it the first expert, of a tie is the lowest index. BIAS: keys are scores
 // with their bias, in 64 bits; else the logits themselves, and only the chosen experts'
-// scores are computed (softmax: and the sum). A key of 0 is a masked expert. Bound by
-// the latency of k rounds of a maximum over the wave: lane moves in the vector unit keep
-// a round near 200 cycles (through LDS permutes, 64-bit values: 1500). One token of 128
-// experts: 3.5 us; 4096 tokens of 256 in 8 groups, sigmoid and bias: 11.7 us.
+// scores are computed (softmax: and the sum). A key of 0 is a masked expert. One token is
+// bound by the latency of k rounds of a maximum over the wave: lane moves in the vector unit
+// keep a round near 200 cycles (through LDS permutes, 64-bit values: 1500). Batches are bound
+// by vector instructions, 64-bit exponentials and divisions most of all: 4096 tokens of 256
+// experts in 8 groups, sigmoid and bias, take 983 a token, and the vector units are busy for
+// 71% of the 11.7 us. One token of 128 experts: 3.5 us.
 template <typename T, int V, bool BIAS>
 __global__ __launch_bounds__(64 * kTokens) void k_route(RouteArgs a) {
     using Key = typename std::conditional<BIAS, uint64_t, uint32_t>::type;
