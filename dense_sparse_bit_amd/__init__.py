@@ -77,12 +77,26 @@ _SIGS.update({
                          C.c_size_t, _p],
     "mq_mx_experts_down": [_p, _int, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _int, _p, C.c_size_t, _p],
 })
+_SIGS.update({
+    "mq_w4_quantize": [_p, _int, _i64, _i64, _i64, _i64, _i64, _int, _int, _p, _p, _p, _p],
+    "mq_w4_pack": [_p, _i64, _i64, _i64, _i64, _i64, _int, _p, _p, _p, _p, _p, _p],
+    "mq_w4_dequantize": [_p, _p, _p, _int, _i64, _i64, _i64, _int, _p, _int, _p],
+    "mq_w4_linear": [_p, _int, _i64, _p, _p, _p, _int, _int, _i64, _i64, _i64, _p, _p, _int, _p, C.c_size_t, _p],
+    "mq_w4_experts": [_p, _int, _i64, _int, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _int, _int, _p, _int, _p,
+                      C.c_size_t, _p],
+    "mq_experts_gather": [_p, _int, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _int, _p, _p, _p],
+    "mq_experts_combine": [_p, _int, _i64, _i64, _i64, _i64, _p, _p, _p, _int, _p, _i64, _p, _p],
+})
 _SIZES = {
     "mq_mx_codes_bytes": [_i64, _i64],
     "mq_mx_scales_bytes": [_i64, _i64],
     "mq_mx_linear_workspace_bytes": [_i64, _i64, _i64],
     "mq_mx_experts_up_workspace_bytes": [_i64, _i64, _i64, _i64, _i64],
     "mq_mx_experts_down_workspace_bytes": [_i64, _i64, _i64, _i64, _i64],
+    "mq_w4_codes_bytes": [_i64, _i64],
+    "mq_w4_scales_bytes": [_i64, _i64, _int],
+    "mq_w4_linear_workspace_bytes": [_i64, _i64, _i64, _int, _int],
+    "mq_w4_experts_workspace_bytes": [_i64, _i64, _i64, _i64, _i64, _int, _int, _int],
 }
 for _name, _args in _SIZES.items():
     getattr(_lib, _name).argtypes = _args
@@ -583,5 +597,6 @@ def forward_layer(x, w, k_blocks: int, bn: int = 64, out_dtype=torch.bfloat16, m
 
 
 from .mx import MX, mx_dequantize, mx_linear, mx_quantize  # noqa: E402
-from .experts import (ExpertPlan, expert_plan, mx_experts, mx_experts_down, mx_experts_up,  # noqa: E402
-                      plan_rows, route)
+from .experts import (ExpertPlan, expert_plan, experts_combine, experts_gather, mx_experts,  # noqa: E402
+                      mx_experts_down, mx_experts_up, plan_rows, route)
+from .w4 import W4, w4_dequantize, w4_experts_linear, w4_linear, w4_pack, w4_quantize  # noqa: E402

@@ -40,6 +40,10 @@ SOURCES = {
     "mx_gemm.hip": [],
     "route.hip": ["-ffp-contract=off"],
     "api_mx.hip": [],
+    "w4_quant.hip": [],
+    "w4_gemm.hip": [],
+    "rows.hip": [],
+    "api_w4.hip": [],
 }
 
 

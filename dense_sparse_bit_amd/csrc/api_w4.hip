@@ -1,0 +1,242 @@
+// C ABI of the group-scaled 4-bit operators and of the calls between tokens and their
+// experts' rows: argument checks, then kernel launches. Declarations and the meaning of
+// every argument are in include/mq.h.
+#include <stdint.h>
+
+#include "../../include/mq.h"
+#include "mx_internal.h"
+#include "w4_internal.h"
+
+namespace {
+
+int status_of(hipError_t e) { return e == hipSuccess ? MQ_OK : MQ_ERR_HIP; }
+bool bad_type(int d) { return d != MQ_F32 && d != MQ_BF16 && d != MQ_F16; }
+bool bad_scales(int d) { return d != MQ_BF16 && d != MQ_F16; }
+bool bad_group(int g) { return g != 32 && g != 64 && g != 128; }
+int64_t type_size(int d) { return d == MQ_F32 ? 4 : 2; }
+bool off(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+constexpr int64_t kMaxRows = int64_t(1) << 24;
+constexpr int64_t kMaxCols = int64_t(1) << 20;
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kMaxSlots = int64_t(1) << 27;
+
+int check_matrix(int64_t B, int64_t R, int64_t K, int group) {
+    if (B < 0 || R < 0 || K <= 0 || bad_group(group)) return MQ_ERR_INVALID_ARG;
+    if (B > kMaxBatch || R > kMaxRows || K > kMaxCols || B * R > kMaxElements / K) return MQ_ERR_UNSUPPORTED;
+    return MQ_OK;
+}
+
+// zeros may be NULL
+int check_weights(const void* codes, const void* scales, const void* zeros, int scale_dtype) {
+    return !codes || !scales || off(codes, 16) || off(scales, 16) || off(zeros, 16) || bad_scales(scale_dtype)
+               ? MQ_ERR_INVALID_ARG
+               : MQ_OK;
+}
+
+int check_product(int64_t M, int64_t N, int64_t K, int group) {
+    if (M < 0 || N <= 0 || K <= 0 || bad_group(group)) return MQ_ERR_INVALID_ARG;
+    if (M > kMaxRows || N > kMaxRows || K > kMaxCols || N > kMaxElements / K || (M && N > kMaxElements / M))
+        return MQ_ERR_UNSUPPORTED;
+    return MQ_OK;
+}
+
+int check_slots(int64_t T, int64_t k, int64_t E) {
+    if (T < 0 || k <= 0 || E <= 0) return MQ_ERR_INVALID_ARG;
+    if (E > MQ_MAX_EXPERTS || T > kMaxSlots / k) return MQ_ERR_UNSUPPORTED;
+    return MQ_OK;
+}
+
+int check_experts(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int group) {
+    const int rc = check_slots(T, k, E);
+    if (rc) return rc;
+    const int product = check_product(mq::plan_rows(T, k, E), N, K, group);
+    return product ? product : check_matrix(E, N, K, group);
+}
+
+int check_rows(int64_t T, int64_t k, int64_t E, int64_t D) {
+    const int rc = check_slots(T, k, E);
+    if (rc) return rc;
+    if (D <= 0) return MQ_ERR_INVALID_ARG;
+    return D > kMaxCols ? MQ_ERR_UNSUPPORTED : MQ_OK;
+}
+
+mq::W4QuantArgs matrix(int64_t B, int64_t R, int64_t K, int group, const uint8_t* codes, const void* scales, const void* zeros) {
+    mq::W4QuantArgs a = {};
+    a.B = B;
+    a.R = R;
+    a.K = static_cast<int>(K);
+    a.group = group;
+    a.codes = const_cast<uint8_t*>(codes);
+    a.scales = static_cast<uint16_t*>(const_cast<void*>(scales));
+    a.zeros = static_cast<uint16_t*>(const_cast<void*>(zeros));
+    return a;
+}
+
+mq::W4GemmArgs product(const void* x, int x_dtype, int64_t stride_x, const uint8_t* codes, const void* scales, const void* zeros,
+                       int scale_dtype, int group, int64_t M, int64_t N, int64_t K, void* y, int y_dtype) {
+    mq::W4GemmArgs a = {};
+    a.x = x;
+    a.x_dtype = x_dtype;
+    a.stride_x = stride_x;
+    a.codes = codes;
+    a.scales = static_cast<const uint16_t*>(scales);
+    a.zeros = static_cast<const uint16_t*>(zeros);
+    a.scale_dtype = scale_dtype;
+    a.group = group;
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.y = y;
+    a.y_dtype = y_dtype;
+    return a;
+}
+
+mq::RowsArgs rows_of(int64_t T, int64_t k, int64_t E, int64_t D, const void* x, int x_dtype, int64_t stride_t, const void* rows,
+                     int rows_dtype, const int32_t* row_of, const float* weights, const void* other, float* dots) {
+    mq::RowsArgs a = {};
+    a.x = x;
+    a.x_dtype = x_dtype;
+    a.stride_t = stride_t;
+    a.rows = rows;
+    a.rows_dtype = rows_dtype;
+    a.T = T;
+    a.P = mq::plan_rows(T, k, E);
+    a.k = static_cast<int>(k);
+    a.D = static_cast<int>(D);
+    a.row_of = row_of;
+    a.weights = weights;
+    a.other = other;
+    a.dots = dots;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mq_w4_codes_bytes(int64_t R, int64_t K) {
+    return check_matrix(1, R, K, 128) ? 0 : static_cast<size_t>(mq::w4_codes_size(R, K));
+}
+
+size_t mq_w4_scales_bytes(int64_t R, int64_t K, int group) {
+    return check_matrix(1, R, K, group) ? 0 : static_cast<size_t>(mq::w4_scales_size(R, K, group));
+}
+
+int mq_w4_quantize(const void* x, int x_dtype, int64_t B, int64_t stride_b, int64_t R, int64_t stride_r, int64_t K, int group,
+                   int scale_dtype, uint8_t* codes, void* scales, void* zeros, void* stream) {
+    int rc = check_matrix(B, R, K, group);
+    if (rc) return rc;
+    if (bad_type(x_dtype) || bad_scales(scale_dtype) || stride_b < 0 || stride_r < 0) return MQ_ERR_INVALID_ARG;
+    if (B == 0 || R == 0) return MQ_OK;
+    if (!x || off(x, type_size(x_dtype))) return MQ_ERR_INVALID_ARG;
+    if ((rc = check_weights(codes, scales, zeros, scale_dtype))) return rc;
+    mq::W4QuantArgs a = matrix(B, R, K, group, codes, scales, zeros);
+    a.x = x;
+    a.dtype = x_dtype;
+    a.stride_b = stride_b;
+    a.stride_r = stride_r;
+    a.scale_dtype = scale_dtype;
+    return status_of(mq::launch_w4_quant(a, static_cast<hipStream_t>(stream)));
+}
+
+int mq_w4_pack(const uint8_t* c, int64_t B, int64_t stride_b, int64_t R, int64_t stride_r, int64_t K, int group, const void* s,
+               const void* z, uint8_t* codes, void* scales, void* zeros, void* stream) {
+    int rc = check_matrix(B, R, K, group);
+    if (rc) return rc;
+    if (stride_b < 0 || stride_r < 0) return MQ_ERR_INVALID_ARG;
+    if (B == 0 || R == 0) return MQ_OK;
+    if (!c || !s || off(s, 2) || off(z, 2) || (z == nullptr) != (zeros == nullptr)) return MQ_ERR_INVALID_ARG;
+    if ((rc = check_weights(codes, scales, zeros, MQ_F16))) return rc;
+    mq::W4QuantArgs a = matrix(B, R, K, group, codes, scales, zeros);
+    a.x = c;
+    a.stride_b = stride_b;
+    a.stride_r = stride_r;
+    a.s = static_cast<const uint16_t*>(s);
+    a.z = static_cast<const uint16_t*>(z);
+    return status_of(mq::launch_w4_pack(a, static_cast<hipStream_t>(stream)));
+}
+
+int mq_w4_dequantize(const uint8_t* codes, const void* scales, const void* zeros, int scale_dtype, int64_t B, int64_t R,
+                     int64_t K, int group, void* y, int y_dtype, void* stream) {
+    int rc = check_matrix(B, R, K, group);
+    if (rc) return rc;
+    if (bad_type(y_dtype) || bad_scales(scale_dtype)) return MQ_ERR_INVALID_ARG;
+    if (B == 0 || R == 0) return MQ_OK;
+    if ((rc = check_weights(codes, scales, zeros, scale_dtype))) return rc;
+    if (!y || off(y, 16)) return MQ_ERR_INVALID_ARG;
+    mq::W4QuantArgs a = matrix(B, R, K, group, codes, scales, zeros);
+    a.scale_dtype = scale_dtype;
+    return status_of(mq::launch_w4_dequant(a, y, y_dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t mq_w4_linear_workspace_bytes(int64_t, int64_t, int64_t, int, int) { return 0; }
+
+int mq_w4_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* codes, const void* scales, const void* zeros,
+                 int scale_dtype, int group, int64_t M, int64_t N, int64_t K, const float* bias, void* y, int y_dtype,
+                 void*, size_t, void* stream) {
+    int rc = check_product(M, N, K, group);
+    if (rc) return rc;
+    if (bad_type(x_dtype) || bad_type(y_dtype) || bad_scales(scale_dtype) || stride_m < 0 || off(bias, 4))
+        return MQ_ERR_INVALID_ARG;
+    if (M == 0) return MQ_OK;
+    if (!x || off(x, type_size(x_dtype)) || !y || off(y, 16)) return MQ_ERR_INVALID_ARG;
+    if ((rc = check_weights(codes, scales, zeros, scale_dtype))) return rc;
+    mq::W4GemmArgs a = product(x, x_dtype, stride_m, codes, scales, zeros, scale_dtype, group, M, N, K, y, y_dtype);
+    a.bias = bias;
+    return status_of(mq::launch_w4_few(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t mq_w4_experts_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int, int, int) { return 0; }
+
+int mq_w4_experts(const void* x, int x_dtype, int64_t stride_r, int by_token, int64_t T, int64_t k, int64_t E, int64_t N,
+                  int64_t K, const int32_t* offsets, const int32_t* row_token, const uint8_t* codes, const void* scales,
+                  const void* zeros, int scale_dtype, int group, void* y, int y_dtype, void*, size_t, void* stream) {
+    int rc = check_experts(T, k, E, N, K, group);
+    if (rc) return rc;
+    if (bad_type(x_dtype) || bad_type(y_dtype) || bad_scales(scale_dtype) || stride_r < 0) return MQ_ERR_INVALID_ARG;
+    if (T == 0) return MQ_OK;
+    if (!x || off(x, type_size(x_dtype)) || !y || off(y, 16)) return MQ_ERR_INVALID_ARG;
+    if (!offsets || off(offsets, 4) || !row_token || off(row_token, 4)) return MQ_ERR_INVALID_ARG;
+    if ((rc = check_weights(codes, scales, zeros, scale_dtype))) return rc;
+    mq::W4GemmArgs a = product(x, x_dtype, stride_r, codes, scales, zeros, scale_dtype, group, mq::plan_rows(T, k, E), N, K, y,
+                               y_dtype);
+    a.offsets = offsets;
+    a.row_token = row_token;
+    a.by_token = by_token != 0;
+    a.E = static_cast<int>(E);
+    a.T = static_cast<int>(T);
+    return status_of(mq::launch_w4_few(a, static_cast<hipStream_t>(stream)));
+}
+
+int mq_experts_gather(const void* x, int x_dtype, int64_t stride_t, int64_t T, int64_t k, int64_t E, int64_t D,
+                      const int32_t* row_token, const int32_t* row_of, const float* weights, void* rows, int rows_dtype,
+                      const void* other, float* dots, void* stream) {
+    const int rc = check_rows(T, k, E, D);
+    if (rc) return rc;
+    if (bad_type(x_dtype) || bad_type(rows_dtype) || stride_t < 0 || off(weights, 4)) return MQ_ERR_INVALID_ARG;
+    if ((other == nullptr) != (dots == nullptr) || off(other, type_size(rows_dtype)) || off(dots, 4)) return MQ_ERR_INVALID_ARG;
+    if (T == 0) return MQ_OK;
+    if (!x || off(x, type_size(x_dtype)) || !rows || off(rows, 16)) return MQ_ERR_INVALID_ARG;
+    if (!row_token || off(row_token, 4) || !row_of || off(row_of, 4)) return MQ_ERR_INVALID_ARG;
+    mq::RowsArgs a = rows_of(T, k, E, D, x, x_dtype, stride_t, rows, rows_dtype, row_of, weights, other, dots);
+    a.row_token = row_token;
+    return status_of(mq::launch_rows_gather(a, static_cast<hipStream_t>(stream)));
+}
+
+int mq_experts_combine(const void* rows, int rows_dtype, int64_t T, int64_t k, int64_t E, int64_t D, const int32_t* row_of,
+                       const float* weights, void* x, int x_dtype, const void* other,
+                       int64_t stride_o, float* dots, void* stream) {
+    const int rc = check_rows(T, k, E, D);
+    if (rc) return rc;
+    if (bad_type(x_dtype) || bad_type(rows_dtype) || off(weights, 4) || stride_o < 0) return MQ_ERR_INVALID_ARG;
+    if ((other == nullptr) != (dots == nullptr) || off(other, type_size(x_dtype)) || off(dots, 4)) return MQ_ERR_INVALID_ARG;
+    if (T == 0) return MQ_OK;
+    if (!rows || off(rows, type_size(rows_dtype)) || !x || off(x, 16) || !row_of || off(row_of, 4)) return MQ_ERR_INVALID_ARG;
+    mq::RowsArgs a = rows_of(T, k, E, D, x, x_dtype, D, rows, rows_dtype, row_of, weights, other, dots);
+    a.stride_o = stride_o;
+    return status_of(mq::launch_rows_combine(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,4 +1,5 @@
-// The short way from Python to the microscaled and routing calls (include/mq.h).
+// The short way from Python to the microscaled, group-scaled, routing and experts' calls
+// (include/mq.h).
 //
 // A call on a few tokens takes the GPU 3 to 10 us, and its way through Python's own
 // checks, ctypes and torch's allocation functions took longer than that. Each function
@@ -12,6 +13,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -32,6 +34,7 @@ using at::ScalarType;
 
 PyTypeObject* mx_type = nullptr;
 PyTypeObject* plan_type = nullptr;
+PyTypeObject* w4_type = nullptr;
 
 struct No {};                                      // not this way
 
@@ -312,6 +315,224 @@ PyObject* experts_down(PyObject* const* a) {
     return wrapped(a[5], y);
 }
 
+// no gradient is wanted of it
+const at::Tensor& plain(const at::Tensor& t) {
+    need(!t.requires_grad() || !at::GradMode::is_enabled());
+    return t;
+}
+
+int group_of(PyObject* o) {
+    const int64_t g = PyBool_Check(o) ? 0 : integer(o);
+    need(g == 32 || g == 64 || g == 128);
+    return static_cast<int>(g);
+}
+
+ScalarType scale_type(ScalarType t) {
+    need(t == ScalarType::Half || t == ScalarType::BFloat16);
+    return t;
+}
+
+struct Group4 {
+    const uint8_t* codes;
+    const void *scales, *zeros;
+    ScalarType type;
+    int64_t rows, cols;
+    int group;
+};
+
+struct Sizes4 {
+    int64_t c[4], s[5];
+    int skip;
+    Sizes4(int64_t batch, int64_t rows, int64_t cols, int group)
+        : c{batch, (rows + 15) / 16, (cols + 127) / 128, 1024}, s{batch, (rows + 15) / 16, (cols + 511) / 512, 16, 512 / group},
+          skip(batch < 0 ? 1 : 0) {}
+    at::IntArrayRef codes() const { return {c + skip, c + 4}; }
+    at::IntArrayRef scales() const { return {s + skip, s + 5}; }
+};
+
+Group4 group4(const Here& here, PyObject* o, int64_t batch = -1) {
+    need(whole(o, w4_type, 6));
+    Group4 m;
+    m.rows = integer(PyTuple_GET_ITEM(o, 3));
+    m.cols = integer(PyTuple_GET_ITEM(o, 4));
+    m.group = group_of(PyTuple_GET_ITEM(o, 5));
+    const Sizes4 size(batch, m.rows, m.cols, m.group);
+    m.codes = contiguous(here, PyTuple_GET_ITEM(o, 0), ScalarType::Byte, size.codes()).const_data_ptr<uint8_t>();
+    m.type = scale_type(tensor(PyTuple_GET_ITEM(o, 1)).scalar_type());
+    m.scales = contiguous(here, PyTuple_GET_ITEM(o, 1), m.type, size.scales()).const_data_ptr();
+    PyObject* const z = PyTuple_GET_ITEM(o, 2);
+    m.zeros = z == Py_None ? nullptr : contiguous(here, z, m.type, size.scales()).const_data_ptr();
+    return m;
+}
+
+// a new W4's tensors, and the tuple of them
+struct New4 {
+    at::Tensor codes, scales, zeros;
+    New4(const Here& here, const Sizes4& size, ScalarType type, bool z)
+        : codes(here.make(size.codes(), ScalarType::Byte)), scales(here.make(size.scales(), type)) {
+        if (z) zeros = here.make(size.scales(), type);
+    }
+    void* zeros_data() const { return zeros.defined() ? data(zeros) : nullptr; }
+    PyObject* tuple(int64_t rows, int64_t cols, int group) const {
+        PyObject* z = Py_None;
+        if (zeros.defined()) z = THPVariable_Wrap(zeros);
+        else Py_INCREF(z);
+        return named(w4_type, {THPVariable_Wrap(codes), THPVariable_Wrap(scales), z, PyLong_FromLongLong(rows),
+                               PyLong_FromLongLong(cols), PyLong_FromLong(group)});
+    }
+};
+
+// w4_quantize(x, group, zeros, scale_dtype, out)
+PyObject* w4_quantize(PyObject* const* a) {
+    const Here here;
+    const bool batched = tensor(a[0]).dim() == 3;
+    const at::Tensor& x = input(here, a[0], batched ? 3 : 2);
+    const int group = group_of(a[1]), z = PyObject_IsTrue(a[2]);
+    need(z >= 0 && a[4] == Py_None && x.size(-1) > 0);
+    const ScalarType type = scale_type(dtype_of(a[3]));
+    const int64_t B = batched ? x.size(0) : 1, R = x.size(-2), K = x.size(-1);
+    const New4 w(here, Sizes4(batched ? B : -1, R, K, group), type, z != 0);
+    need(mq_w4_quantize(data(x), type_code(x.scalar_type()), B, batched ? x.stride(0) : 0, R, x.stride(-2), K, group,
+                        type_code(type), static_cast<uint8_t*>(data(w.codes)), data(w.scales), w.zeros_data(), here.stream()) == MQ_OK);
+    return w.tuple(R, K, group);
+}
+
+// w4_pack(codes, scales, zeros, group)
+PyObject* w4_pack(PyObject* const* a) {
+    const Here here;
+    const bool batched = tensor(a[0]).dim() == 3;
+    const at::Tensor& c = input(here, a[0], batched ? 3 : 2);
+    const int group = group_of(a[3]);
+    const int64_t B = batched ? c.size(0) : 1, R = c.size(-2), K = c.size(-1), n = (K + group - 1) / group;
+    need(c.scalar_type() == ScalarType::Byte && K > 0);
+    const ScalarType type = scale_type(tensor(a[1]).scalar_type());
+    const int64_t given[3] = {B, R, n};
+    const at::IntArrayRef per(given + (batched ? 0 : 1), given + 3);
+    const void* const s = contiguous(here, a[1], type, per).const_data_ptr();
+    const void* const z = a[2] == Py_None ? nullptr : contiguous(here, a[2], type, per).const_data_ptr();
+    const New4 w(here, Sizes4(batched ? B : -1, R, K, group), type, a[2] != Py_None);
+    need(mq_w4_pack(c.const_data_ptr<uint8_t>(), B, batched ? c.stride(0) : 0, R, c.stride(-2), K, group, s, z,
+                    static_cast<uint8_t*>(data(w.codes)), data(w.scales), w.zeros_data(), here.stream()) == MQ_OK);
+    return w.tuple(R, K, group);
+}
+
+// w4_dequantize(a, dtype, out)
+PyObject* w4_dequantize(PyObject* const* a) {
+    const Here here;
+    need(whole(a[0], w4_type, 6));
+    const at::Tensor& c = tensor(PyTuple_GET_ITEM(a[0], 0));
+    const bool batched = c.dim() == 4;
+    const int64_t B = batched ? c.size(0) : 1;
+    const Group4 m = group4(here, a[0], batched ? B : -1);
+    const int64_t size[3] = {B, m.rows, m.cols};
+    const at::Tensor y = output(here, a[2], a[1], {size + (batched ? 0 : 1), size + 3});
+    need(mq_w4_dequantize(m.codes, m.scales, m.zeros, type_code(m.type), B, m.rows, m.cols, m.group, data(y),
+                          type_code(y.scalar_type()), here.stream()) == MQ_OK);
+    return wrapped(a[2], y);
+}
+
+// w4_linear(x, w, bias, out_dtype, y)
+PyObject* w4_linear(PyObject* const* a) {
+    const Here here;
+    const at::Tensor& x = plain(input(here, a[0], 2));
+    const Group4 w = group4(here, a[1]);
+    const float* bias = a[2] == Py_None ? nullptr : plain(contiguous(here, a[2], ScalarType::Float, {w.rows})).const_data_ptr<float>();
+    need(x.size(1) == w.cols);
+    const int64_t M = x.size(0);
+    const int code = type_code(x.scalar_type());
+    const at::Tensor y = output(here, a[4], a[3], {M, w.rows});
+    const size_t bytes = mq_w4_linear_workspace_bytes(M, w.rows, w.cols, code, w.group);
+    at::Tensor work;
+    if (bytes) work = here.make({static_cast<int64_t>(bytes)}, ScalarType::Byte);
+    need(mq_w4_linear(data(x), code, x.stride(0), w.codes, w.scales, w.zeros, type_code(w.type), w.group, M, w.rows, w.cols, bias,
+                      data(y), type_code(y.scalar_type()), bytes ? data(work) : nullptr, bytes, here.stream()) == MQ_OK);
+    return wrapped(a[4], y);
+}
+
+// w4_experts(x, w, plan, by_token, out_dtype, y)
+PyObject* w4_experts(PyObject* const* a) {
+    const Here here;
+    const at::Tensor& x = plain(input(here, a[0], 2));
+    const Plan p = plan(here, a[2]);
+    const Group4 w = group4(here, a[1], p.E);
+    const int by_token = PyObject_IsTrue(a[3]), code = type_code(x.scalar_type());
+    need(by_token >= 0 && x.size(0) == (by_token ? p.T : p.rows) && x.size(1) == w.cols);
+    const at::Tensor y = output(here, a[5], a[4], {p.rows, w.rows});
+    const size_t bytes = mq_w4_experts_workspace_bytes(p.T, p.k, p.E, w.rows, w.cols, by_token, code, w.group);
+    at::Tensor work;
+    if (bytes) work = here.make({static_cast<int64_t>(bytes)}, ScalarType::Byte);
+    need(mq_w4_experts(data(x), code, x.stride(0), by_token, p.T, p.k, p.E, w.rows, w.cols, p.offsets, p.row_token, w.codes,
+                       w.scales, w.zeros, type_code(w.type), w.group, data(y), type_code(y.scalar_type()),
+                       bytes ? data(work) : nullptr, bytes, here.stream()) == MQ_OK);
+    return wrapped(a[5], y);
+}
+
+const float* weights_of(const Here& here, PyObject* o, const Plan& p) {
+    return o == Py_None ? nullptr : plain(contiguous(here, o, ScalarType::Float, {p.T, p.k})).const_data_ptr<float>();
+}
+
+// (y, dots), or y alone
+PyObject* with_dots(PyObject* given, const at::Tensor& y, const at::Tensor& dots) {
+    if (!dots.defined()) return wrapped(given, y);
+    PyObject* both = PyTuple_New(2);
+    if (!both) return nullptr;
+    PyTuple_SET_ITEM(both, 0, wrapped(given, y));
+    PyTuple_SET_ITEM(both, 1, THPVariable_Wrap(dots));
+    return both;
+}
+
+// an output of `type`, or of the type `same` where that is None
+at::Tensor output_as(const Here& here, PyObject* o, PyObject* type, ScalarType same, at::IntArrayRef size) {
+    return o == Py_None && type == Py_None ? here.make(size, same) : output(here, o, type, size);
+}
+
+// gather(x, plan, weights, dtype, rows, other)
+PyObject* gather(PyObject* const* a) {
+    const Here here;
+    const at::Tensor& x = plain(input(here, a[0], 2));
+    const Plan p = plan(here, a[1]);
+    const int64_t D = x.size(1);
+    const int code = type_code(x.scalar_type());
+    need(x.size(0) == p.T && D > 0);
+    const float* const weights = weights_of(here, a[2], p);
+    const at::Tensor rows = output_as(here, a[4], a[3], x.scalar_type(), {p.rows, D});
+    const void* other = nullptr;
+    at::Tensor dots;
+    if (a[5] != Py_None) {
+        other = contiguous(here, a[5], rows.scalar_type(), {p.rows, D}).const_data_ptr();
+        dots = here.make({p.T, p.k}, ScalarType::Float);
+    }
+    need(mq_experts_gather(data(x), code, x.stride(0), p.T, p.k, p.E, D, p.row_token, p.row_of, weights, data(rows),
+                           type_code(rows.scalar_type()), other, other ? static_cast<float*>(data(dots)) : nullptr,
+                           here.stream()) == MQ_OK);
+    return with_dots(a[4], rows, dots);
+}
+
+// combine(rows, plan, weights, dtype, y, other)
+PyObject* combine(PyObject* const* a) {
+    const Here here;
+    const Plan p = plan(here, a[1]);
+    const at::Tensor& rows = plain(input(here, a[0], 2));
+    const int64_t D = rows.size(1);
+    const int code = type_code(rows.scalar_type());
+    need(rows.size(0) == p.rows && D > 0 && rows.is_contiguous());
+    const float* const weights = weights_of(here, a[2], p);
+    const at::Tensor y = output_as(here, a[4], a[3], rows.scalar_type(), {p.T, D});
+    const void* other = nullptr;
+    int64_t stride = 0;
+    at::Tensor dots;
+    if (a[5] != Py_None) {
+        const at::Tensor& o = input(here, a[5], 2);
+        need(o.scalar_type() == y.scalar_type() && o.size(0) == p.T && o.size(1) == D);
+        other = o.const_data_ptr();
+        stride = o.stride(0);
+        dots = here.make({p.T, p.k}, ScalarType::Float);
+    }
+    need(mq_experts_combine(data(rows), code, p.T, p.k, p.E, D, p.row_of, weights, data(y), type_code(y.scalar_type()), other, stride,
+                            other ? static_cast<float*>(data(dots)) : nullptr, here.stream()) == MQ_OK);
+    return with_dots(a[4], y, dots);
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     try {
@@ -338,6 +559,17 @@ PyObject* types(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+// types_w4(W4)
+PyObject* types_w4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    if (n != 1 || !PyType_Check(args[0]) || !PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(args[0]), &PyTuple_Type)) {
+        PyErr_SetString(PyExc_TypeError, "a tuple type is needed");
+        return nullptr;
+    }
+    Py_INCREF(args[0]);
+    w4_type = reinterpret_cast<PyTypeObject*>(args[0]);
+    Py_RETURN_NONE;
+}
+
 #define ENTRY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     {"types", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(types)), METH_FASTCALL, nullptr},
@@ -348,6 +580,14 @@ PyMethodDef methods[] = {
     ENTRY(expert_plan, 2),
     ENTRY(experts_up, 6),
     ENTRY(experts_down, 6),
+    {"types_w4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(types_w4)), METH_FASTCALL, nullptr},
+    ENTRY(w4_quantize, 5),
+    ENTRY(w4_pack, 4),
+    ENTRY(w4_dequantize, 3),
+    ENTRY(w4_linear, 5),
+    ENTRY(w4_experts, 6),
+    ENTRY(gather, 6),
+    ENTRY(combine, 6),
     {nullptr, nullptr, 0, nullptr},
 };
 

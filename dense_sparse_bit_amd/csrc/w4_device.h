@@ -1,0 +1,82 @@
+// Device helpers of the group-scaled 4-bit operators.
+#pragma once
+
+#include "mx_device.h"
+
+namespace mq {
+
+typedef __bf16 w4_b8 __attribute__((ext_vector_type(8)));
+typedef _Float16 w4_h8 __attribute__((ext_vector_type(8)));
+typedef uint32_t w4_u4 __attribute__((ext_vector_type(4)));
+
+// A 16-bit scale or zero point. Both conversions and a select: the type is the same for
+// all, but a branch would keep loads from being in flight together.
+__device__ __forceinline__ float w4_float(uint32_t bits, bool bf) {
+    const float h = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<unsigned short>(bits)));
+    return bf ? __uint_as_float(bits << 16) : h;
+}
+
+__device__ __forceinline__ uint32_t w4_bits(float v, bool bf) {
+    return bf ? __builtin_bit_cast(unsigned short, static_cast<__bf16>(v)) : __builtin_bit_cast(unsigned short, static_cast<_Float16>(v));
+}
+
+template <typename T>
+__device__ __forceinline__ void w4_values(const MxRaw8<T>& r, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r.v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (__is_same(T, __bf16)) {
+                v[2 * i] = __uint_as_float(r.w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+            } else {
+                const mx_h2 h = __builtin_bit_cast(mx_h2, r.w[i]);
+                v[2 * i] = static_cast<float>(h.x);
+                v[2 * i + 1] = static_cast<float>(h.y);
+            }
+        }
+    }
+}
+
+// `have` of eight values to p, rounded; rows need no alignment beyond their type's.
+template <typename T>
+__device__ __forceinline__ void w4_store8(T* p, int have, const float (&v)[8]) {
+    if (have >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            typedef float Out __attribute__((ext_vector_type(4), aligned(4)));
+            *reinterpret_cast<Out*>(p) = Out{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<Out*>(p + 4) = Out{v[4], v[5], v[6], v[7]};
+        } else {
+            typedef uint32_t Out __attribute__((ext_vector_type(4), aligned(2)));
+            *reinterpret_cast<Out*>(p) = Out{mx_pack2<T>(v[0], v[1]), mx_pack2<T>(v[2], v[3]), mx_pack2<T>(v[4], v[5]),
+                                             mx_pack2<T>(v[6], v[7])};
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < have) p[j] = mx_round<T>(v[j]);
+    }
+}
+
+// Reductions over the lanes of a group: 4, 8 or 16 neighbours hold 32, 64 or 128 inputs.
+// (Lane moves within four, then across halves of eight and of sixteen by mirroring.)
+template <typename F>
+__device__ __forceinline__ int w4_over_group(int v, int group, F f) {
+    v = f(v, __builtin_amdgcn_mov_dpp(v, 0xB1, 0xf, 0xf, true));
+    v = f(v, __builtin_amdgcn_mov_dpp(v, 0x4E, 0xf, 0xf, true));
+    if (group >= 64) v = f(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true));
+    if (group >= 128) v = f(v, __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true));
+    return v;
+}
+
+// The word of eight codes: input i in the low half of byte i, or the high half of byte i - 4.
+__device__ __forceinline__ uint32_t w4_word(const uint32_t (&c)[8]) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= c[i] << (i < 4 ? 8 * i : 8 * (i - 4) + 4);
+    return w;
+}
+
+}  // namespace mq

@@ -1,0 +1,68 @@
+// Internal interface of the group-scaled 4-bit operators and of the calls between tokens
+// and their experts' rows (api_w4.hip checks arguments; w4_quant.hip, w4_gemm.hip and
+// rows.hip launch).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mq {
+
+// Layout of a matrix [R][K] (mq.h): 16-row x 128-input code tiles in the lane order of the
+// 16x16x32 matrix instructions, scales by row in quads of tiles.
+inline int64_t w4_row_tiles(int64_t R) { return (R + 15) / 16; }
+inline int64_t w4_tiles(int64_t K) { return (K + 127) / 128; }
+inline int64_t w4_quads(int64_t K) { return (K + 511) / 512; }
+inline int64_t w4_codes_size(int64_t R, int64_t K) { return w4_row_tiles(R) * w4_tiles(K) * 1024; }
+inline int64_t w4_scales_size(int64_t R, int64_t K, int group) { return w4_row_tiles(R) * w4_quads(K) * 16 * (512 / group) * 2; }
+
+struct W4QuantArgs {
+    const void* x;                   // values, or codes one to a byte (pack)
+    int dtype;
+    const uint16_t *s, *z;           // pack: scales and zero points [B][R][ceil(K/group)]
+    int64_t B, stride_b, R, stride_r;
+    int K, group, scale_dtype;
+    uint8_t* codes;
+    uint16_t *scales, *zeros;
+};
+
+// Y = X W^T. Dense: M x N outputs. With offsets: M rows of a plan, each with its expert's
+// matrix; by_token: row p is x's row row_token[p].
+struct W4GemmArgs {
+    const void* x;
+    int x_dtype;
+    int64_t stride_x;
+    const uint8_t* codes;
+    const uint16_t *scales, *zeros;
+    int scale_dtype, group;
+    int M, N, K;
+    const float* bias;
+    void* y;
+    int y_dtype;
+    const int32_t *offsets, *row_token;
+    int by_token, E, T;
+};
+
+struct RowsArgs {
+    const void* x;                   // [T][D], the tokens' side
+    int x_dtype;
+    int64_t stride_t;
+    const void* rows;                // [P][D], the experts' side
+    int rows_dtype;
+    int64_t T, P;
+    int k, D;
+    const int32_t *row_token, *row_of;
+    const float* weights;
+    const void* other;               // of the output's size; combine: rows stride_o apart
+    int64_t stride_o;
+    float* dots;
+};
+
+hipError_t launch_w4_quant(const W4QuantArgs& a, hipStream_t st);
+hipError_t launch_w4_pack(const W4QuantArgs& a, hipStream_t st);
+hipError_t launch_w4_dequant(const W4QuantArgs& a, void* y, int y_dtype, hipStream_t st);
+hipError_t launch_w4_few(const W4GemmArgs& a, hipStream_t st);
+hipError_t launch_rows_gather(const RowsArgs& a, hipStream_t st);
+hipError_t launch_rows_combine(const RowsArgs& a, hipStream_t st);
+
+}  // namespace mq

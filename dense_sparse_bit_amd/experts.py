@@ -1,5 +1,5 @@
-"""Routing to experts, the plan of a batch's rows by expert, and the experts' products
-over microscaled 4-bit weights (include/mq.h)."""
+"""Routing to experts, the plan of a batch's rows by expert, tokens to those rows and back
+(with gradients), and the experts' products over microscaled 4-bit weights (include/mq.h)."""
 from __future__ import annotations
 
 from typing import NamedTuple
@@ -27,6 +27,7 @@ if _binding is not None:
 _route, _plan_rows, _expert_plan = _lib.mq_route, _lib.mq_plan_rows, _lib.mq_expert_plan
 _up, _up_workspace = _lib.mq_mx_experts_up, _lib.mq_mx_experts_up_workspace_bytes
 _down, _down_workspace = _lib.mq_mx_experts_down, _lib.mq_mx_experts_down_workspace_bytes
+_gather_rows, _combine_rows = _lib.mq_experts_gather, _lib.mq_experts_combine
 
 
 def plan_rows(T: int, k: int, experts: int) -> int:
@@ -124,6 +125,147 @@ def _plan(plan, index):
     _check(row_token, "plan.row_token", torch.int32, (rows,), index)
     _check(row_of, "plan.row_of", torch.int32, (T, k), index)
     return T, k, E, rows
+
+
+def _gather(x, plan, weights, dtype, rows, other):
+    """rows [P, D] of `dtype` (x's where None): v[t, j] * x[t] at row_of[t, j], zero for rows
+    of no token; with other [P, D] also dots [T, k] = x[t] . other[row_of[t, j]]."""
+    if _binding is not None:
+        done = _binding.gather(x, plan, weights, dtype, rows, other)
+        if done is not None:
+            return done
+    code = _input(x, "x", 2)
+    index = x.get_device()
+    if index < 0 or index != _current_device():
+        with _on(index, None):
+            return _gather(x, plan, weights, dtype, rows, other)
+    T, k, E, P = _plan(plan, index)
+    D = x.shape[1]
+    if x.shape[0] != T or D == 0:
+        raise ValueError(f"x must be [{T}, columns] for this plan, got {tuple(x.shape)}")
+    if weights is not None:
+        _check(weights, "weights", torch.float32, (T, k), index)
+    rows = _output(rows, "rows", (P, D), x.dtype if dtype is None else dtype, index)
+    dots = None
+    if other is not None:
+        _check(other, "other", rows.dtype, (P, D), index)
+        dots = torch.empty((T, k), dtype=torch.float32, device=x.device)
+    rc = _gather_rows(x.data_ptr(), code, x.stride(0), T, k, E, D, plan.row_token.data_ptr(), plan.row_of.data_ptr(),
+                      None if weights is None else weights.data_ptr(), rows.data_ptr(), _TYPES[rows.dtype],
+                      None if other is None else other.data_ptr(), None if other is None else dots.data_ptr(),
+                      _raw_stream(index))
+    if rc:
+        raise MQError("mq_experts_gather", rc)
+    return rows if other is None else (rows, dots)
+
+
+def _combine(rows, plan, weights, dtype, y, other):
+    """y [T, D] of `dtype` (the rows' where None): the sum over j of v[t, j] * rows[row_of[t, j]];
+    with other [T, D] also dots [T, k] = other[t] . rows[row_of[t, j]]."""
+    if _binding is not None:
+        done = _binding.combine(rows, plan, weights, dtype, y, other)
+        if done is not None:
+            return done
+    code = _input(rows, "rows", 2)
+    index = rows.get_device()
+    if index < 0 or index != _current_device():
+        with _on(index, None):
+            return _combine(rows, plan, weights, dtype, y, other)
+    T, k, E, P = _plan(plan, index)
+    D = rows.shape[1]
+    if D == 0:
+        raise ValueError("rows have no columns")
+    _check(rows, "rows", rows.dtype, (P, D), index)
+    if weights is not None:
+        _check(weights, "weights", torch.float32, (T, k), index)
+    y = _output(y, "y", (T, D), rows.dtype if dtype is None else dtype, index)
+    dots = None
+    if other is not None:
+        _input(other, "other", 2)
+        if other.shape != (T, D) or other.dtype != y.dtype or other.get_device() != index:
+            raise ValueError(f"other must be [{T}, {D}] of {y.dtype} on cuda:{index}")
+        dots = torch.empty((T, k), dtype=torch.float32, device=rows.device)
+    rc = _combine_rows(rows.data_ptr(), code, T, k, E, D, plan.row_of.data_ptr(),
+                       None if weights is None else weights.data_ptr(), y.data_ptr(), _TYPES[y.dtype],
+                       None if other is None else other.data_ptr(), 0 if other is None else other.stride(0),
+                       None if other is None else dots.data_ptr(), _raw_stream(index))
+    if rc:
+        raise MQError("mq_experts_combine", rc)
+    return y if other is None else (y, dots)
+
+
+class _Gather(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weights, plan):
+        rows = _gather(x, plan, weights, None, None, None)
+        dots = weights is not None and weights.requires_grad
+        ctx.save_for_backward(weights, x if dots else None, *plan)
+        ctx.dtype, ctx.dots = x.dtype, dots
+        return rows
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, drows):
+        weights, x, *plan = ctx.saved_tensors
+        done = _combine(drows.contiguous(), ExpertPlan(*plan), weights, ctx.dtype, None, x)
+        return (*done, None) if ctx.dots else (done, None, None)
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, weights, plan, dtype):
+        y = _combine(rows, plan, weights, dtype, None, None)
+        dots = weights is not None and weights.requires_grad
+        ctx.save_for_backward(weights, rows if dots else None, *plan)
+        ctx.dtype, ctx.dots = rows.dtype, dots
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        weights, rows, *plan = ctx.saved_tensors
+        if dy.stride(-1) != 1 or dy.stride(0) < 0:
+            dy = dy.contiguous()
+        done = _gather(dy, ExpertPlan(*plan), weights, ctx.dtype, None, rows)
+        return (*done, None, None) if ctx.dots else (done, None, None, None)
+
+
+def _wants_gradient(out, name, *inputs):
+    """Whether a call has to leave its gradient; not with an output of the caller's."""
+    if not torch.is_grad_enabled() or not any(isinstance(t, torch.Tensor) and t.requires_grad for t in inputs):
+        return False
+    if out is not None:
+        raise ValueError(f"{name} cannot be given where a gradient is wanted")
+    return True
+
+
+def experts_gather(x, plan: ExpertPlan, weights=None, rows=None, stream=None):
+    """Tokens to the rows of their experts: rows [P, D] of x's type, x[t] (times weights[t, j],
+    where given) at row plan.row_of[t, j], zero for rows of no token. x [T, D] (fp32, bf16,
+    fp16; its last axis contiguous), weights fp32 [T, k]. Has gradients of x (the sum over the
+    token's rows, in the order of the slots) and of weights."""
+    if stream is not None:
+        _input(x, "x", 2)
+        with _on(x.get_device(), stream, x, plan, weights, rows):
+            return experts_gather(x, plan, weights, rows)
+    if _wants_gradient(rows, "rows", x, weights):
+        return _Gather.apply(x, weights, plan)
+    return _gather(x, plan, weights, None, rows, None)
+
+
+def experts_combine(rows, plan: ExpertPlan, weights=None, out_dtype=None, y=None, stream=None):
+    """The experts' rows back to their tokens: y[t] = sum over slots j of weights[t, j] *
+    rows[row_of[t, j]] (weights None: of the rows), in the order of the slots, rounded once to
+    out_dtype (the rows' type where None). A slot without a row adds weights[t, j] * 0. rows [P, D]
+    (fp32, bf16, fp16), weights fp32 [T, k]. Has gradients of rows (zero for rows of no token)
+    and of weights (0 for slots without a row)."""
+    if stream is not None:
+        _input(rows, "rows", 2)
+        with _on(rows.get_device(), stream, rows, plan, weights, y):
+            return experts_combine(rows, plan, weights, out_dtype, y)
+    if _wants_gradient(y, "y", rows, weights):
+        return _Combine.apply(rows, weights, plan, out_dtype)
+    return _combine(rows, plan, weights, out_dtype, y, None)
 
 
 def mx_experts_up(x, w_gate: MX, w_up: MX, plan: ExpertPlan, out_dtype=torch.bfloat16, h=None, stream=None):

@@ -444,6 +444,99 @@ int mq_mx_experts_down(const void* h, int h_dtype, int64_t T, int64_t k, int64_t
                        const uint8_t* ws, void* y, int y_dtype, void* workspace, size_t workspace_bytes,
                        void* stream);
 
+/*
+ * ---------------------------------------------------------------------------------
+ * Group-scaled 4-bit weights and products of unquantized rows with them.
+ *
+ * The format: `group` (32, 64 or 128) consecutive inputs of a row share a scale s and a
+ * zero point z, both 16-bit floats of one type (scale_dtype: MQ_F16 or MQ_BF16); z is 8
+ * where there are no zero points. A weight is s * (c - z), its code c = 0 .. 15.
+ *   Device layout of a matrix [R][K] (RT = ceil(R/16), G = ceil(K/128), Q = ceil(K/512)):
+ *     codes   RT * G tiles of 1 KB, 16 rows x 128 inputs. The codes of row r and the inputs
+ *             8j .. 8j + 7 are the word (j/4) % 4 of the 16 bytes at
+ *               (((r/16)*G + j/16)*64 + (j % 4)*16 + r % 16) * 16,
+ *             input 8j + i in the low half of its byte i (i < 4) or the high half of its
+ *             byte i - 4.
+ *     scales, zeros   the value of (r, k) is entry
+ *               (((r/16)*Q + k/512)*16 + r % 16) * (512/group) + (k % 512)/group
+ *   Rows up to RT * 16 and inputs up to G * 128 (scales: Q * 512) exist and hold zeros. A
+ *   batch [B][R][K] is B such matrices in a row. codes, scales and zeros 16-byte aligned.
+ *   Any R, K >= 1 (K <= 2^20, R <= 2^24).
+ */
+size_t mq_w4_codes_bytes(int64_t R, int64_t K);   /* 0 outside the supported sizes */
+size_t mq_w4_scales_bytes(int64_t R, int64_t K, int group);
+
+/*
+ * Quantization, x [B][R][K] with strides stride_b, stride_r; r32 and r16 round to fp32 and
+ * to the scales' type, rne to the nearest whole number, ties to even:
+ *   zeros NULL:  s = r16(r32(max |x| / 7)),  c = clamp(rne(x / s), -8, 7) + 8
+ *   else:        lo = min(0, min x), hi = max(0, max x), s = r16(r32(r32(hi - lo) / 15)),
+ *                z = clamp(rne(-lo / s), 0, 15),  c = clamp(rne(x / s) + z, 0, 15)
+ * The quotients by s are exact. s is at most the type's largest value; where it is 0,
+ * c = z (z = 0 with zero points). A group with a NaN or an infinity gets s = NaN and reads
+ * back, and multiplies, as NaN.
+ */
+int mq_w4_quantize(const void* x, int x_dtype, int64_t B, int64_t stride_b, int64_t R, int64_t stride_r, int64_t K,
+                   int group, int scale_dtype, uint8_t* codes, void* scales, void* zeros, void* stream);
+
+/* Weights that are quantized already, as checkpoints hold them: c [B][R][K], one code a
+ * byte (its low four bits count; strides stride_b, stride_r), s and z (or NULL)
+ * [B][R][ceil(K/group)], contiguous, of any 16-bit float type, in the library's layout. */
+int mq_w4_pack(const uint8_t* c, int64_t B, int64_t stride_b, int64_t R, int64_t stride_r, int64_t K, int group,
+               const void* s, const void* z, uint8_t* codes, void* scales, void* zeros, void* stream);
+
+/* The values back: y [B][R][K], in fp32 and rounded to y's type. */
+int mq_w4_dequantize(const uint8_t* codes, const void* scales, const void* zeros, int scale_dtype, int64_t B, int64_t R,
+                     int64_t K, int group, void* y, int y_dtype, void* stream);
+
+/*
+ * y[m][n] = sum_k x[m][k] w[n][k] (+ bias[n], fp32, may be NULL), x [M][K] (row stride
+ * stride_m) as it is, w [N][K]: sums of x times codes, which are exact products, are held in
+ * fp32, a group's sum is scaled once. A row of x with a NaN or an infinity gives NaN, and so
+ * does a group whose sum of |x| times 15 leaves fp32's range. workspace: device scratch of at
+ * least mq_w4_linear_workspace_bytes, 16-byte aligned (may be NULL where that is 0).
+ */
+size_t mq_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_dtype, int group);
+int mq_w4_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* codes, const void* scales,
+                 const void* zeros, int scale_dtype, int group, int64_t M, int64_t N, int64_t K, const float* bias,
+                 void* y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The same for the rows of a plan (mq_expert_plan), each with its expert's matrix:
+ *   y[p][n] = sum_k x[r][k] w[e][n][k], e the expert of row p,
+ * r = p, x [mq_plan_rows][K], or by_token r = row_token[p], x [T][K]. Rows of no token are
+ * zero. w: E matrices N x K, y: [mq_plan_rows][N]. Entries of the plan out of range are
+ * taken as "no row".
+ */
+size_t mq_w4_experts_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int by_token, int x_dtype,
+                                     int group);
+int mq_w4_experts(const void* x, int x_dtype, int64_t stride_r, int by_token, int64_t T, int64_t k, int64_t E, int64_t N,
+                  int64_t K, const int32_t* offsets, const int32_t* row_token, const uint8_t* codes, const void* scales,
+                  const void* zeros, int scale_dtype, int group, void* y, int y_dtype, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------------
+ * Tokens to the rows of their experts and back, over a plan (mq_expert_plan); each is
+ * the other's gradient. v[t][j] = weights[t][j] (fp32 [T][k]), or 1 where weights is NULL.
+ *   gather   rows[row_of[t][j]] = v[t][j] * x[t]; rows of no token are zero
+ *   combine  x[t] = sum over j of v[t][j] * rows[row_of[t][j]], added in the order of the slots;
+ *            a slot without a row adds v[t][j] * 0
+ * With `other` also the dots, the gradient of the weights, in fp32 [T][k]:
+ *   gather   other [mq_plan_rows][D] of rows' type, dots[t][j] = x[t] . other[row_of[t][j]]
+ *   combine  other [T][D] of x's type, its rows stride_o apart, dots[t][j] = other[t] .
+ *            rows[row_of[t][j]]
+ * and 0 for slots without a row. x [T][D] (gather: its rows stride_t apart), rows
+ * [mq_plan_rows][D]; each of its own type. Products and sums in fp32, rounded once. Entries of row_of and
+ * row_token out of range are taken as "no row". D <= 2^20.
+ */
+int mq_experts_gather(const void* x, int x_dtype, int64_t stride_t, int64_t T, int64_t k, int64_t E, int64_t D,
+                      const int32_t* row_token, const int32_t* row_of, const float* weights, void* rows, int rows_dtype,
+                      const void* other, float* dots, void* stream);
+int mq_experts_combine(const void* rows, int rows_dtype, int64_t T, int64_t k, int64_t E, int64_t D,
+                       const int32_t* row_of, const float* weights, void* x, int x_dtype, const void* other,
+                       int64_t stride_o, float* dots, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
