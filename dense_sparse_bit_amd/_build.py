@@ -42,6 +42,7 @@ SOURCES = {
     "api_mx.hip": [],
     "w4_quant.hip": [],
     "w4_gemm.hip": [],
+    "w4_wide.hip": [],
     "rows.hip": [],
     "api_w4.hip": [],
 }

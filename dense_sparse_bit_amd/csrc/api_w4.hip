@@ -2,6 +2,7 @@
 // experts' rows: argument checks, then kernel launches. Declarations and the meaning of
 // every argument are in include/mq.h.
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "../../include/mq.h"
 #include "mx_internal.h"
@@ -20,6 +21,7 @@ constexpr int64_t kMaxRows = int64_t(1) << 24;
 constexpr int64_t kMaxCols = int64_t(1) << 20;
 constexpr int64_t kMaxElements = int64_t(1) << 40;
 constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kMaxPitch = int64_t(1) << 22;       // of rows that the tiles take as they are: 128 of them within 32 bits
 constexpr int64_t kMaxSlots = int64_t(1) << 27;
 
 int check_matrix(int64_t B, int64_t R, int64_t K, int group) {
@@ -112,6 +114,81 @@ mq::RowsArgs rows_of(int64_t T, int64_t k, int64_t E, int64_t D, const void* x, 
     return a;
 }
 
+size_t round16(int64_t n) { return static_cast<size_t>((n + 15) / 16 * 16); }
+
+// The way of a product: a run of K a wave (launch_w4_few), or tiles of 32 rt rows and 128 ct
+// columns.
+struct Way {
+    int rt, ct;                                        // rt 0: few rows
+};
+Way dense_way(int64_t M, int64_t N, int64_t K, int planes) {
+    if (const char* s = getenv("W4_WAY")) return {s[0] - '0', s[1] - '0'};
+    if (M <= 64) return {0, 0};
+    return {2, 2};
+}
+Way experts_way(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int planes) {
+    if (const char* s = getenv("W4_WAY")) return {s[0] - '0', s[1] - '0'};
+    if (T * k <= 16 * E) return {0, 0};
+    return {4, 2};
+}
+
+// Workspace of the tiles: the rows' sums, a copy of the rows, row blocks
+struct Parts {
+    size_t copy, tiles, bytes;
+    Parts(int64_t R, int64_t K, int x_dtype, int group, int64_t blocks) {
+        const int planes = mq::w4_planes(x_dtype);
+        copy = mq::w4_sums_size(R, K, planes, group);
+        tiles = copy + round16(mq::w4_copy_size(R, K, planes));
+        bytes = tiles + round16(blocks ? (4 + 4 * blocks) * 4 : 0);
+    }
+};
+
+// The rows' part, then the tiles. R: rows of x.
+int wide(const mq::W4GemmArgs& a, Way way, int64_t R, const int32_t* offsets, void* workspace, size_t workspace_bytes, hipStream_t st) {
+    const int64_t blocks = offsets ? mq::mx_tiles_cap(a.M, a.E) : 0;
+    const Parts parts(R, a.K, a.x_dtype, a.group, blocks);
+    if (workspace_bytes < parts.bytes || !workspace || off(workspace, 16)) return MQ_ERR_INVALID_ARG;
+    uint8_t* const work = static_cast<uint8_t*>(workspace);
+    const bool as_it_is = a.x_dtype != MQ_F32 && !off(a.x, 16) && a.stride_x % 8 == 0 && a.K % 128 == 0 && a.stride_x <= kMaxPitch;
+    mq::W4RowsArgs r = {};
+    r.x = a.x;
+    r.dtype = a.x_dtype;
+    r.R = R;
+    r.stride = a.stride_x;
+    r.K = a.K;
+    r.group = a.group;
+    r.sums = work;
+    r.copy = as_it_is ? nullptr : work + parts.copy;
+    int32_t* const tiles = reinterpret_cast<int32_t*>(work + parts.tiles);
+    if (offsets) r.plan = {offsets, a.E, a.M / 16, tiles, static_cast<int>(blocks)};
+    if (mq::launch_w4_rows(r, st) != hipSuccess) return MQ_ERR_HIP;
+    mq::W4WideArgs w = {};
+    const int64_t pitch = mq::w4_tiles(a.K) * mq::w4_planes(a.x_dtype) * 128;
+    w.x = static_cast<const uint16_t*>(as_it_is ? a.x : r.copy);
+    w.x_dtype = a.x_dtype;
+    w.ldx = as_it_is ? a.stride_x : pitch;
+    w.rows_x = R;
+    w.planes = mq::w4_planes(a.x_dtype);
+    w.sums = static_cast<const uint4*>(r.sums);
+    w.codes = a.codes;
+    w.scales = a.scales;
+    w.zeros = a.zeros;
+    w.scale_dtype = a.scale_dtype;
+    w.group = a.group;
+    w.M = a.M;
+    w.N = a.N;
+    w.K = a.K;
+    w.bias = a.bias;
+    w.y = a.y;
+    w.y_dtype = a.y_dtype;
+    w.row_token = a.row_token;
+    w.tiles = offsets ? tiles : nullptr;
+    w.by_token = a.by_token;
+    w.E = a.E;
+    w.T = a.T;
+    return status_of(mq::launch_w4_wide(w, way.rt, way.ct, st));
+}
+
 }  // namespace
 
 extern "C" {
@@ -171,11 +248,14 @@ int mq_w4_dequantize(const uint8_t* codes, const void* scales, const void* zeros
     return status_of(mq::launch_w4_dequant(a, y, y_dtype, static_cast<hipStream_t>(stream)));
 }
 
-size_t mq_w4_linear_workspace_bytes(int64_t, int64_t, int64_t, int, int) { return 0; }
+size_t mq_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_dtype, int group) {
+    if (check_product(M, N, K, group) || bad_type(x_dtype) || !dense_way(M, N, K, mq::w4_planes(x_dtype)).rt) return 0;
+    return Parts(M, K, x_dtype, group, 0).bytes;
+}
 
 int mq_w4_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* codes, const void* scales, const void* zeros,
                  int scale_dtype, int group, int64_t M, int64_t N, int64_t K, const float* bias, void* y, int y_dtype,
-                 void*, size_t, void* stream) {
+                 void* workspace, size_t workspace_bytes, void* stream) {
     int rc = check_product(M, N, K, group);
     if (rc) return rc;
     if (bad_type(x_dtype) || bad_type(y_dtype) || bad_scales(scale_dtype) || stride_m < 0 || off(bias, 4))
@@ -185,14 +265,20 @@ int mq_w4_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* co
     if ((rc = check_weights(codes, scales, zeros, scale_dtype))) return rc;
     mq::W4GemmArgs a = product(x, x_dtype, stride_m, codes, scales, zeros, scale_dtype, group, M, N, K, y, y_dtype);
     a.bias = bias;
-    return status_of(mq::launch_w4_few(a, static_cast<hipStream_t>(stream)));
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const Way way = dense_way(M, N, K, mq::w4_planes(x_dtype));
+    return way.rt ? wide(a, way, M, nullptr, workspace, workspace_bytes, st) : status_of(mq::launch_w4_few(a, st));
 }
 
-size_t mq_w4_experts_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int, int, int) { return 0; }
+size_t mq_w4_experts_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int by_token, int x_dtype, int group) {
+    if (check_experts(T, k, E, N, K, group) || bad_type(x_dtype) || !experts_way(T, k, E, N, K, mq::w4_planes(x_dtype)).rt) return 0;
+    const int64_t P = mq::plan_rows(T, k, E);
+    return Parts(by_token ? T : P, K, x_dtype, group, mq::mx_tiles_cap(P, E)).bytes;
+}
 
 int mq_w4_experts(const void* x, int x_dtype, int64_t stride_r, int by_token, int64_t T, int64_t k, int64_t E, int64_t N,
                   int64_t K, const int32_t* offsets, const int32_t* row_token, const uint8_t* codes, const void* scales,
-                  const void* zeros, int scale_dtype, int group, void* y, int y_dtype, void*, size_t, void* stream) {
+                  const void* zeros, int scale_dtype, int group, void* y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
     int rc = check_experts(T, k, E, N, K, group);
     if (rc) return rc;
     if (bad_type(x_dtype) || bad_type(y_dtype) || bad_scales(scale_dtype) || stride_r < 0) return MQ_ERR_INVALID_ARG;
@@ -207,7 +293,9 @@ int mq_w4_experts(const void* x, int x_dtype, int64_t stride_r, int by_token, in
     a.by_token = by_token != 0;
     a.E = static_cast<int>(E);
     a.T = static_cast<int>(T);
-    return status_of(mq::launch_w4_few(a, static_cast<hipStream_t>(stream)));
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const Way way = experts_way(T, k, E, N, K, mq::w4_planes(x_dtype));
+    return way.rt ? wide(a, way, by_token ? T : a.M, offsets, workspace, workspace_bytes, st) : status_of(mq::launch_w4_few(a, st));
 }
 
 int mq_experts_gather(const void* x, int x_dtype, int64_t stride_t, int64_t T, int64_t k, int64_t E, int64_t D,

@@ -18,6 +18,7 @@ typedef float mx_f16 __attribute__((ext_vector_type(16)));
 typedef float mx_f2 __attribute__((ext_vector_type(2)));
 typedef __bf16 mx_b2 __attribute__((ext_vector_type(2)));
 typedef _Float16 mx_h2 __attribute__((ext_vector_type(2)));
+typedef unsigned int mx_u4 __attribute__((ext_vector_type(4)));
 typedef unsigned short mx_u16x2 __attribute__((ext_vector_type(2)));
 
 // Scale byte of a block whose largest magnitude has the fp32 bits `peak`:
@@ -219,6 +220,22 @@ __device__ inline void mx_store4(void* y, int dtype, int64_t at, int have, bool 
         else if (dtype == MQ_BF16) static_cast<__bf16*>(y)[at + i] = static_cast<__bf16>(v[i]);
         else static_cast<_Float16*>(y)[at + i] = static_cast<_Float16>(v[i]);
     }
+}
+
+// Buffer loads: reads past the operand's end give zero.
+__device__ inline __amdgpu_buffer_rsrc_t buffer(const void* base, int64_t bytes) {
+    // wave-uniform by construction; said so here, or every load becomes a loop over lanes
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p >> 32));
+    const int n = __builtin_amdgcn_readfirstlane(static_cast<int>(bytes < 0 ? 0 : (bytes < 0xffffffff ? bytes : 0xffffffff)));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(static_cast<uint64_t>(hi) << 32 | lo), 0, n, 0x00020000);
+}
+__device__ inline mx_i4 load16(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
+    return __builtin_bit_cast(mx_i4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_at, at, 0));
+}
+__device__ inline int load4(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
+    return static_cast<int>(__builtin_amdgcn_raw_buffer_load_b32(r, lane_at, at, 0));
 }
 
 // g / (1 + exp(-g)), by the hardware's exponential of 2 and reciprocal, each within a unit in

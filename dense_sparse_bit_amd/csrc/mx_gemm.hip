@@ -10,8 +10,6 @@
 namespace mq {
 namespace {
 
-typedef unsigned int mx_u4 __attribute__((ext_vector_type(4)));
-
 __device__ inline mx_i8 wide8(mx_i4 v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
 
 // c += A B^T over one 128-input tile of 16 x 16; the scales are the low bytes
@@ -337,21 +335,6 @@ constexpr int kMaxSub = kBlockTiles / 2;      // 32-row pieces of a row block
 constexpr int kScaleBlock = 128 * kMaxSub + 128;
 constexpr int kScaleBytes = 4 * kScaleBlock;
 constexpr int kOutBytes = 32 * (64 * 4 + 16); // a wave's results on their way out: 32 rows, 16 B apart in the banks
-
-__device__ inline __amdgpu_buffer_rsrc_t buffer(const void* base, int64_t bytes) {
-    // wave-uniform by construction; said so here, or every load becomes a loop over lanes
-    const uint64_t p = reinterpret_cast<uint64_t>(base);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p));
-    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p >> 32));
-    const int n = __builtin_amdgcn_readfirstlane(static_cast<int>(bytes < 0 ? 0 : (bytes < 0xffffffff ? bytes : 0xffffffff)));
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(static_cast<uint64_t>(hi) << 32 | lo), 0, n, 0x00020000);
-}
-__device__ inline mx_i4 load16(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
-    return __builtin_bit_cast(mx_i4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_at, at, 0));
-}
-__device__ inline int load4(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
-    return static_cast<int>(__builtin_amdgcn_raw_buffer_load_b32(r, lane_at, at, 0));
-}
 
 // Pieces of 32 rows in a row block, for `rows32` pieces in all over `cols` column blocks:
 // the least time of n workgroups of s pieces each, two to a CU. Measured in us (K = 1024,

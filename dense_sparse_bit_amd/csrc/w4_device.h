@@ -79,4 +79,24 @@ __device__ __forceinline__ uint32_t w4_word(const uint32_t (&c)[8]) {
     return w;
 }
 
+// The scales or zero points of a code tile's groups in one word.
+template <int GS> struct W4Scales { typedef uint32_t T; };
+template <> struct W4Scales<4> { typedef uint64_t T; };
+
+// Eight codes as bf16 or fp16, exactly, in the order of the inputs: as e4m3 bytes they are
+// c * 2^-9. A mask of 0 makes them zeros.
+template <typename E>
+__device__ __forceinline__ auto w4_codes(uint32_t w, uint32_t mask = 0x0f0f0f0fu) {
+    const uint32_t lo = w & mask, hi = w >> 4 & mask;
+    if constexpr (__is_same(E, _Float16)) {
+        const mx_h2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, false), __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, true),
+                            __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false), __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true)};
+        return __builtin_bit_cast(w4_h8, v);
+    } else {
+        const mx_b2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true),
+                            __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true)};
+        return __builtin_bit_cast(w4_b8, v);
+    }
+}
+
 }  // namespace mq

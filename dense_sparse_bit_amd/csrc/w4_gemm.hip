@@ -14,27 +14,17 @@ namespace {
 
 // The type the matrix instructions take, and how many of it make one value of x.
 template <typename XT> struct W4Op {                  // bf16
+    typedef __bf16 E;
     typedef w4_b8 V;
     static constexpr int kPieces = 1;
     static __device__ __forceinline__ mx_f4 mfma16(V a, V b, mx_f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-    static __device__ __forceinline__ V codes(uint32_t w) {
-        const uint32_t lo = w & 0x0f0f0f0fu, hi = w >> 4 & 0x0f0f0f0fu;
-        const mx_b2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true),
-                            __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true)};
-        return __builtin_bit_cast(V, v);
-    }
     static __device__ __forceinline__ V ones() { return __builtin_bit_cast(V, w4_u4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}); }
 };
 template <> struct W4Op<_Float16> {
+    typedef _Float16 E;
     typedef w4_h8 V;
     static constexpr int kPieces = 1;
     static __device__ __forceinline__ mx_f4 mfma16(V a, V b, mx_f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-    static __device__ __forceinline__ V codes(uint32_t w) {
-        const uint32_t lo = w & 0x0f0f0f0fu, hi = w >> 4 & 0x0f0f0f0fu;
-        const mx_h2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, false), __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, true),
-                            __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false), __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true)};
-        return __builtin_bit_cast(V, v);
-    }
     static __device__ __forceinline__ V ones() { return __builtin_bit_cast(V, w4_u4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u}); }
 };
 // fp32 is the sum of three bf16 values: the first eight significant bits, the next eight
@@ -179,7 +169,7 @@ __global__ __launch_bounds__(512) void k_w4_few(W4GemmArgs a) {
                     for (int s = g * 4 / GS; s < (g + 1) * 4 / GS; ++s) {
                         V b[NT];
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) b[j] = Op::codes(wc[j][s]);
+                        for (int j = 0; j < NT; ++j) b[j] = w4_codes<typename Op::E>(wc[j][s]);
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
                             V x[kPieces];

@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "mx_internal.h"
+
 namespace mq {
 
 // Layout of a matrix [R][K] (mq.h): 16-row x 128-input code tiles in the lane order of the
@@ -43,6 +45,38 @@ struct W4GemmArgs {
     int by_token, E, T;
 };
 
+
+// What launch_w4_wide takes of x: the sums of its groups, and a copy where x itself does not
+// do (fp32, or rows that are not made of aligned 16-byte units).
+struct W4RowsArgs {
+    const void* x;
+    int dtype;
+    int64_t R, stride;
+    int K, group;
+    void *sums, *copy;
+    MxTilesArgs plan;                // row blocks that the launch makes too
+};
+inline int w4_planes(int x_dtype) { return x_dtype == 0 ? 3 : 1; }
+inline int64_t w4_sums_size(int64_t R, int64_t K, int planes, int group) { return w4_tiles(K) * planes * (128 / group) * R * 16; }
+inline int64_t w4_copy_size(int64_t R, int64_t K, int planes) { return R * w4_tiles(K) * planes * 256; }
+
+struct W4WideArgs {
+    const uint16_t* x;               // 16-bit rows in whole runs of 128 inputs, ldx apart
+    int x_dtype;
+    int64_t ldx, rows_x;             // rows of x
+    int planes;                      // runs of 128 inputs for each 128 of K
+    const uint4* sums;
+    const uint8_t* codes;
+    const uint16_t *scales, *zeros;
+    int scale_dtype, group;
+    int M, N, K;
+    const float* bias;
+    void* y;
+    int y_dtype;
+    const int32_t *row_token, *tiles;
+    int by_token, E, T;
+};
+
 struct RowsArgs {
     const void* x;                   // [T][D], the tokens' side
     int x_dtype;
@@ -62,6 +96,9 @@ hipError_t launch_w4_quant(const W4QuantArgs& a, hipStream_t st);
 hipError_t launch_w4_pack(const W4QuantArgs& a, hipStream_t st);
 hipError_t launch_w4_dequant(const W4QuantArgs& a, void* y, int y_dtype, hipStream_t st);
 hipError_t launch_w4_few(const W4GemmArgs& a, hipStream_t st);
+hipError_t launch_w4_rows(const W4RowsArgs& a, hipStream_t st);
+// tiles of 32 rt rows and 128 ct columns: rt <= 2 with ct = 1, rt <= 4 with ct = 2 (4 for a plan's)
+hipError_t launch_w4_wide(const W4WideArgs& a, int rt, int ct, hipStream_t st);
 hipError_t launch_rows_gather(const RowsArgs& a, hipStream_t st);
 hipError_t launch_rows_combine(const RowsArgs& a, hipStream_t st);
 

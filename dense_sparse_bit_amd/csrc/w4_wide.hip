@@ -1,0 +1,463 @@
+// Products of many unquantized rows with group-scaled 4-bit weights, by tiles.
+//
+// As in w4_gemm.hip, y = sum over groups of s * (P - z * X). Here P - z * X is one chain of matrix
+// instructions: X, the sum of a row's group, is known before (a pass over x) as three
+// bf16 pieces, and one instruction more a group multiplies them by -z. fp32 x comes as
+// three bf16 planes, which are as many runs of K over the same weights.
+#include "plan_tiles.h"
+#include "w4_device.h"
+#include "w4_internal.h"
+
+namespace mq {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------- rows
+// The sums of each row's groups, [stage][group][row] units of 16 bytes: bf16 hi, mid, lo, hi,
+// mid, lo, 0, 0 (the second three meet the low part of z), and where `copy` is given the
+// rows themselves, [row][stage][128], zeros past K. A stage is 128 inputs; of fp32 rows, of
+// one of their planes (stage 3h + plane). One wave: 512 inputs of four rows.
+constexpr int kRows = 4;
+template <typename XT>
+__global__ __launch_bounds__(kThreads) void k_w4_rows(const XT* x, int64_t R, int64_t stride, int K, int group, uint4* sums,
+                                                      uint16_t* copy, MxTilesArgs plan) {
+    __shared__ int lds[kTilesLds];
+    const int first = plan.offsets ? 1 : 0;            // workgroups (0, 0): the plan's row blocks alone
+    if (static_cast<int>(blockIdx.x) < first) {
+        if (blockIdx.y == 0) plan_tiles<kBlockTiles>(plan, lds);
+        return;
+    }
+    constexpr int kPlanes = sizeof(XT) == 4 ? 3 : 1;
+    const int G = (K + 127) / 128, per = 128 / group, unit = group / 8;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t r0 = (static_cast<int64_t>(blockIdx.x - first) * 4 + wave) * kRows;
+    const int h = blockIdx.y * 4 + (lane >> 4), k0 = blockIdx.y * 512 + 8 * lane;
+    MxRaw8<XT> raw[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) raw[i] = mx_load8(x + (r0 + i) * stride + k0, r0 + i < R ? K - k0 : 0);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t r = r0 + i;
+        float v[8];
+        w4_values(raw[i], v);
+#pragma unroll
+        for (int p = 0; p < kPlanes; ++p) {
+            if constexpr (kPlanes == 3) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = raw[i].v[j];
+            }
+            float s = 0;
+            w4_u4 words;
+            if constexpr (kPlanes == 3) {
+                float cut[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) cut[j] = __uint_as_float(__float_as_uint(v[j]) & 0xffff0000u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    words[j] = __builtin_amdgcn_perm(__float_as_uint(cut[2 * j + 1]), __float_as_uint(cut[2 * j]), 0x07060302u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    s += cut[j];
+                    raw[i].v[j] = v[j] - cut[j];
+                }
+            } else {
+                words = w4_u4{raw[i].w[0], raw[i].w[1], raw[i].w[2], raw[i].w[3]};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s += v[j];
+            }
+            s = __int_as_float(w4_over_group(__float_as_int(s), group, [](int a, int b) {
+                return __float_as_int(__int_as_float(a) + __int_as_float(b));
+            }));
+            if (r >= R || h >= G) continue;
+            const int64_t stage = static_cast<int64_t>(h) * kPlanes + p;
+            if ((lane & (unit - 1)) == 0) {
+                const uint32_t hi = __float_as_uint(s) >> 16;
+                const float rest = s - __uint_as_float(hi << 16);
+                const uint32_t mid = __float_as_uint(rest) >> 16;
+                const uint32_t lo = __float_as_uint(rest - __uint_as_float(mid << 16)) >> 16;
+                sums[(stage * per + (lane & 15) / unit) * R + r] = make_uint4(hi | mid << 16, lo | hi << 16, mid | lo << 16, 0);
+            }
+            if (copy) *reinterpret_cast<w4_u4*>(copy + (r * G * kPlanes + stage) * 128 + (lane & 15) * 8) = words;
+        }
+    }
+}
+
+template <typename XT>
+hipError_t rows(const W4RowsArgs& a, hipStream_t st) {
+    const unsigned first = a.plan.offsets ? 1 : 0;
+    const dim3 grid(static_cast<unsigned>((a.R + 4 * kRows - 1) / (4 * kRows)) + first, static_cast<unsigned>((a.K + 511) / 512));
+    k_w4_rows<XT><<<grid, kThreads, 0, st>>>(static_cast<const XT*>(a.x), a.R, a.stride, a.K, a.group, static_cast<uint4*>(a.sums),
+                                             static_cast<uint16_t*>(a.copy), a.plan);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------- tiles
+template <typename E> struct Op;
+template <> struct Op<__bf16> {
+    typedef w4_b8 V;
+    static __device__ __forceinline__ mx_f16 mfma(V a, V b, mx_f16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+};
+template <> struct Op<_Float16> {
+    typedef w4_h8 V;
+    static __device__ __forceinline__ mx_f16 mfma(V a, V b, mx_f16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+};
+
+// 16 bytes a lane to lane * 16 behind `to` (wave-uniform)
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, int lane_at, int at, uint8_t* to) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, lane_at, at, 0, 0);
+}
+
+// The kernel's arguments where the launch put them: as a parameter that three branches use
+// they went to scratch memory, and their loads waited for those of the weights.
+typedef __attribute__((address_space(4))) W4WideArgs Args;
+
+template <int RT, int GS> struct WideLds {
+    static constexpr int kX = 32 * RT * 256, kSums = GS * 32 * RT * 16, kStage = kX + kSums;
+    static constexpr int kOut = 32 * (64 * 4 + 16);      // a wave's results on their way out
+    static constexpr int kBytes = 2 * kStage > 4 * kOut ? 2 * kStage : 4 * kOut;
+};
+
+// One wave's part of a tile of 32 RT rows: 32 CT columns. The rows of a stage (128 inputs) go
+// from memory to LDS, units of 16 bytes in an order that has a row's sixteen and sixteen
+// rows' alike in different banks; the weights go to registers, each wave its own, a stage
+// ahead.
+//
+// The sums stand in units of the column's present scale: where a group begins, they are
+// multiplied by the last scale over the new one, and go on through the matrix instructions.
+// Beside them a second set, to be added to once a group, has no room in the registers of
+// a tile of this size. A scale that is 0, or below 2^-48 of the present one (whose sums would
+// leave fp32's range), does not become the unit: its codes count as zeros.
+template <typename E, int GS, int RT, int CT>
+__device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, int row0, int rows, int n0) {
+    typedef typename Op<E>::V V;
+    typedef WideLds<RT, GS> L;
+    constexpr int kSteps = 8 / GS;
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int N = a.N, planes = a.planes, G = (a.K + 127) / 128, Q = (G + 3) / 4, stages = G * planes, n_tiles = (N + 15) / 16;
+    const bool bf = a.scale_dtype == MQ_BF16, has_zeros = a.zeros != nullptr, by_token = a.by_token != 0;
+    const int32_t* const row_token = a.row_token;
+    const int64_t rows_x = a.rows_x;
+    const uint4* const all_sums = a.sums;
+    const int T = a.T, y_dtype = a.y_dtype;
+    const float* const bias = a.bias;
+    void* const y = a.y;
+    // x's row of a row of the block; those past its end read the last one's
+    auto row_at = [&](int r) __attribute__((always_inline)) -> int {
+        const int p = min(r, rows - 1);
+        if (!by_token) return p;
+        const int token = row_token[row0 + p];
+        return static_cast<unsigned>(token) < static_cast<unsigned>(T) ? token : 0;
+    };
+    const int64_t first_row = by_token ? 0 : row0;
+    // this lane's places: rows 4 (2 RT wave + i) + lane / 16, unit lane % 16 of LDS is unit
+    // (lane % 16) ^ (row % 16) of the row
+    uint32_t xat[2 * RT];
+#pragma unroll
+    for (int i = 0; i < 2 * RT; ++i) {
+        const int r = 4 * (2 * RT * wave + i) + (lane >> 4);
+        xat[i] = static_cast<uint32_t>(row_at(r)) * static_cast<uint32_t>(a.ldx) * 2 + 16 * ((lane & 15) ^ (r & 15));
+    }
+    constexpr int kSumsPer = (GS * 32 * RT + kThreads - 1) / kThreads;
+    uint32_t sat[kSumsPer];
+#pragma unroll
+    for (int i = 0; i < kSumsPer; ++i) {
+        const int u = min(i * kThreads + static_cast<int>(threadIdx.x), GS * 32 * RT - 1);
+        sat[i] = (static_cast<uint32_t>(u / (32 * RT)) * static_cast<uint32_t>(rows_x) + row_at(u % (32 * RT))) * 16;
+    }
+    const uint16_t* const x0 = a.x + first_row * a.ldx;
+    const int64_t x_bytes = ((by_token ? T : rows) - 1) * a.ldx * 2 + 256;         // behind a stage's first input
+    auto load_x = [&](int stage) __attribute__((always_inline)) {
+        uint8_t* const to = lds + (stage & 1) * L::kStage;
+        const __amdgpu_buffer_rsrc_t xr = buffer(x0 + static_cast<int64_t>(stage) * 128, x_bytes);
+        const __amdgpu_buffer_rsrc_t sr = buffer(all_sums + static_cast<int64_t>(stage) * GS * rows_x + first_row,
+                                                 (GS * rows_x - first_row) * 16);
+#pragma unroll
+        for (int i = 0; i < 2 * RT; ++i) to_lds(xr, xat[i], 0, to + (2 * RT * wave + i) * 1024);
+#pragma unroll
+        for (int i = 0; i < kSumsPer; ++i)
+            if (i * kThreads + static_cast<int>(threadIdx.x) < GS * 32 * RT) to_lds(sr, sat[i], 0, to + L::kX + (i * kThreads + wave * 64) * 16);
+    };
+    // weights: a wave with no column of its own (past N) reads the last tile's and writes nothing
+    const int tile0 = min(n0 / 16, n_tiles - 1), have = min(n_tiles - tile0, 2 * CT);
+    const int64_t first = static_cast<int64_t>(e) * n_tiles + tile0;
+    const int scale_bytes = Q * 16 * 4 * GS * 2;         // of a row tile
+    const __amdgpu_buffer_rsrc_t wr = buffer(a.codes + first * G * 1024, static_cast<int64_t>(have) * G * 1024);
+    const __amdgpu_buffer_rsrc_t scr = buffer(a.scales + first * (scale_bytes / 2), static_cast<int64_t>(have) * scale_bytes);
+    const __amdgpu_buffer_rsrc_t zr = has_zeros ? buffer(a.zeros + first * (scale_bytes / 2), static_cast<int64_t>(have) * scale_bytes) : scr;
+    const int wat = (lane >> 4 & 1) * G * 1024 + (half * 16 + (lane & 15)) * 16;
+    const int scat = (lane >> 4 & 1) * scale_bytes + (lane & 15) * 8 * GS;
+    // words w of [j][0] are steps 2w, of [j][1] steps 2w + 1
+    mx_i4 W[CT][2];
+    typedef typename W4Scales<GS>::T Scales;
+    Scales S[CT], Z[CT];
+    auto scales_at = [&](__amdgpu_buffer_rsrc_t r, int at) __attribute__((always_inline)) -> Scales {
+        if constexpr (GS == 1) return __builtin_amdgcn_raw_buffer_load_b16(r, scat, at, 0);
+        else if constexpr (GS == 2) return __builtin_amdgcn_raw_buffer_load_b32(r, scat, at, 0);
+        else return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(r, scat, at, 0));
+    };
+    auto load_w = [&](int stage) __attribute__((always_inline)) {
+        const int h = planes == 1 ? stage : stage / 3, at = ((h >> 2) * 64 + (h & 3)) * GS * 2;
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            W[j][0] = load16(wr, wat, 2 * j * G * 1024 + h * 1024);
+            W[j][1] = load16(wr, wat, 2 * j * G * 1024 + h * 1024 + 512);
+            S[j] = scales_at(scr, 2 * j * scale_bytes + at);
+            Z[j] = scales_at(zr, 2 * j * scale_bytes + at);
+        }
+    };
+    mx_f16 acc[RT][CT] = {};
+    // A group's: the factor from the last unit to its own, its unit, -z as the matrix
+    // instructions take it (the sums' pieces meet the high part, then the low part), its codes'
+    // mask.
+    float unit[CT] = {}, by[CT], next[CT];
+    w4_b8 zb[CT];
+    uint32_t mask[CT];
+    auto begin = [&](const Scales (&sw)[CT], const Scales (&zw)[CT], int g) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const float s = w4_float(static_cast<uint32_t>(sw[j] >> 16 * g) & 0xffff, bf);
+            const bool keep = s == 0.0f || fabsf(s) < fabsf(unit[j]) * 0x1p-48f;
+            next[j] = keep ? unit[j] : s;
+            const float to = keep ? 1.0f : s, from = keep ? 1.0f : unit[j], inv = __builtin_amdgcn_rcpf(to), q = from * inv;
+            by[j] = __builtin_fmaf(__builtin_fmaf(-q, to, from), inv, q);
+            mask[j] = keep ? 0 : 0x0f0f0f0fu;
+            const float given = -w4_float(static_cast<uint32_t>(zw[j] >> 16 * g) & 0xffff, bf), z = has_zeros ? given : -8.0f;
+            const bool none = keep || half;
+            const uint32_t hi = none ? 0 : __float_as_uint(z) >> 16;
+            const uint32_t lo = none ? 0 : __float_as_uint(z - __uint_as_float(__float_as_uint(z) & 0xffff0000u)) >> 16;
+            zb[j] = __builtin_bit_cast(w4_b8, w4_u4{hi | hi << 16, hi | lo << 16, lo | lo << 16, 0});
+        }
+    };
+    V x_of[2][RT], b[2][CT];
+    // a row tile's share of the conversions of a step
+    auto convert = [&](const mx_i4 (&w)[CT][2], int step, int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+            if (j * RT / CT == i) b[step & 1][j] = w4_codes<E>(w[j][step & 1][step >> 1], mask[j]);
+    };
+    load_x(0);
+    load_w(0);
+    begin(S, Z, 0);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) convert(W, 0, i);
+    const int swap = (half ^ (lane & 15)) * 16;
+    for (int stage = 0; stage < stages; ++stage) {
+        __syncthreads();                                 // stage's rows are there, the other buffer's reads are done
+        mx_i4 w[CT][2];
+        Scales sw[CT], zw[CT];
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            w[j][0] = W[j][0];
+            w[j][1] = W[j][1];
+            sw[j] = S[j];
+            zw[j] = Z[j];
+        }
+        if (stage + 1 < stages) {
+            load_x(stage + 1);
+            load_w(stage + 1);
+        }
+        const uint8_t* const x = lds + (stage & 1) * L::kStage + (lane & 31) * 256;
+        const uint8_t* const sums = lds + (stage & 1) * L::kStage + L::kX + (lane & 31) * 16;
+        w4_b8 sum[RT];
+        auto read = [&](int step, int i) __attribute__((always_inline)) {
+            x_of[step & 1][i] = *reinterpret_cast<const V*>(x + 32 * i * 256 + (swap ^ step * 32));
+        };
+        auto read_sum = [&](int g, int i) __attribute__((always_inline)) {
+            sum[i] = *reinterpret_cast<const w4_b8*>(sums + (g * 32 * RT + 32 * i) * 16);
+        };
+        // A step's operands are read and converted during the step before, a group's begun
+        // during the last one's end; the scheduling barriers keep each row tile's products
+        // with its share of that. Left alone, the compiler reads operands right before
+        // their use, and the matrix units wait for them and for the conversions.
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            read_sum(0, i);
+            read(0, i);
+        }
+#pragma unroll
+        for (int g = 0; g < GS; ++g) {
+#pragma unroll
+            for (int j = 0; j < CT; ++j) unit[j] = next[j];
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const int step = g * kSteps + s;
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    if (s == 0) {
+#pragma unroll
+                        for (int j = 0; j < CT; ++j) acc[i][j] *= by[j];
+#pragma unroll
+                        for (int j = 0; j < CT; ++j) acc[i][j] = Op<__bf16>::mfma(sum[i], zb[j], acc[i][j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) acc[i][j] = Op<E>::mfma(x_of[step & 1][i], b[step & 1][j], acc[i][j]);
+                    if (s + 1 < kSteps) {
+                        read(step + 1, i);
+                        convert(w, step + 1, i);
+                    } else if (g + 1 < GS) {
+                        if (i == 0) begin(sw, zw, g + 1);
+                        read_sum(g + 1, i);
+                        read(step + 1, i);
+                        convert(w, step + 1, i);
+                    } else {                             // (past the last stage: of its own again, not used)
+                        if (i == 0) {
+#pragma unroll
+                            for (int j = 0; j < CT; ++j) asm volatile("" : "+v"(S[j]), "+v"(Z[j]));    // no use of these loads sooner
+                            begin(S, Z, 0);
+                        }
+                        convert(W, 0, i);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+    }
+
+    // The results leave through LDS, piece by piece: a lane holds one column of rows
+    // 8 (r / 4) + 4 (l / 32) + r % 4; read back, a lane holds eight columns of a row.
+    constexpr int kPitch = 32 * CT * 4 + 16, kLanes = 4 * CT, kRound = 64 / kLanes;
+    uint8_t* const tile = lds + wave * L::kOut;
+    __syncthreads();
+    const int n = n0 + (lane % kLanes) * 8;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        mx_wave_sync();
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                *reinterpret_cast<float*>(tile + (8 * (r >> 2) + 4 * half + (r & 3)) * kPitch + (32 * j + (lane & 31)) * 4) =
+                    acc[i][j][r] * unit[j];
+        mx_wave_sync();
+#pragma unroll
+        for (int q = 0; q < 32 / kRound; ++q) {
+            const int r = q * kRound + lane / kLanes, p = row0 + 32 * i + r;
+            if (32 * i + r >= rows || n >= N) continue;
+            const mx_f4 lo = *reinterpret_cast<const mx_f4*>(tile + r * kPitch + (lane % kLanes) * 32);
+            const mx_f4 hi = *reinterpret_cast<const mx_f4*>(tile + r * kPitch + (lane % kLanes) * 32 + 16);
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            if (bias) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[c] += n + c < N ? bias[n + c] : 0.0f;
+            }
+            if (row_token && static_cast<unsigned>(row_token[p]) >= static_cast<unsigned>(T)) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[c] = 0.0f;
+            }
+            const int64_t at = static_cast<int64_t>(p) * N + n;
+            if (y_dtype == MQ_F32) w4_store8(static_cast<float*>(y) + at, N - n, v);
+            else if (y_dtype == MQ_BF16) w4_store8(static_cast<__bf16*>(y) + at, N - n, v);
+            else w4_store8(static_cast<_Float16*>(y) + at, N - n, v);
+        }
+    }
+}
+
+// zeros for rows after the last expert's
+template <int COLS>
+__device__ void zero_rows(const Args& a, int row0, int rows, int n0) {
+    const float none[8] = {};
+    for (int i = threadIdx.x; i < rows * (COLS / 8); i += kThreads) {
+        const int n = n0 + i % (COLS / 8) * 8;
+        const int64_t at = static_cast<int64_t>(row0 + i / (COLS / 8)) * a.N + n;
+        if (n >= a.N) continue;
+        if (a.y_dtype == MQ_F32) w4_store8(static_cast<float*>(a.y) + at, a.N - n, none);
+        else if (a.y_dtype == MQ_BF16) w4_store8(static_cast<__bf16*>(a.y) + at, a.N - n, none);
+        else w4_store8(static_cast<_Float16*>(a.y) + at, a.N - n, none);
+    }
+}
+
+// Four waves side by side, on blocks of at most 32 RT rows.
+template <typename E, int GS, int RT, int CT>
+__global__ __launch_bounds__(kThreads, 2) void k_w4_wide(W4WideArgs) {
+    const Args& a = *(const Args*)__builtin_amdgcn_kernarg_segment_ptr();
+    __shared__ __align__(16) uint8_t lds[WideLds<RT, GS>::kBytes];
+    constexpr int kCols = 128 * CT, kSlots = 64;           // workgroups that a die holds at a time
+    const int ncol = (a.N + kCols - 1) / kCols, blocks = (a.M + 32 * RT - 1) / (32 * RT);
+    const int count = a.tiles ? a.tiles[0] : blocks;
+    // Workgroups go to the eight dies in turn: each die takes a run of neighbouring tiles,
+    // which share rows and weights in its L2. The tiles that would be left for a last round of
+    // few workgroups are split by rows, so that they fill it.
+    const int total = count * ncol, share = (total + 7) / 8;
+    const int die = blockIdx.x & 7, mine = min(share, total - die * share);
+    int u = blockIdx.x >> 3, part = 0, parts = 1;
+    if (!a.tiles && mine > kSlots) {
+        const int whole = mine / kSlots * kSlots, rest = mine - whole;
+        parts = rest * 4 <= kSlots && RT == 4 ? 4 : (rest * 2 <= kSlots && RT > 1 ? 2 : 1);
+        if (u >= whole) {
+            part = (u - whole) % parts;
+            u = whole + (u - whole) / parts;
+        } else {
+            parts = 1;
+        }
+    }
+    const int t = die * share + u;
+    if (u >= mine) return;
+    int e = 0, row0, rows, col;
+    if (a.tiles) {
+        const int4 tile = *reinterpret_cast<const int4*>(a.tiles + 4 + 4 * (t / ncol));
+        e = __builtin_amdgcn_readfirstlane(tile.x);
+        row0 = __builtin_amdgcn_readfirstlane(tile.y) * 16;
+        rows = min(__builtin_amdgcn_readfirstlane(tile.z) * 16, a.M - row0);
+        col = t % ncol;
+    } else {
+        // neighbours: eight row blocks, then the next columns of these, so that the 64 tiles at
+        // work on a die share eight blocks of rows and eight of columns
+        const int group = t / (8 * ncol), in_group = min(8, blocks - 8 * group), i = t - group * 8 * ncol;
+        const int pieces = (RT + parts - 1) / parts;       // of 32 rows
+        row0 = ((8 * group + i % in_group) * RT + part * pieces) * 32;
+        rows = min(32 * min(pieces, RT - part * pieces), a.M - row0);
+        col = i / in_group;
+        if (rows <= 0) return;
+    }
+    if (e < 0) {
+        zero_rows<kCols>(a, row0, rows, col * kCols);
+        return;
+    }
+    const int n0 = col * kCols + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 32 * CT;
+    if (RT >= 4 && rows > 96) wide_tile<E, GS, RT, CT>(a, lds, e, row0, rows, n0);
+    else if (RT >= 3 && rows > 64) wide_tile<E, GS, RT < 3 ? RT : 3, CT>(a, lds, e, row0, rows, n0);
+    else if (RT >= 2 && rows > 32) wide_tile<E, GS, RT < 2 ? RT : 2, CT>(a, lds, e, row0, rows, n0);
+    else wide_tile<E, GS, 1, CT>(a, lds, e, row0, rows, n0);
+}
+
+template <typename E, int GS, int RT, int CT>
+hipError_t wide(const W4WideArgs& a, hipStream_t st) {
+    const int64_t ncol = (a.N + 128 * CT - 1) / (128 * CT);
+    const int64_t n = a.tiles ? mx_tiles_cap(a.M, a.E) : (a.M + 32 * RT - 1) / (32 * RT);
+    const int64_t rest = 64 * 8 * 4;                       // what the last round's tiles make when they are split, at most
+    const int64_t want = (n * ncol + 7) / 8 * 8 + (a.tiles || n * ncol <= 512 ? 0 : rest);
+    if (want >= int64_t(1) << 24) return hipErrorInvalidConfiguration;       // a grid holds 2^32 threads
+    k_w4_wide<E, GS, RT, CT><<<static_cast<unsigned>(want), kThreads, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+template <typename E, int GS>
+hipError_t wide_tiles(const W4WideArgs& a, int rt, int ct, hipStream_t st) {
+    if (ct == 1) return rt == 1 ? wide<E, GS, 1, 1>(a, st) : wide<E, GS, 2, 1>(a, st);
+    if (rt <= 2) return rt == 1 ? wide<E, GS, 1, 2>(a, st) : wide<E, GS, 2, 2>(a, st);
+    return rt == 3 ? wide<E, GS, 3, 2>(a, st) : wide<E, GS, 4, 2>(a, st);
+}
+
+template <typename E>
+hipError_t wide_groups(const W4WideArgs& a, int rt, int ct, hipStream_t st) {
+    if (a.group == 128) return wide_tiles<E, 1>(a, rt, ct, st);
+    return a.group == 64 ? wide_tiles<E, 2>(a, rt, ct, st) : wide_tiles<E, 4>(a, rt, ct, st);
+}
+
+}  // namespace
+
+hipError_t launch_w4_rows(const W4RowsArgs& a, hipStream_t st) {
+    switch (a.dtype) {
+        case MQ_F32: return rows<float>(a, st);
+        case MQ_BF16: return rows<__bf16>(a, st);
+        default: return rows<_Float16>(a, st);
+    }
+}
+
+hipError_t launch_w4_wide(const W4WideArgs& a, int rt, int ct, hipStream_t st) {
+    return a.x_dtype == MQ_F16 ? wide_groups<_Float16>(a, rt, ct, st) : wide_groups<__bf16>(a, rt, ct, st);
+}
+
+}  // namespace mq
