@@ -6,6 +6,8 @@
 // so P is a sum of exact products on the matrix instructions, held in fp32, and the scales,
 // which 16 bits would round, come in once a group in fp32. X comes from the same
 // instructions, against ones.
+#include <stdlib.h>
+
 #include "w4_device.h"
 #include "w4_internal.h"
 
@@ -33,18 +35,16 @@ template <> struct W4Op<float> : W4Op<__bf16> {
     static constexpr int kPieces = 3;
 };
 
-// Eight values of LDS (of a row: 16-byte units, fp32 two of them) as matrix operands.
+// Eight values as matrix operands.
 template <typename XT>
-__device__ __forceinline__ void pieces(const uint8_t* from, typename W4Op<XT>::V (&a)[W4Op<XT>::kPieces]) {
+__device__ __forceinline__ void pieces(const MxRaw8<XT>& r, typename W4Op<XT>::V (&a)[W4Op<XT>::kPieces]) {
     typedef typename W4Op<XT>::V V;
-    const w4_u4 lo = *reinterpret_cast<const w4_u4*>(from);
     if constexpr (sizeof(XT) == 2) {
-        a[0] = __builtin_bit_cast(V, lo);
+        a[0] = __builtin_bit_cast(V, w4_u4{r.w[0], r.w[1], r.w[2], r.w[3]});
     } else {
-        const w4_u4 hi = *reinterpret_cast<const w4_u4*>(from + 16);
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i < 4 ? lo[i & 3] : hi[i & 3]);
+        for (int i = 0; i < 8; ++i) v[i] = r.v[i];
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
             w4_u4 w;
@@ -84,19 +84,281 @@ __device__ __forceinline__ uint64_t load_scales(const uint16_t* p) {
     else return *reinterpret_cast<const uint64_t*>(p);
 }
 
+// The scales or zero points of a quad of code tiles (4 GS of them).
+template <int GS> struct Quad {
+    uint32_t w[2 * GS];
+    __device__ __forceinline__ void load(const uint16_t* p) {
+        if constexpr (GS == 1) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            w[0] = v.x;
+            w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < GS / 2; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ float get(int i, bool bf) const { return w4_float(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffff, bf); }
+};
+
 // ------------------------------------------------------------------- few rows
-// A wave's rows of one code tile (128 inputs) in LDS; rows are 16 bytes further apart than
-// they are long, so that 16 rows' units of 16 bytes lie in different banks.
+constexpr int kMaxWaves = 8;
+// 16 rows of one code tile (128 inputs) in LDS, 16 bytes further apart than they are long, so
+// that their units of 16 bytes lie in different banks.
 template <typename XT> constexpr int kRowPitch = 128 * sizeof(XT) + 16;
 
-// One workgroup: 16 MT rows x NT column tiles of 16, its waves each a run of K; their
-// partial sums are added through LDS in the order of the waves. GS: groups in 128 inputs.
-template <typename XT, int GS, bool Z, int NT, int MT>
-__global__ __launch_bounds__(512) void k_w4_few(W4GemmArgs a) {
+template <typename XT>
+__device__ __forceinline__ void put8(uint8_t* to, const MxRaw8<XT>& v) {
+    if constexpr (sizeof(XT) == 2) {
+        *reinterpret_cast<w4_u4*>(to) = w4_u4{v.w[0], v.w[1], v.w[2], v.w[3]};
+    } else {
+        *reinterpret_cast<mx_f4*>(to) = mx_f4{v.v[0], v.v[1], v.v[2], v.v[3]};
+        *reinterpret_cast<mx_f4*>(to + 16) = mx_f4{v.v[4], v.v[5], v.v[6], v.v[7]};
+    }
+}
+template <typename XT>
+__device__ __forceinline__ MxRaw8<XT> get8(const uint8_t* from) {
+    MxRaw8<XT> r;
+    const mx_f4 lo = *reinterpret_cast<const mx_f4*>(from);
+    if constexpr (sizeof(XT) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = __float_as_uint(lo[i]);
+    } else {
+        const mx_f4 hi = *reinterpret_cast<const mx_f4*>(from + 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r.v[i] = lo[i];
+            r.v[4 + i] = hi[i];
+        }
+    }
+    return r;
+}
+
+// The products of one code tile, all in this wave: acc += s (P - z X) for each of its groups.
+// `from`: this lane's operands of step 0 in LDS, row tiles 16 pitches apart; scale(g, j) and
+// zero(g, j).
+template <typename XT, int GS, int NT, int MT, typename Scale, typename Zero>
+__device__ __forceinline__ void tile_products(const mx_i4 (&c)[NT], const uint8_t* from, int pitch, Scale scale, Zero zero,
+                                              mx_f4 (&acc)[NT][MT]) {
     typedef W4Op<XT> Op;
     typedef typename Op::V V;
-    constexpr int kPieces = Op::kPieces, kPitch = kRowPitch<XT>, kUnit = 8 * sizeof(XT);
-    extern __shared__ __align__(16) uint8_t lds[];    // each wave's rows, then the waves' sums
+    constexpr int kPieces = Op::kPieces, kUnit = 8 * sizeof(XT);
+#pragma unroll
+    for (int g = 0; g < GS; ++g) {
+        mx_f4 P[NT][MT] = {}, X[MT] = {};
+#pragma unroll
+        for (int s = g * 4 / GS; s < (g + 1) * 4 / GS; ++s) {
+            V b[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) b[j] = w4_codes<typename Op::E>(c[j][s]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                V v[kPieces];
+                pieces<XT>(get8<XT>(from + 16 * i * pitch + 4 * s * kUnit), v);
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p) {
+                    X[i] = Op::mfma16(v[p], Op::ones(), X[i]);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) P[j][i] = Op::mfma16(v[p], b[j], P[j][i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const float sv = scale(g, j), zv = zero(g, j);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[j][i][r] += sv * (P[j][i][r] - zv * X[i][r]);
+        }
+        // One group's products at a time, the sums made right after them: put off to the end
+        // they keep many groups' products in registers, and the waves that would hide the
+        // loads out.
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) asm volatile("" : "+v"(acc[j][i]));
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// The waves' sums added in the order of the waves, and stored: columns from n0 on of the rows
+// first .. first + count - 1 of the MT row tiles at row0. live(r): not a row of no token.
+template <int NT, int MT, typename Live>
+__device__ __forceinline__ void add_and_store(const W4GemmArgs& a, float* red, const mx_f4 (&acc)[NT][MT], int row0, int first,
+                                              int count, int n0, Live live) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    __syncthreads();                                       // [waves][NT][MT][64][4]
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) reinterpret_cast<mx_f4*>(red)[((wave * NT + j) * MT + i) * 64 + lane] = acc[j][i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < NT * 16 * count; o += blockDim.x) {
+        const int c = o % (16 * NT), r = first + o / (16 * NT), m = row0 + r, n = n0 + c;
+        if (n >= a.N) continue;
+        const int at = (((c >> 4) * MT + (r >> 4)) * 64 + (r >> 2 & 3) * 16 + (c & 15)) * 4 + (r & 3);
+        float v = 0;
+        for (int s = 0; s < waves; ++s) v += red[s * NT * MT * 256 + at];
+        if (a.bias) v += a.bias[n];
+        store1(a.y, a.y_dtype, static_cast<int64_t>(m) * a.N + n, live(r) ? v : 0.0f);
+    }
+    __syncthreads();
+}
+
+// Eight values of a row from k on, zeros past K; not by a branch where K >= 8.
+template <typename XT>
+__device__ __forceinline__ MxRaw8<XT> load8(const XT* row, int k, int K, bool whole) {
+    if (whole) return mx_load8(row + k, 8);
+    return K >= 8 ? mx_load8_tail(row, k, K, K) : mx_load8(row + k, K - k);
+}
+
+// At most RB (1 or 4) rows and 16 columns a workgroup, its waves each a run of K in quads of
+// code tiles (512 inputs), which are loaded while the quad before is multiplied. A row reaches
+// the matrix instructions through LDS, one load of 1 KB a quad; the sums of its groups come
+// from the lanes that loaded it. The instructions' rows 0 .. RB - 1 (lanes 0 .. 15 of the
+// result) are the rows, the others repeat the last. GS: groups in 128 inputs.
+template <typename XT, int GS, bool Z, int RB>
+__global__ __launch_bounds__(64 * kMaxWaves) void k_w4_one(W4GemmArgs a) {
+    typedef W4Op<XT> Op;
+    typedef typename Op::V V;
+    constexpr int kUnit = 8 * sizeof(XT), kPieces = Op::kPieces;
+    // rows a quad at a time, 16 bytes apart in the banks
+    constexpr int kPitch = 512 * sizeof(XT) + 16;
+    __shared__ __align__(16) uint8_t lds[kMaxWaves * RB * kPitch];
+    __shared__ float sums[kMaxWaves][RB][16];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int G = (a.K + 127) / 128, Q = (G + 3) / 4, n_tiles = (a.N + 15) / 16;
+    const bool bf = a.scale_dtype == MQ_BF16;
+    uint8_t* const mine = lds + wave * RB * kPitch;
+    const int q0 = static_cast<int>(static_cast<int64_t>(Q) * wave / waves);
+    const int q1 = static_cast<int>(static_cast<int64_t>(Q) * (wave + 1) / waves);
+    // dense: RB rows; of a plan, 16 rows of one expert
+    const int per = a.offsets ? 16 : RB;
+    for (int row0 = blockIdx.y * per; row0 < a.M; row0 += gridDim.y * per) {
+        int e = 0, rows = min(RB, a.M - row0);
+        uint64_t alive = ~0ull;                            // which of a plan's rows have a token
+        if (a.offsets) {
+            const int token = a.row_token[row0 + (lane & 15)];
+            alive = __ballot(static_cast<unsigned>(token) < static_cast<unsigned>(a.T)) & 0xffff;
+            e = __builtin_amdgcn_readfirstlane(expert_of(a.offsets, a.E, row0));
+            if (e < 0) alive = 0;
+            rows = alive ? 64 - __builtin_clzll(alive) : 0;
+            for (int o = threadIdx.x; o < 256; o += blockDim.x)                    // zeros for the others
+                if (!(alive >> (o >> 4) & 1) && blockIdx.x * 16 + (o & 15) < a.N)
+                    store1(a.y, a.y_dtype, static_cast<int64_t>(row0 + (o >> 4)) * a.N + blockIdx.x * 16 + (o & 15), 0.0f);
+        }
+        const int64_t tile = static_cast<int64_t>(e) * n_tiles + blockIdx.x;
+        const uint8_t* const w = a.codes + tile * G * 1024 + lane * 16;
+        const uint16_t* const ws = a.scales + (tile * Q * 16 + (lane & 15)) * 4 * GS;
+        const uint16_t* const wz = Z ? a.zeros + (tile * Q * 16 + (lane & 15)) * 4 * GS : nullptr;
+        for (int r0 = 0; r0 < rows; r0 += RB) {
+            const int here = min(RB, rows - r0);
+            const XT* from[RB];
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                int64_t r = row0 + r0 + min(i, here - 1);
+                if (a.by_token) {
+                    const int t = a.row_token[r];
+                    r = static_cast<unsigned>(t) < static_cast<unsigned>(a.T) ? t : 0;
+                }
+                from[i] = static_cast<const XT*>(a.x) + r * a.stride_x;
+            }
+            MxRaw8<XT> v[RB];
+            mx_i4 c[4], cc[4];
+            Quad<GS> sc, zc, ss, zz;
+            auto load = [&](int q) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+                    if (i < here) v[i] = load8(from[i], 512 * q + 8 * lane, a.K, 512 * (q + 1) <= a.K);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)                // past K: the last tile, times zeros
+                    c[u] = *reinterpret_cast<const mx_i4*>(w + static_cast<int64_t>(min(4 * q + u, G - 1)) * 1024);
+                sc.load(ws + static_cast<int64_t>(q) * 64 * GS);
+                if constexpr (Z) zc.load(wz + static_cast<int64_t>(q) * 64 * GS);
+            };
+            float acc[RB] = {};
+            const uint8_t* const mine_at = mine + min(lane & 15, here - 1) * kPitch + (lane >> 4) * kUnit;
+            if (q0 < q1) load(q0);
+            for (int q = q0; q < q1; ++q) {
+                int X[RB];                                 // a lane's group's sum
+                mx_wave_sync();                            // the last quad's reads come first
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+                    X[i] = 0;
+                    if (i >= here) continue;
+                    put8(mine + i * kPitch + lane * kUnit, v[i]);
+                    float f[8];
+                    w4_values(v[i], f);
+                    X[i] = w4_over_group(__float_as_int(((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]))), 128 / GS,
+                                         [](int p, int r) { return __float_as_int(__int_as_float(p) + __int_as_float(r)); });
+                }
+                mx_wave_sync();
+#pragma unroll
+                for (int u = 0; u < 4; ++u) cc[u] = c[u];
+                ss = sc;
+                zz = zc;
+                if (q + 1 < q1) load(q + 1);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    mx_f4 P[GS] = {};
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        V x[kPieces];
+                        pieces<XT>(get8<XT>(mine_at + (16 * u + 4 * s) * kUnit), x);
+                        const V b = w4_codes<typename Op::E>(cc[u][s]);
+#pragma unroll
+                        for (int p = 0; p < kPieces; ++p) P[s * GS / 4] = Op::mfma16(x[p], b, P[s * GS / 4]);
+                    }
+#pragma unroll
+                    for (int g = 0; g < GS; ++g) {
+                        const float sv = ss.get(u * GS + g, bf), zv = Z ? zz.get(u * GS + g, bf) : 8.0f;
+#pragma unroll
+                        for (int i = 0; i < RB; ++i)
+                            acc[i] += sv * (P[g][i] - zv * __int_as_float(__builtin_amdgcn_readlane(X[i], (u * GS + g) * (16 / GS))));
+                    }
+                    // Two tiles' products at a time, the sums made right after them: put off to the
+                    // end they keep a quad's products in registers, and the waves that would
+                    // hide the loads out.
+                    if (u & 1) {
+#pragma unroll
+                        for (int i = 0; i < RB; ++i) asm volatile("" : "+v"(acc[i]));
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+            // the waves' sums, in the order of the waves
+            if (lane < 16) {
+#pragma unroll
+                for (int i = 0; i < RB; ++i) sums[wave][i][lane] = acc[i];
+            }
+            __syncthreads();
+            const int n = blockIdx.x * 16 + (threadIdx.x & 15), i = threadIdx.x >> 4;
+            if (i < here && n < a.N && (alive >> (r0 + i) & 1)) {
+                float y = 0;
+                for (int s = 0; s < waves; ++s) y += sums[s][i][threadIdx.x & 15];
+                if (a.bias) y += a.bias[n];
+                store1(a.y, a.y_dtype, static_cast<int64_t>(row0 + r0 + i) * a.N + n, y);
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// One workgroup: 16 MT rows x NT column tiles of 16, its waves each a run of K, tile by tile;
+// rows reach the matrix instructions through LDS (256 bytes of four rows a load; lanes that
+// read their own operands, 64 bytes of 16 rows, take twice the time).
+template <typename XT, int GS, bool Z, int NT, int MT, int W>
+__global__ __launch_bounds__(64 * W) void k_w4_few(W4GemmArgs a) {
+    constexpr int kPitch = kRowPitch<XT>, kUnit = 8 * sizeof(XT);
+    // each wave's rows, then the waves' sums
+    __shared__ __align__(16) uint8_t lds[W * (16 * MT * kPitch > NT * MT * 1024 ? 16 * MT * kPitch : NT * MT * 1024)];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int G = (a.K + 127) / 128, Q = (G + 3) / 4, n_tiles = (a.N + 15) / 16, ct = blockIdx.x * NT;
@@ -104,28 +366,29 @@ __global__ __launch_bounds__(512) void k_w4_few(W4GemmArgs a) {
     const bool bf = a.scale_dtype == MQ_BF16;
     uint8_t* const mine = lds + wave * 16 * MT * kPitch;
     for (int rb = blockIdx.y; rb < blocks; rb += gridDim.y) {
-        const int row0 = rb * 16 * MT, rows = min(16 * MT, a.M - row0);
-        int e = 0;
-        uint64_t alive = ~0ull;                        // which of a plan's rows have a token
-        // lane l loads inputs 8 (l % 16) .. of rows 4j + l / 16
-        const XT* from[4 * MT];
-        if (a.offsets) {
-            const int token = a.row_token[row0 + (lane & 15)];                     // (MT = 1)
+        const int row0 = rb * 16 * MT;
+        int rows = min(16 * MT, a.M - row0), e = 0;
+        uint64_t alive = ~0ull;                            // which of a plan's rows have a token
+        if (a.offsets) {                                   // (MT = 1) lane l % 16 is row l % 16
+            const int token = a.row_token[row0 + (lane & 15)];
             alive = __ballot(static_cast<unsigned>(token) < static_cast<unsigned>(a.T)) & 0xffff;
             e = __builtin_amdgcn_readfirstlane(expert_of(a.offsets, a.E, row0));
             if (e < 0) alive = 0;
-        }
-#pragma unroll
-        for (int j = 0; j < 4 * MT; ++j) {
-            int64_t r = row0 + min(4 * j + (lane >> 4), rows - 1);
-            if (a.by_token) {
-                const int t = a.row_token[r];
-                r = static_cast<unsigned>(t) < static_cast<unsigned>(a.T) ? t : 0;
-            }
-            from[j] = static_cast<const XT*>(a.x) + r * a.stride_x + 8 * (lane & 15);
+            rows = 64 - __builtin_clzll(alive | 1);
         }
         mx_f4 acc[NT][MT] = {};
         if (alive) {
+            // lane l brings inputs 8 (l % 16) .. of rows 4i + l / 16
+            const XT* from[4 * MT];
+#pragma unroll
+            for (int i = 0; i < 4 * MT; ++i) {
+                int64_t r = row0 + min(4 * i + (lane >> 4), rows - 1);
+                if (a.by_token) {
+                    const int t = a.row_token[r];
+                    r = static_cast<unsigned>(t) < static_cast<unsigned>(a.T) ? t : 0;
+                }
+                from[i] = static_cast<const XT*>(a.x) + r * a.stride_x;
+            }
             const uint8_t* w[NT];
             const uint16_t *ws[NT], *wz[NT];
 #pragma unroll
@@ -139,100 +402,67 @@ __global__ __launch_bounds__(512) void k_w4_few(W4GemmArgs a) {
             const int h1 = static_cast<int>(static_cast<int64_t>(G) * (wave + 1) / waves);
             for (int h = h0; h < h1; ++h) {
                 MxRaw8<XT> v[4 * MT];
-                mx_i4 wc[NT];
+                mx_i4 c[NT];
                 uint64_t sc[NT], zc[NT] = {};
 #pragma unroll
-                for (int j = 0; j < 4 * MT; ++j) v[j] = mx_load8(from[j] + h * 128, a.K - h * 128 - 8 * (lane & 15));
+                for (int i = 0; i < 4 * MT; ++i)
+                    if (4 * i < rows) v[i] = load8(from[i], 128 * h + 8 * (lane & 15), a.K, 128 * (h + 1) <= a.K);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    wc[j] = *reinterpret_cast<const mx_i4*>(w[j] + static_cast<int64_t>(h) * 1024);
+                    c[j] = *reinterpret_cast<const mx_i4*>(w[j] + static_cast<int64_t>(h) * 1024);
                     const int at = ((h >> 2) * 16 * 4 + (h & 3)) * GS;
                     sc[j] = load_scales<GS>(ws[j] + at);
                     if constexpr (Z) zc[j] = load_scales<GS>(wz[j] + at);
                 }
-                mx_wave_sync();                        // the last tile's reads come first
+                mx_wave_sync();                            // the last tile's reads come first
 #pragma unroll
-                for (int j = 0; j < 4 * MT; ++j) {
-                    uint8_t* const to = mine + (4 * j + (lane >> 4)) * kPitch + (lane & 15) * kUnit;
-                    if constexpr (sizeof(XT) == 2) {
-                        *reinterpret_cast<w4_u4*>(to) = w4_u4{v[j].w[0], v[j].w[1], v[j].w[2], v[j].w[3]};
-                    } else {
-                        *reinterpret_cast<mx_f4*>(to) = mx_f4{v[j].v[0], v[j].v[1], v[j].v[2], v[j].v[3]};
-                        *reinterpret_cast<mx_f4*>(to + 16) = mx_f4{v[j].v[4], v[j].v[5], v[j].v[6], v[j].v[7]};
-                    }
-                }
+                for (int i = 0; i < 4 * MT; ++i)
+                    if (4 * i < rows) put8(mine + (4 * i + (lane >> 4)) * kPitch + (lane & 15) * kUnit, v[i]);
                 mx_wave_sync();
-#pragma unroll
-                for (int g = 0; g < GS; ++g) {
-                    mx_f4 P[NT][MT] = {}, X[MT] = {};
-#pragma unroll
-                    for (int s = g * 4 / GS; s < (g + 1) * 4 / GS; ++s) {
-                        V b[NT];
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) b[j] = w4_codes<typename Op::E>(wc[j][s]);
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            V x[kPieces];
-                            pieces<XT>(mine + (16 * i + (lane & 15)) * kPitch + (4 * s + (lane >> 4)) * kUnit, x);
-#pragma unroll
-                            for (int p = 0; p < kPieces; ++p) {
-                                X[i] = Op::mfma16(x[p], Op::ones(), X[i]);
-#pragma unroll
-                                for (int j = 0; j < NT; ++j) P[j][i] = Op::mfma16(x[p], b[j], P[j][i]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const float sv = w4_float(static_cast<uint32_t>(sc[j] >> 16 * g) & 0xffff, bf);
-                        const float zv = Z ? w4_float(static_cast<uint32_t>(zc[j] >> 16 * g) & 0xffff, bf) : 8.0f;
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) acc[j][i][r] += sv * (P[j][i][r] - zv * X[i][r]);
-                    }
-                }
+                tile_products<XT, GS>(c, mine + (lane & 15) * kPitch + (lane >> 4) * kUnit, kPitch,
+                                      [&](int g, int j) __attribute__((always_inline)) { return w4_float(static_cast<uint32_t>(sc[j] >> 16 * g) & 0xffff, bf); },
+                                      [&](int g, int j) __attribute__((always_inline)) {
+                                          return Z ? w4_float(static_cast<uint32_t>(zc[j] >> 16 * g) & 0xffff, bf) : 8.0f;
+                                      },
+                                      acc);
             }
         }
-        float* const red = reinterpret_cast<float*>(lds);   // [waves][NT][MT][64][4]
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) reinterpret_cast<mx_f4*>(red)[((wave * NT + j) * MT + i) * 64 + lane] = acc[j][i];
-        __syncthreads();
-        // output o: column o % (16 NT) of row o / (16 NT)
-        for (int o = threadIdx.x; o < NT * MT * 256; o += blockDim.x) {
-            const int c = o % (16 * NT), r = o / (16 * NT), m = row0 + r, n = ct * 16 + c;
-            if (m >= a.M || n >= a.N) continue;
-            const int at = (((c >> 4) * MT + (r >> 4)) * 64 + (r >> 2 & 3) * 16 + (c & 15)) * 4 + (r & 3);
-            float v = 0;
-            for (int s = 0; s < waves; ++s) v += red[s * NT * MT * 256 + at];
-            if (a.bias) v += a.bias[n];
-            if (a.offsets && !(alive >> (r & 15) & 1)) v = 0;
-            store1(a.y, a.y_dtype, static_cast<int64_t>(m) * a.N + n, v);
-        }
-        __syncthreads();
+        add_and_store(a, reinterpret_cast<float*>(lds), acc, row0, 0, min(16 * MT, a.M - row0), ct * 16,
+                      [&](int r) { return !a.offsets || (alive >> (r & 15) & 1); });
     }
 }
 
-template <typename XT, int GS, bool Z, int NT, int MT>
+template <typename XT, int GS, bool Z, int NT, int MT, int W>
 hipError_t few(const W4GemmArgs& a, hipStream_t st) {
-    const int G = (a.K + 127) / 128;
-    const int most = MT == 1 ? 8 : 4, want = G >= 32 ? 8 : (G >= 8 ? 4 : (G >= 4 ? 2 : 1)), waves = want < most ? want : most;
+    const int G = (a.K + 127) / 128, want = G >= 32 ? 8 : (G >= 8 ? 4 : (G >= 4 ? 2 : 1)), waves = want < W ? want : W;
     const unsigned cols = static_cast<unsigned>(((a.N + 15) / 16 + NT - 1) / NT);
     const int blocks = (a.M + 16 * MT - 1) / (16 * MT);
-    const size_t one = 16 * MT * kRowPitch<XT>, sums = NT * MT * 1024;
-    k_w4_few<XT, GS, Z, NT, MT><<<dim3(cols, blocks < 65535 ? blocks : 65535), 64 * waves, waves * (one > sums ? one : sums), st>>>(a);
+    k_w4_few<XT, GS, Z, NT, MT, W><<<dim3(cols, blocks < 65535 ? blocks : 65535), 64 * waves, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+template <typename XT, int GS, bool Z, int RB>
+hipError_t one(const W4GemmArgs& a, hipStream_t st) {
+    const int Q = (a.K + 511) / 512, each = (Q + kMaxWaves - 1) / kMaxWaves, waves = (Q + each - 1) / each;
+    const int blocks = a.offsets ? a.M / 16 : (a.M + RB - 1) / RB;
+    k_w4_one<XT, GS, Z, RB><<<dim3((a.N + 15) / 16, blocks < 65535 ? blocks : 65535), 64 * waves, 0, st>>>(a);
     return hipGetLastError();
 }
 
 template <typename XT, int GS, bool Z>
 hipError_t few_rows(const W4GemmArgs& a, hipStream_t st) {
+    const char* wy = getenv("W4_FEW"); const int way = wy ? atoi(wy) : 0;
+    const int rows = a.offsets ? a.T : a.M;
+    if (rows == 1) return one<XT, GS, Z, 1>(a, st);
+    if (rows <= 4) return one<XT, GS, Z, 4>(a, st);
     if constexpr (sizeof(XT) == 2) {
-        if (!a.offsets && a.M > 16) return few<XT, GS, Z, 2, 2>(a, st);
+        if (!a.offsets && way == 1) return few<XT, GS, Z, 2, 1, 8>(a, st);
+        if (!a.offsets && way == 2) return few<XT, GS, Z, 2, 2, 4>(a, st);
+        if (!a.offsets && way == 3) return few<XT, GS, Z, 4, 2, 8>(a, st);
+        if (!a.offsets && way == 4) return few<XT, GS, Z, 2, 2, 8>(a, st);
+        if (!a.offsets && way == 5) return few<XT, GS, Z, 4, 2, 4>(a, st);
     }
-    return few<XT, GS, Z, 1, 1>(a, st);
+    return few<XT, GS, Z, 1, 1, 8>(a, st);
 }
 
 template <typename XT>
