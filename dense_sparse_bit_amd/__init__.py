@@ -81,6 +81,7 @@ _SIGS.update({
     "mq_w4_quantize": [_p, _int, _i64, _i64, _i64, _i64, _i64, _int, _int, _p, _p, _p, _p],
     "mq_w4_pack": [_p, _i64, _i64, _i64, _i64, _i64, _int, _p, _p, _p, _p, _p, _p],
     "mq_w4_dequantize": [_p, _p, _p, _int, _i64, _i64, _i64, _int, _p, _int, _p],
+    "mq_w4_linear_way": [_i64, _i64, _i64, _int, _int],
     "mq_w4_linear": [_p, _int, _i64, _p, _p, _p, _int, _int, _i64, _i64, _i64, _p, _p, _int, _p, C.c_size_t, _p],
     "mq_w4_experts": [_p, _int, _i64, _int, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _int, _int, _p, _int, _p,
                       C.c_size_t, _p],

@@ -1,8 +1,8 @@
 // C ABI of the group-scaled 4-bit operators and of the calls between tokens and their
 // experts' rows: argument checks, then kernel launches. Declarations and the meaning of
 // every argument are in include/mq.h.
+#include <math.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include "../../include/mq.h"
 #include "mx_internal.h"
@@ -21,7 +21,7 @@ constexpr int64_t kMaxRows = int64_t(1) << 24;
 constexpr int64_t kMaxCols = int64_t(1) << 20;
 constexpr int64_t kMaxElements = int64_t(1) << 40;
 constexpr int64_t kMaxBatch = 65535;
-constexpr int64_t kMaxPitch = int64_t(1) << 22;       // of rows that the tiles take as they are: 128 of them within 32 bits
+constexpr int64_t kMaxOffset = 0xffffffff;             // of x's rows in the tiles: of a block's, or of all tokens'
 constexpr int64_t kMaxSlots = int64_t(1) << 27;
 
 int check_matrix(int64_t B, int64_t R, int64_t K, int group) {
@@ -116,40 +116,117 @@ mq::RowsArgs rows_of(int64_t T, int64_t k, int64_t E, int64_t D, const void* x, 
 
 size_t round16(int64_t n) { return static_cast<size_t>((n + 15) / 16 * 16); }
 
-// The way of a product: a run of K a wave (launch_w4_few), or tiles of 32 rt rows and 128 ct
-// columns.
+// The way of a product: a kernel of few rows, or (rt > 0) tiles of 32 rt rows and 128 ct columns
+// with K in `parts`.
 struct Way {
-    int rt, ct;                                        // rt 0: few rows
+    mq::W4Few few;
+    int rt, ct, parts;
 };
-Way dense_way(int64_t M, int64_t N, int64_t K, int planes) {
-    if (const char* s = getenv("W4_WAY")) return {s[0] - '0', s[1] - '0'};
-    if (M <= 64) return {0, 0};
-    return {2, 2};
+
+// Parts of K are whole stages of the tiles, one at least.
+Way tiles_way(int rt, int ct, int64_t parts, int64_t stages) {
+    return {mq::kW4One, rt, ct, static_cast<int>(parts < 1 ? 1 : (parts < stages ? parts : stages))};
 }
-Way experts_way(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int planes) {
-    if (const char* s = getenv("W4_WAY")) return {s[0] - '0', s[1] - '0'};
-    if (T * k <= 16 * E) return {0, 0};
-    return {4, 2};
+
+// The costs below are fits, in us, of times measured on weights that no cache holds: ten
+// sizes from 1024 x 1024 to 17408 x 5120, 2 to 2048 rows, every way. Over the 150 sizes of
+// more than four rows the choice is within 22% of the fastest way, 2% on average.
+//
+// A kernel of few rows: in rounds of workgroups (`per` rounds for each 256 of eight waves), a start
+// and each wave's code tiles, whose time grows with the groups in them.
+double few_cost(int64_t M, int64_t N, int64_t K, int group, int rows, int cols, double start, double round, double tile,
+                double per, double groups) {
+    const double G = static_cast<double>(mq::w4_tiles(K)), waves = G >= 32 ? 8 : (G >= 8 ? 4 : (G >= 4 ? 2 : 1));
+    const double n = static_cast<double>((N + cols - 1) / cols) * static_cast<double>((M + rows - 1) / rows) / 256;
+    return start + (round + tile * (G / waves) * (1 + groups * (128 / group - 1))) * fmax(1.0, per * n * waves / 8);
+}
+
+// Tiles: the sums of the rows' groups, then the stages, each as long as its chain of
+// instructions where a CU has one workgroup (alone) and as its products where it has more;
+// the parts' sums written, read and added.
+struct TileCost {
+    int rt, ct;
+    double start, alone, busy, join, moved, groups;
+};
+constexpr TileCost kTiles[] = {{1, 1, 8.13, 0.59, 0.40, 2.48, 0.57, 0.17},
+                               {2, 1, 8.44, 0.68, 0.59, 2.65, 0.42, 0.22},
+                               {2, 2, 9.63, 1.04, 1.09, 3.06, 0.35, 0.28},
+                               {3, 2, 9.93, 1.41, 1.20, 2.57, 0.35, 0.27},
+                               {4, 2, 10.8, 1.72, 1.52, 2.16, 0.35, 0.22}};
+double tile_cost(const TileCost& c, int64_t M, int64_t N, int64_t K, int planes, int group, int parts) {
+    const double tiles = static_cast<double>((M + 32 * c.rt - 1) / (32 * c.rt)) * static_cast<double>((N + 128 * c.ct - 1) / (128 * c.ct));
+    const double n = tiles * parts / 256, stages = static_cast<double>(mq::w4_tiles(K) * planes) / parts;
+    const double stage = fmax(c.alone, c.busy * (c.rt >= 3 && n > 1 ? ceil(n) : n));
+    const double rows = static_cast<double>(M) * static_cast<double>(K) * planes * 0.67e-6;
+    const double join = parts > 1 ? c.join + c.moved * parts * static_cast<double>(M) * static_cast<double>(N) * 4e-6 : 0;
+    return c.start + rows + stages * stage * (1 + c.groups * (128 / group - 1)) + join;
+}
+
+Way dense_way(int64_t M, int64_t N, int64_t K, int x_dtype, int group) {
+    const int planes = mq::w4_planes(x_dtype);
+    const int64_t stages = mq::w4_tiles(K) * planes;
+    // Four rows, 4096 x 4096: by four 5.8 us, by 16 7.7; 14336 x 4096: 17.8, 12.2. Sixteen rows,
+    // 16 columns a workgroup / 32: 7.3 / 8.2 and 18.0 / 14.0.
+    if (M == 1 || (M <= 4 && N <= 8192)) return {mq::kW4One, 0, 0, 1};
+    if (M <= 16) return {N <= 8192 ? mq::kW4Rows16 : mq::kW4Rows16x32, 0, 0, 1};
+    Way best = {mq::kW4Rows16, 0, 0, 1};
+    double least = 1e300;
+    auto take = [&](Way w, double cost) {
+        if (cost < least) {
+            least = cost;
+            best = w;
+        }
+    };
+    if (M <= 256) {
+        if (planes == 1) {
+            take({mq::kW4Rows32x32, 0, 0, 1}, few_cost(M, N, K, group, 32, 32, 1.66, 2.53, 1.37, 1.18, 0.22));
+            take({mq::kW4Rows32x64, 0, 0, 1}, few_cost(M, N, K, group, 32, 64, 2.81, 2.47, 1.88, 1.40, 0.24));
+        } else {                                           // fp32 rows: three times the products
+            take({mq::kW4Rows16, 0, 0, 1}, few_cost(M, N, K, group, 16, 16, 0, 2.51, 2 * 0.98, 0.73, 0.12));
+        }
+    }
+    for (const TileCost& c : kTiles) {
+        if (c.rt == 4 && group == 32) continue;
+        const int64_t tiles = ((M + 32 * c.rt - 1) / (32 * c.rt)) * ((N + 128 * c.ct - 1) / (128 * c.ct));
+        for (int parts = 1; parts <= 8; parts *= 2)
+            if (parts == 1 || (stages >= 4 * parts && tiles * parts <= 1100))
+                take(tiles_way(c.rt, c.ct, parts, stages), tile_cost(c, M, N, K, planes, group, parts));
+    }
+    return best;
+}
+
+// 64 experts, 8 a token, 1024 x 4096 / 4096 x 1024, in us: 1 token one row at a time 5.9 / 5.7, by
+// 16 rows 6.8 / 7.0; 64 tokens by 16 rows 39 / 43, by tiles 51 / 43; 128 tokens 51 / 58 and 51 / 44.
+// By 16 rows, 32 columns a workgroup / 64: 1024 x 4096 39 / 48, 4096 x 1024 49 / 43. K in parts
+// for tiles of 256 tokens: 65 / 61 / 59 in 1, 2, 4 (1024 x 4096) and 51 / 77 / 124.
+Way experts_way(int64_t T, int64_t k, int64_t E, int64_t K, bool by_token, int x_dtype, int group) {
+    if (T == 1) return {mq::kW4One, 0, 0, 1};
+    // the tiles find tokens' rows by offsets of 32 bits (in a copy, where x's own are too far apart)
+    const bool held = !by_token || mq::w4_copy_size(T, K, mq::w4_planes(x_dtype)) <= kMaxOffset;
+    if (T * k <= 12 * E || !held) return {K > 2048 || x_dtype == MQ_F32 ? mq::kW4Rows16x32 : mq::kW4Rows16x64, 0, 0, 1};
+    return tiles_way(group == 32 ? 3 : 4, 2, 1, 1);
 }
 
 // Workspace of the tiles: the rows' sums, a copy of the rows, row blocks
 struct Parts {
-    size_t copy, tiles, bytes;
-    Parts(int64_t R, int64_t K, int x_dtype, int group, int64_t blocks) {
+    size_t copy, tiles, partial, bytes;
+    Parts(int64_t R, int64_t K, int x_dtype, int group, int64_t blocks, int parts, int64_t M, int64_t N) {
         const int planes = mq::w4_planes(x_dtype);
         copy = mq::w4_sums_size(R, K, planes, group);
         tiles = copy + round16(mq::w4_copy_size(R, K, planes));
-        bytes = tiles + round16(blocks ? (4 + 4 * blocks) * 4 : 0);
+        partial = tiles + round16(blocks ? (4 + 4 * blocks) * 4 : 0);
+        bytes = partial + (parts > 1 ? round16(parts * M * N * 4) : 0);
     }
 };
 
 // The rows' part, then the tiles. R: rows of x.
 int wide(const mq::W4GemmArgs& a, Way way, int64_t R, const int32_t* offsets, void* workspace, size_t workspace_bytes, hipStream_t st) {
-    const int64_t blocks = offsets ? mq::mx_tiles_cap(a.M, a.E) : 0;
-    const Parts parts(R, a.K, a.x_dtype, a.group, blocks);
+    const int64_t blocks = offsets ? mq::w4_blocks_cap(a.M, a.E, way.rt) : 0;
+    const Parts parts(R, a.K, a.x_dtype, a.group, blocks, way.parts, a.M, a.N);
     if (workspace_bytes < parts.bytes || !workspace || off(workspace, 16)) return MQ_ERR_INVALID_ARG;
     uint8_t* const work = static_cast<uint8_t*>(workspace);
-    const bool as_it_is = a.x_dtype != MQ_F32 && !off(a.x, 16) && a.stride_x % 8 == 0 && a.K % 128 == 0 && a.stride_x <= kMaxPitch;
+    const bool as_it_is = a.x_dtype != MQ_F32 && !off(a.x, 16) && a.stride_x % 8 == 0 && a.K % 128 == 0 &&
+                          a.stride_x <= kMaxOffset / 2 / (a.by_token ? R + 1 : 129);
     mq::W4RowsArgs r = {};
     r.x = a.x;
     r.dtype = a.x_dtype;
@@ -160,6 +237,7 @@ int wide(const mq::W4GemmArgs& a, Way way, int64_t R, const int32_t* offsets, vo
     r.sums = work;
     r.copy = as_it_is ? nullptr : work + parts.copy;
     int32_t* const tiles = reinterpret_cast<int32_t*>(work + parts.tiles);
+    r.rt = way.rt;
     if (offsets) r.plan = {offsets, a.E, a.M / 16, tiles, static_cast<int>(blocks)};
     if (mq::launch_w4_rows(r, st) != hipSuccess) return MQ_ERR_HIP;
     mq::W4WideArgs w = {};
@@ -186,6 +264,8 @@ int wide(const mq::W4GemmArgs& a, Way way, int64_t R, const int32_t* offsets, vo
     w.by_token = a.by_token;
     w.E = a.E;
     w.T = a.T;
+    w.parts = way.parts;
+    w.partial = way.parts > 1 ? reinterpret_cast<float*>(work + parts.partial) : nullptr;
     return status_of(mq::launch_w4_wide(w, way.rt, way.ct, st));
 }
 
@@ -249,8 +329,17 @@ int mq_w4_dequantize(const uint8_t* codes, const void* scales, const void* zeros
 }
 
 size_t mq_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_dtype, int group) {
-    if (check_product(M, N, K, group) || bad_type(x_dtype) || !dense_way(M, N, K, mq::w4_planes(x_dtype)).rt) return 0;
-    return Parts(M, K, x_dtype, group, 0).bytes;
+    if (check_product(M, N, K, group) || bad_type(x_dtype)) return 0;
+    const Way way = dense_way(M, N, K, x_dtype, group);
+    return way.rt ? Parts(M, K, x_dtype, group, 0, way.parts, M, N).bytes : 0;
+}
+
+int mq_w4_linear_way(int64_t M, int64_t N, int64_t K, int x_dtype, int group) {
+    const int rc = check_product(M, N, K, group);
+    if (rc) return rc;
+    if (bad_type(x_dtype)) return MQ_ERR_INVALID_ARG;
+    const Way way = dense_way(M, N, K, x_dtype, group);
+    return way.rt ? 8 * way.parts + (way.ct == 1 ? way.rt - 1 : way.rt) : way.few;
 }
 
 int mq_w4_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* codes, const void* scales, const void* zeros,
@@ -266,14 +355,15 @@ int mq_w4_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* co
     mq::W4GemmArgs a = product(x, x_dtype, stride_m, codes, scales, zeros, scale_dtype, group, M, N, K, y, y_dtype);
     a.bias = bias;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const Way way = dense_way(M, N, K, mq::w4_planes(x_dtype));
-    return way.rt ? wide(a, way, M, nullptr, workspace, workspace_bytes, st) : status_of(mq::launch_w4_few(a, st));
+    const Way way = dense_way(M, N, K, x_dtype, group);
+    return way.rt ? wide(a, way, M, nullptr, workspace, workspace_bytes, st) : status_of(mq::launch_w4_few(a, way.few, st));
 }
 
 size_t mq_w4_experts_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int by_token, int x_dtype, int group) {
-    if (check_experts(T, k, E, N, K, group) || bad_type(x_dtype) || !experts_way(T, k, E, N, K, mq::w4_planes(x_dtype)).rt) return 0;
+    if (check_experts(T, k, E, N, K, group) || bad_type(x_dtype)) return 0;
+    const Way way = experts_way(T, k, E, K, by_token != 0, x_dtype, group);
     const int64_t P = mq::plan_rows(T, k, E);
-    return Parts(by_token ? T : P, K, x_dtype, group, mq::mx_tiles_cap(P, E)).bytes;
+    return way.rt ? Parts(by_token ? T : P, K, x_dtype, group, mq::w4_blocks_cap(P, E, way.rt), way.parts, P, N).bytes : 0;
 }
 
 int mq_w4_experts(const void* x, int x_dtype, int64_t stride_r, int by_token, int64_t T, int64_t k, int64_t E, int64_t N,
@@ -294,8 +384,8 @@ int mq_w4_experts(const void* x, int x_dtype, int64_t stride_r, int by_token, in
     a.E = static_cast<int>(E);
     a.T = static_cast<int>(T);
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const Way way = experts_way(T, k, E, N, K, mq::w4_planes(x_dtype));
-    return way.rt ? wide(a, way, by_token ? T : a.M, offsets, workspace, workspace_bytes, st) : status_of(mq::launch_w4_few(a, st));
+    const Way way = experts_way(T, k, E, K, by_token != 0, x_dtype, group);
+    return way.rt ? wide(a, way, by_token ? T : a.M, offsets, workspace, workspace_bytes, st) : status_of(mq::launch_w4_few(a, way.few, st));
 }
 
 int mq_experts_gather(const void* x, int x_dtype, int64_t stride_t, int64_t T, int64_t k, int64_t E, int64_t D,

@@ -6,8 +6,6 @@
 // so P is a sum of exact products on the matrix instructions, held in fp32, and the scales,
 // which 16 bits would round, come in once a group in fp32. X comes from the same
 // instructions, against ones.
-#include <stdlib.h>
-
 #include "w4_device.h"
 #include "w4_internal.h"
 
@@ -450,35 +448,30 @@ hipError_t one(const W4GemmArgs& a, hipStream_t st) {
 }
 
 template <typename XT, int GS, bool Z>
-hipError_t few_rows(const W4GemmArgs& a, hipStream_t st) {
-    const char* wy = getenv("W4_FEW"); const int way = wy ? atoi(wy) : 0;
-    const int rows = a.offsets ? a.T : a.M;
-    if (rows == 1) return one<XT, GS, Z, 1>(a, st);
-    if (rows <= 4) return one<XT, GS, Z, 4>(a, st);
+hipError_t few_rows(const W4GemmArgs& a, W4Few kind, hipStream_t st) {
+    if (kind == kW4One) return a.offsets || a.M == 1 ? one<XT, GS, Z, 1>(a, st) : one<XT, GS, Z, 4>(a, st);
     if constexpr (sizeof(XT) == 2) {
-        if (!a.offsets && way == 1) return few<XT, GS, Z, 2, 1, 8>(a, st);
-        if (!a.offsets && way == 2) return few<XT, GS, Z, 2, 2, 4>(a, st);
-        if (!a.offsets && way == 3) return few<XT, GS, Z, 4, 2, 8>(a, st);
-        if (!a.offsets && way == 4) return few<XT, GS, Z, 2, 2, 8>(a, st);
-        if (!a.offsets && way == 5) return few<XT, GS, Z, 4, 2, 4>(a, st);
+        if (kind == kW4Rows16x64) return few<XT, GS, Z, 4, 1, 8>(a, st);
+        if (kind == kW4Rows32x32) return few<XT, GS, Z, 2, 2, 8>(a, st);
+        if (kind == kW4Rows32x64) return few<XT, GS, Z, 4, 2, 8>(a, st);
     }
-    return few<XT, GS, Z, 1, 1, 8>(a, st);
+    return kind == kW4Rows16 ? few<XT, GS, Z, 1, 1, 8>(a, st) : few<XT, GS, Z, 2, 1, 8>(a, st);
 }
 
 template <typename XT>
-hipError_t few_groups(const W4GemmArgs& a, hipStream_t st) {
-    if (a.group == 128) return a.zeros ? few_rows<XT, 1, true>(a, st) : few_rows<XT, 1, false>(a, st);
-    if (a.group == 64) return a.zeros ? few_rows<XT, 2, true>(a, st) : few_rows<XT, 2, false>(a, st);
-    return a.zeros ? few_rows<XT, 4, true>(a, st) : few_rows<XT, 4, false>(a, st);
+hipError_t few_groups(const W4GemmArgs& a, W4Few kind, hipStream_t st) {
+    if (a.group == 128) return a.zeros ? few_rows<XT, 1, true>(a, kind, st) : few_rows<XT, 1, false>(a, kind, st);
+    if (a.group == 64) return a.zeros ? few_rows<XT, 2, true>(a, kind, st) : few_rows<XT, 2, false>(a, kind, st);
+    return a.zeros ? few_rows<XT, 4, true>(a, kind, st) : few_rows<XT, 4, false>(a, kind, st);
 }
 
 }  // namespace
 
-hipError_t launch_w4_few(const W4GemmArgs& a, hipStream_t st) {
+hipError_t launch_w4_few(const W4GemmArgs& a, W4Few kind, hipStream_t st) {
     switch (a.x_dtype) {
-        case MQ_F32: return few_groups<float>(a, st);
-        case MQ_BF16: return few_groups<__bf16>(a, st);
-        default: return few_groups<_Float16>(a, st);
+        case MQ_F32: return few_groups<float>(a, kind, st);
+        case MQ_BF16: return few_groups<__bf16>(a, kind, st);
+        default: return few_groups<_Float16>(a, kind, st);
     }
 }
 

@@ -46,6 +46,9 @@ struct W4GemmArgs {
 };
 
 
+// Row blocks of a plan for launch_w4_wide, as MxTilesArgs' but of at most 2 rt 16-row tiles.
+inline int64_t w4_blocks_cap(int64_t P, int64_t E, int rt) { return P / 16 / (2 * rt) + E + 2; }
+
 // What launch_w4_wide takes of x: the sums of its groups, and a copy where x itself does not
 // do (fp32, or rows that are not made of aligned 16-byte units).
 struct W4RowsArgs {
@@ -54,7 +57,8 @@ struct W4RowsArgs {
     int64_t R, stride;
     int K, group;
     void *sums, *copy;
-    MxTilesArgs plan;                // row blocks that the launch makes too
+    MxTilesArgs plan;                // row blocks that the launch makes too,
+    int rt;                          // of 32 rt rows (3 or 4)
 };
 inline int w4_planes(int x_dtype) { return x_dtype == 0 ? 3 : 1; }
 inline int64_t w4_sums_size(int64_t R, int64_t K, int planes, int group) { return w4_tiles(K) * planes * (128 / group) * R * 16; }
@@ -75,6 +79,8 @@ struct W4WideArgs {
     int y_dtype;
     const int32_t *row_token, *tiles;
     int by_token, E, T;
+    int parts;                       // of K, at most its stages (w4_tiles(K) * planes)
+    float* partial;                  // [parts][M][N] where there are more than one
 };
 
 struct RowsArgs {
@@ -95,9 +101,14 @@ struct RowsArgs {
 hipError_t launch_w4_quant(const W4QuantArgs& a, hipStream_t st);
 hipError_t launch_w4_pack(const W4QuantArgs& a, hipStream_t st);
 hipError_t launch_w4_dequant(const W4QuantArgs& a, void* y, int y_dtype, hipStream_t st);
-hipError_t launch_w4_few(const W4GemmArgs& a, hipStream_t st);
+// The kernels of few rows: up to 4 rows and 16 columns a workgroup, a quad of code tiles at a
+// time, or 16 or 32 rows and these columns, tile by tile; each splits K over its waves. fp32
+// and a plan's rows: at most 16 rows, at most 32 columns for fp32, 64 else.
+enum W4Few { kW4One, kW4Rows16, kW4Rows16x32, kW4Rows16x64, kW4Rows32x32, kW4Rows32x64 };
+hipError_t launch_w4_few(const W4GemmArgs& a, W4Few kind, hipStream_t st);
 hipError_t launch_w4_rows(const W4RowsArgs& a, hipStream_t st);
-// tiles of 32 rt rows and 128 ct columns: rt <= 2 with ct = 1, rt <= 4 with ct = 2 (4 for a plan's)
+// tiles of 32 rt rows and 128 ct columns: rt <= 2 with ct = 1, 2 <= rt <= 4 with ct = 2 (3 or 4 for
+// a plan's rows)
 hipError_t launch_w4_wide(const W4WideArgs& a, int rt, int ct, hipStream_t st);
 hipError_t launch_rows_gather(const RowsArgs& a, hipStream_t st);
 hipError_t launch_rows_combine(const RowsArgs& a, hipStream_t st);

@@ -21,11 +21,14 @@ constexpr int kThreads = 256;
 constexpr int kRows = 4;
 template <typename XT>
 __global__ __launch_bounds__(kThreads) void k_w4_rows(const XT* x, int64_t R, int64_t stride, int K, int group, uint4* sums,
-                                                      uint16_t* copy, MxTilesArgs plan) {
+                                                      uint16_t* copy, MxTilesArgs plan, int rt) {
     __shared__ int lds[kTilesLds];
     const int first = plan.offsets ? 1 : 0;            // workgroups (0, 0): the plan's row blocks alone
     if (static_cast<int>(blockIdx.x) < first) {
-        if (blockIdx.y == 0) plan_tiles<kBlockTiles>(plan, lds);
+        if (blockIdx.y == 0) {
+            if (rt == 4) plan_tiles<8>(plan, lds);
+            else plan_tiles<6>(plan, lds);
+        }
         return;
     }
     constexpr int kPlanes = sizeof(XT) == 4 ? 3 : 1;
@@ -88,7 +91,7 @@ hipError_t rows(const W4RowsArgs& a, hipStream_t st) {
     const unsigned first = a.plan.offsets ? 1 : 0;
     const dim3 grid(static_cast<unsigned>((a.R + 4 * kRows - 1) / (4 * kRows)) + first, static_cast<unsigned>((a.K + 511) / 512));
     k_w4_rows<XT><<<grid, kThreads, 0, st>>>(static_cast<const XT*>(a.x), a.R, a.stride, a.K, a.group, static_cast<uint4*>(a.sums),
-                                             static_cast<uint16_t*>(a.copy), a.plan);
+                                             static_cast<uint16_t*>(a.copy), a.plan, a.rt);
     return hipGetLastError();
 }
 
@@ -112,11 +115,20 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, int lane_at, in
 // they went to scratch memory, and their loads waited for those of the weights.
 typedef __attribute__((address_space(4))) W4WideArgs Args;
 
-template <int RT, int GS> struct WideLds {
+// Stages in LDS: one at work, the others on their way. Small tiles have little to do in a
+// stage and wait for memory with one on its way (64 rows of 4096 x 4096, weights from memory:
+// 31.3 us with one, 26.6 with three); large ones have no registers for more weights.
+template <int RT, int CT> constexpr int kDepth = RT <= 2 ? (RT * CT == 1 ? 4 : 3) : 2;
+template <int RT, int GS, int D> struct WideLds {
     static constexpr int kX = 32 * RT * 256, kSums = GS * 32 * RT * 16, kStage = kX + kSums;
     static constexpr int kOut = 32 * (64 * 4 + 16);      // a wave's results on their way out
-    static constexpr int kBytes = 2 * kStage > 4 * kOut ? 2 * kStage : 4 * kOut;
+    static constexpr int kBytes = D * kStage > 4 * kOut ? D * kStage : 4 * kOut;
 };
+// Every wave's loads but the last N are done, and so are all waves' reads before.
+template <int N>
+__device__ __forceinline__ void loads_and_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
 // One wave's part of a tile of 32 RT rows: 32 CT columns. The rows of a stage (128 inputs) go
 // from memory to LDS, units of 16 bytes in an order that has a row's sixteen and sixteen
@@ -128,10 +140,10 @@ template <int RT, int GS> struct WideLds {
 // Beside them a second set, to be added to once a group, has no room in the registers of
 // a tile of this size. A scale that is 0, or below 2^-48 of the present one (whose sums would
 // leave fp32's range), does not become the unit: its codes count as zeros.
-template <typename E, int GS, int RT, int CT>
+template <typename E, int GS, int RT, int CT, int D>
 __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, int row0, int rows, int n0) {
     typedef typename Op<E>::V V;
-    typedef WideLds<RT, GS> L;
+    typedef WideLds<RT, GS, D> L;
     constexpr int kSteps = 8 / GS;
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -140,9 +152,14 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
     const int32_t* const row_token = a.row_token;
     const int64_t rows_x = a.rows_x;
     const uint4* const all_sums = a.sums;
-    const int T = a.T, y_dtype = a.y_dtype;
-    const float* const bias = a.bias;
-    void* const y = a.y;
+    // a part of K: its sums go to its own fp32 rows, and become outputs with the others'
+    const bool parted = a.partial != nullptr;
+    const int T = a.T, y_dtype = parted ? MQ_F32 : a.y_dtype;
+    const float* const bias = parted ? nullptr : a.bias;
+    void* const y = parted ? a.partial + static_cast<int64_t>(blockIdx.y) * a.M * a.N : a.y;
+    // (there are no more parts than stages: each has one at least)
+    const int first_stage = static_cast<int>(static_cast<int64_t>(stages) * blockIdx.y / gridDim.y);
+    const int last = static_cast<int>(static_cast<int64_t>(stages) * (blockIdx.y + 1) / gridDim.y) - 1;
     // x's row of a row of the block; those past its end read the last one's
     auto row_at = [&](int r) __attribute__((always_inline)) -> int {
         const int p = min(r, rows - 1);
@@ -159,17 +176,20 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
         const int r = 4 * (2 * RT * wave + i) + (lane >> 4);
         xat[i] = static_cast<uint32_t>(row_at(r)) * static_cast<uint32_t>(a.ldx) * 2 + 16 * ((lane & 15) ^ (r & 15));
     }
-    constexpr int kSumsPer = (GS * 32 * RT + kThreads - 1) / kThreads;
+    // and the wave's fourth of the sums' units
+    constexpr int kUnits = 8 * GS * RT, kSumsPer = (kUnits + 63) / 64;
     uint32_t sat[kSumsPer];
 #pragma unroll
     for (int i = 0; i < kSumsPer; ++i) {
-        const int u = min(i * kThreads + static_cast<int>(threadIdx.x), GS * 32 * RT - 1);
+        const int u = wave * kUnits + min(i * 64 + lane, kUnits - 1);
         sat[i] = (static_cast<uint32_t>(u / (32 * RT)) * static_cast<uint32_t>(rows_x) + row_at(u % (32 * RT))) * 16;
     }
     const uint16_t* const x0 = a.x + first_row * a.ldx;
     const int64_t x_bytes = ((by_token ? T : rows) - 1) * a.ldx * 2 + 256;         // behind a stage's first input
-    auto load_x = [&](int stage) __attribute__((always_inline)) {
-        uint8_t* const to = lds + (stage & 1) * L::kStage;
+    constexpr int kLoads = 2 * RT + kSumsPer + 4 * CT;   // of a stage, in every wave
+    static_assert(D == 2 || kUnits <= 64);
+    auto load_x = [&](int stage, int buf) __attribute__((always_inline)) {
+        uint8_t* const to = lds + buf * L::kStage;
         const __amdgpu_buffer_rsrc_t xr = buffer(x0 + static_cast<int64_t>(stage) * 128, x_bytes);
         const __amdgpu_buffer_rsrc_t sr = buffer(all_sums + static_cast<int64_t>(stage) * GS * rows_x + first_row,
                                                  (GS * rows_x - first_row) * 16);
@@ -177,7 +197,7 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
         for (int i = 0; i < 2 * RT; ++i) to_lds(xr, xat[i], 0, to + (2 * RT * wave + i) * 1024);
 #pragma unroll
         for (int i = 0; i < kSumsPer; ++i)
-            if (i * kThreads + static_cast<int>(threadIdx.x) < GS * 32 * RT) to_lds(sr, sat[i], 0, to + L::kX + (i * kThreads + wave * 64) * 16);
+            if (i * 64 + lane < kUnits) to_lds(sr, sat[i], 0, to + L::kX + (wave * kUnits + i * 64) * 16);
     };
     // weights: a wave with no column of its own (past N) reads the last tile's and writes nothing
     const int tile0 = min(n0 / 16, n_tiles - 1), have = min(n_tiles - tile0, 2 * CT);
@@ -189,22 +209,24 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
     const int wat = (lane >> 4 & 1) * G * 1024 + (half * 16 + (lane & 15)) * 16;
     const int scat = (lane >> 4 & 1) * scale_bytes + (lane & 15) * 8 * GS;
     // words w of [j][0] are steps 2w, of [j][1] steps 2w + 1
-    mx_i4 W[CT][2];
     typedef typename W4Scales<GS>::T Scales;
-    Scales S[CT], Z[CT];
+    struct Weights {
+        mx_i4 c[CT][2];
+        Scales s[CT], z[CT];
+    } W[D - 1];
     auto scales_at = [&](__amdgpu_buffer_rsrc_t r, int at) __attribute__((always_inline)) -> Scales {
         if constexpr (GS == 1) return __builtin_amdgcn_raw_buffer_load_b16(r, scat, at, 0);
         else if constexpr (GS == 2) return __builtin_amdgcn_raw_buffer_load_b32(r, scat, at, 0);
         else return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(r, scat, at, 0));
     };
-    auto load_w = [&](int stage) __attribute__((always_inline)) {
+    auto load_w = [&](int stage, Weights& to) __attribute__((always_inline)) {
         const int h = planes == 1 ? stage : stage / 3, at = ((h >> 2) * 64 + (h & 3)) * GS * 2;
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
-            W[j][0] = load16(wr, wat, 2 * j * G * 1024 + h * 1024);
-            W[j][1] = load16(wr, wat, 2 * j * G * 1024 + h * 1024 + 512);
-            S[j] = scales_at(scr, 2 * j * scale_bytes + at);
-            Z[j] = scales_at(zr, 2 * j * scale_bytes + at);
+            to.c[j][0] = load16(wr, wat, 2 * j * G * 1024 + h * 1024);
+            to.c[j][1] = load16(wr, wat, 2 * j * G * 1024 + h * 1024 + 512);
+            to.s[j] = scales_at(scr, 2 * j * scale_bytes + at);
+            to.z[j] = scales_at(zr, 2 * j * scale_bytes + at);
         }
     };
     mx_f16 acc[RT][CT] = {};
@@ -214,16 +236,16 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
     float unit[CT] = {}, by[CT], next[CT];
     w4_b8 zb[CT];
     uint32_t mask[CT];
-    auto begin = [&](const Scales (&sw)[CT], const Scales (&zw)[CT], int g) __attribute__((always_inline)) {
+    auto begin = [&](const Weights& w, int g) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
-            const float s = w4_float(static_cast<uint32_t>(sw[j] >> 16 * g) & 0xffff, bf);
+            const float s = w4_float(static_cast<uint32_t>(w.s[j] >> 16 * g) & 0xffff, bf);
             const bool keep = s == 0.0f || fabsf(s) < fabsf(unit[j]) * 0x1p-48f;
             next[j] = keep ? unit[j] : s;
             const float to = keep ? 1.0f : s, from = keep ? 1.0f : unit[j], inv = __builtin_amdgcn_rcpf(to), q = from * inv;
             by[j] = __builtin_fmaf(__builtin_fmaf(-q, to, from), inv, q);
             mask[j] = keep ? 0 : 0x0f0f0f0fu;
-            const float given = -w4_float(static_cast<uint32_t>(zw[j] >> 16 * g) & 0xffff, bf), z = has_zeros ? given : -8.0f;
+            const float given = -w4_float(static_cast<uint32_t>(w.z[j] >> 16 * g) & 0xffff, bf), z = has_zeros ? given : -8.0f;
             const bool none = keep || half;
             const uint32_t hi = none ? 0 : __float_as_uint(z) >> 16;
             const uint32_t lo = none ? 0 : __float_as_uint(z - __uint_as_float(__float_as_uint(z) & 0xffff0000u)) >> 16;
@@ -232,34 +254,31 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
     };
     V x_of[2][RT], b[2][CT];
     // a row tile's share of the conversions of a step
-    auto convert = [&](const mx_i4 (&w)[CT][2], int step, int i) __attribute__((always_inline)) {
+    auto convert = [&](const Weights& w, int step, int i) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < CT; ++j)
-            if (j * RT / CT == i) b[step & 1][j] = w4_codes<E>(w[j][step & 1][step >> 1], mask[j]);
+            if (j * RT / CT == i) b[step & 1][j] = w4_codes<E>(w.c[j][step & 1][step >> 1], mask[j]);
     };
-    load_x(0);
-    load_w(0);
-    begin(S, Z, 0);
 #pragma unroll
-    for (int i = 0; i < RT; ++i) convert(W, 0, i);
+    for (int d = 0; d < D - 1; ++d) {
+        load_x(min(first_stage + d, last), d);
+        load_w(min(first_stage + d, last), W[d]);
+    }
+    begin(W[0], 0);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) convert(W[0], 0, i);
     const int swap = (half ^ (lane & 15)) * 16;
-    for (int stage = 0; stage < stages; ++stage) {
-        __syncthreads();                                 // stage's rows are there, the other buffer's reads are done
-        mx_i4 w[CT][2];
-        Scales sw[CT], zw[CT];
-#pragma unroll
-        for (int j = 0; j < CT; ++j) {
-            w[j][0] = W[j][0];
-            w[j][1] = W[j][1];
-            sw[j] = S[j];
-            zw[j] = Z[j];
-        }
-        if (stage + 1 < stages) {
-            load_x(stage + 1);
-            load_w(stage + 1);
-        }
-        const uint8_t* const x = lds + (stage & 1) * L::kStage + (lane & 31) * 256;
-        const uint8_t* const sums = lds + (stage & 1) * L::kStage + L::kX + (lane & 31) * 16;
+    // Stage `stage` (whose weights are in `now`, the next one's in `after`). Loads past the last
+    // stage are of that again, and not used: a wave's loads are counted.
+    int buf = 0;
+    auto run = [&](int stage, Weights& now, Weights& after) __attribute__((always_inline)) {
+        loads_and_barrier<(D - 2) * kLoads>();           // stage's rows are there, reads of the buffer to be filled are done
+        const Weights w = now;
+        load_x(min(stage + D - 1, last), buf == 0 ? D - 1 : buf - 1);
+        load_w(min(stage + D - 1, last), now);
+        const uint8_t* const x = lds + buf * L::kStage + (lane & 31) * 256;
+        const uint8_t* const sums = lds + buf * L::kStage + L::kX + (lane & 31) * 16;
+        buf = buf == D - 1 ? 0 : buf + 1;
         w4_b8 sum[RT];
         auto read = [&](int step, int i) __attribute__((always_inline)) {
             x_of[step & 1][i] = *reinterpret_cast<const V*>(x + 32 * i * 256 + (swap ^ step * 32));
@@ -297,29 +316,37 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
                         read(step + 1, i);
                         convert(w, step + 1, i);
                     } else if (g + 1 < GS) {
-                        if (i == 0) begin(sw, zw, g + 1);
+                        if (i == 0) begin(w, g + 1);
                         read_sum(g + 1, i);
                         read(step + 1, i);
                         convert(w, step + 1, i);
                     } else {                             // (past the last stage: of its own again, not used)
                         if (i == 0) {
 #pragma unroll
-                            for (int j = 0; j < CT; ++j) asm volatile("" : "+v"(S[j]), "+v"(Z[j]));    // no use of these loads sooner
-                            begin(S, Z, 0);
+                            for (int j = 0; j < CT; ++j) asm volatile("" : "+v"(after.s[j]), "+v"(after.z[j]));    // no use of these loads sooner
+                            begin(after, 0);
                         }
-                        convert(W, 0, i);
+                        convert(after, 0, i);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
+    };
+    int stage = first_stage;
+    for (; stage + D - 2 <= last; stage += D - 1) {
+#pragma unroll
+        for (int d = 0; d < D - 1; ++d) run(stage + d, W[d], W[d + 1 == D - 1 ? 0 : d + 1]);
     }
+#pragma unroll
+    for (int d = 0; d < D - 2; ++d)
+        if (stage + d <= last) run(stage + d, W[d], W[d + 1]);
 
     // The results leave through LDS, piece by piece: a lane holds one column of rows
     // 8 (r / 4) + 4 (l / 32) + r % 4; read back, a lane holds eight columns of a row.
     constexpr int kPitch = 32 * CT * 4 + 16, kLanes = 4 * CT, kRound = 64 / kLanes;
     uint8_t* const tile = lds + wave * L::kOut;
-    __syncthreads();
+    loads_and_barrier<0>();                              // nothing is on its way to LDS any more
     const int n = n0 + (lane % kLanes) * 8;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -342,7 +369,7 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[c] += n + c < N ? bias[n + c] : 0.0f;
             }
-            if (row_token && static_cast<unsigned>(row_token[p]) >= static_cast<unsigned>(T)) {
+            if (row_token && !parted && static_cast<unsigned>(row_token[p]) >= static_cast<unsigned>(T)) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[c] = 0.0f;
             }
@@ -357,22 +384,61 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
 // zeros for rows after the last expert's
 template <int COLS>
 __device__ void zero_rows(const Args& a, int row0, int rows, int n0) {
+    const bool parted = a.partial != nullptr;
+    void* const y = parted ? a.partial + static_cast<int64_t>(blockIdx.y) * a.M * a.N : a.y;
+    const int y_dtype = parted ? MQ_F32 : a.y_dtype;
     const float none[8] = {};
     for (int i = threadIdx.x; i < rows * (COLS / 8); i += kThreads) {
         const int n = n0 + i % (COLS / 8) * 8;
         const int64_t at = static_cast<int64_t>(row0 + i / (COLS / 8)) * a.N + n;
         if (n >= a.N) continue;
-        if (a.y_dtype == MQ_F32) w4_store8(static_cast<float*>(a.y) + at, a.N - n, none);
-        else if (a.y_dtype == MQ_BF16) w4_store8(static_cast<__bf16*>(a.y) + at, a.N - n, none);
-        else w4_store8(static_cast<_Float16*>(a.y) + at, a.N - n, none);
+        if (y_dtype == MQ_F32) w4_store8(static_cast<float*>(y) + at, a.N - n, none);
+        else if (y_dtype == MQ_BF16) w4_store8(static_cast<__bf16*>(y) + at, a.N - n, none);
+        else w4_store8(static_cast<_Float16*>(y) + at, a.N - n, none);
     }
+}
+
+// y = the parts' sums, in the order of the parts, and the bias; zero for rows of no token.
+// Eight outputs a thread.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_w4_add(const float* partial, int parts, int64_t M, int N, const float* bias,
+                                                     const int32_t* row_token, int tokens, T* y) {
+    const int n = (blockIdx.x * kThreads + threadIdx.x) * 8;
+    if (n >= N) return;
+    for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
+        float sum[8] = {};
+        if (!row_token || static_cast<unsigned>(row_token[m]) < static_cast<unsigned>(tokens)) {
+            for (int p0 = 0; p0 < parts; p0 += 4) {
+                MxRaw8<float> v[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) v[p] = mx_load8(partial + ((p0 + p) * M + m) * N + n, p0 + p < parts ? N - n : 0);
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[i] += v[p].v[i];
+            }
+            if (bias) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] += n + i < N ? bias[n + i] : 0.0f;
+            }
+        }
+        w4_store8(y + m * N + n, N - n, sum);
+    }
+}
+
+template <typename T>
+hipError_t add_parts(const W4WideArgs& a, hipStream_t st) {
+    const dim3 grid((a.N + 8 * kThreads - 1) / (8 * kThreads), a.M < 65535 ? a.M : 65535);
+    k_w4_add<T><<<grid, kThreads, 0, st>>>(a.partial, a.parts, a.M, a.N, a.bias, a.row_token, a.T, static_cast<T*>(a.y));
+    return hipGetLastError();
 }
 
 // Four waves side by side, on blocks of at most 32 RT rows.
 template <typename E, int GS, int RT, int CT>
 __global__ __launch_bounds__(kThreads, 2) void k_w4_wide(W4WideArgs) {
     const Args& a = *(const Args*)__builtin_amdgcn_kernarg_segment_ptr();
-    __shared__ __align__(16) uint8_t lds[WideLds<RT, GS>::kBytes];
+    constexpr int D = kDepth<RT, CT>;
+    __shared__ __align__(16) uint8_t lds[WideLds<RT, GS, D>::kBytes];
     constexpr int kCols = 128 * CT, kSlots = 64;           // workgroups that a die holds at a time
     const int ncol = (a.N + kCols - 1) / kCols, blocks = (a.M + 32 * RT - 1) / (32 * RT);
     const int count = a.tiles ? a.tiles[0] : blocks;
@@ -416,28 +482,31 @@ __global__ __launch_bounds__(kThreads, 2) void k_w4_wide(W4WideArgs) {
         return;
     }
     const int n0 = col * kCols + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 32 * CT;
-    if (RT >= 4 && rows > 96) wide_tile<E, GS, RT, CT>(a, lds, e, row0, rows, n0);
-    else if (RT >= 3 && rows > 64) wide_tile<E, GS, RT < 3 ? RT : 3, CT>(a, lds, e, row0, rows, n0);
-    else if (RT >= 2 && rows > 32) wide_tile<E, GS, RT < 2 ? RT : 2, CT>(a, lds, e, row0, rows, n0);
-    else wide_tile<E, GS, 1, CT>(a, lds, e, row0, rows, n0);
+    if (RT >= 4 && rows > 96) wide_tile<E, GS, RT, CT, D>(a, lds, e, row0, rows, n0);
+    else if (RT >= 3 && rows > 64) wide_tile<E, GS, RT < 3 ? RT : 3, CT, D>(a, lds, e, row0, rows, n0);
+    else if (RT >= 2 && rows > 32) wide_tile<E, GS, RT < 2 ? RT : 2, CT, D>(a, lds, e, row0, rows, n0);
+    else wide_tile<E, GS, 1, CT, D>(a, lds, e, row0, rows, n0);
 }
 
 template <typename E, int GS, int RT, int CT>
 hipError_t wide(const W4WideArgs& a, hipStream_t st) {
     const int64_t ncol = (a.N + 128 * CT - 1) / (128 * CT);
-    const int64_t n = a.tiles ? mx_tiles_cap(a.M, a.E) : (a.M + 32 * RT - 1) / (32 * RT);
-    const int64_t rest = 64 * 8 * 4;                       // what the last round's tiles make when they are split, at most
-    const int64_t want = (n * ncol + 7) / 8 * 8 + (a.tiles || n * ncol <= 512 ? 0 : rest);
+    const int64_t n = a.tiles ? w4_blocks_cap(a.M, a.E, RT) : (a.M + 32 * RT - 1) / (32 * RT);
+    // split tiles make up to 64 workgroups on each die
+    const int64_t want = ((n * ncol + 7) / 8 + (a.tiles || n * ncol <= 8 * 64 ? 0 : 64)) * 8;
     if (want >= int64_t(1) << 24) return hipErrorInvalidConfiguration;       // a grid holds 2^32 threads
-    k_w4_wide<E, GS, RT, CT><<<static_cast<unsigned>(want), kThreads, 0, st>>>(a);
+    k_w4_wide<E, GS, RT, CT><<<dim3(static_cast<unsigned>(want), a.parts), kThreads, 0, st>>>(a);
     return hipGetLastError();
 }
 
 template <typename E, int GS>
 hipError_t wide_tiles(const W4WideArgs& a, int rt, int ct, hipStream_t st) {
     if (ct == 1) return rt == 1 ? wide<E, GS, 1, 1>(a, st) : wide<E, GS, 2, 1>(a, st);
-    if (rt <= 2) return rt == 1 ? wide<E, GS, 1, 2>(a, st) : wide<E, GS, 2, 2>(a, st);
-    return rt == 3 ? wide<E, GS, 3, 2>(a, st) : wide<E, GS, 4, 2>(a, st);
+    if (rt == 2) return wide<E, GS, 2, 2>(a, st);
+    if constexpr (GS < 4) {                                // (groups of 32: 128 rows go beyond the registers)
+        if (rt == 4) return wide<E, GS, 4, 2>(a, st);
+    }
+    return wide<E, GS, 3, 2>(a, st);
 }
 
 template <typename E>
@@ -457,7 +526,13 @@ hipError_t launch_w4_rows(const W4RowsArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_w4_wide(const W4WideArgs& a, int rt, int ct, hipStream_t st) {
-    return a.x_dtype == MQ_F16 ? wide_groups<_Float16>(a, rt, ct, st) : wide_groups<__bf16>(a, rt, ct, st);
+    const hipError_t rc = a.x_dtype == MQ_F16 ? wide_groups<_Float16>(a, rt, ct, st) : wide_groups<__bf16>(a, rt, ct, st);
+    if (rc != hipSuccess || !a.partial) return rc;
+    switch (a.y_dtype) {
+        case MQ_F32: return add_parts<float>(a, st);
+        case MQ_BF16: return add_parts<__bf16>(a, st);
+        default: return add_parts<_Float16>(a, st);
+    }
 }
 
 }  // namespace mq
