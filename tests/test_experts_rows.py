@@ -244,6 +244,30 @@ def test_gradients_that_are_not_contiguous_and_partial_wants(mq):
     assert torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("k", [1, 3, 8, 9, 20])
+def test_slots_without_a_row_have_no_gradient(mq, k):
+    """Their dots are 0 whatever the token holds, and a NaN in rows of no token goes nowhere."""
+    import torch
+    g = _gen(4)
+    T, E, D = 40, 6, 75
+    ids, plan = _plan(mq, g, T, E, k)
+    lost = plan.row_of < 0
+    assert lost.any()
+    for D in (72, 75):
+        x, w = torch.randn(T, D, generator=g, device="cuda"), torch.rand(T, k, generator=g, device="cuda")
+        x[::3] = float("nan")
+        x[1::3, 5] = float("inf")
+        wl = w.clone().requires_grad_()
+        given = torch.randn(plan.row_token.numel(), D, generator=g, device="cuda")
+        (dw,) = torch.autograd.grad(mq.experts_gather(x, plan, wl), wl, given)
+        assert (dw[lost] == 0).all() and (dw[::3][~lost[::3]]).isnan().all()
+        wl = w.clone().requires_grad_()
+        rows = torch.randn(plan.row_token.numel(), D, generator=g, device="cuda")
+        rows[plan.row_token < 0] = float("nan")
+        (dw,) = torch.autograd.grad(mq.experts_combine(rows, plan, wl), wl, x)
+        assert (dw[lost] == 0).all() and (dw[::3][~lost[::3]]).isnan().all()
+
+
 def test_changed_inputs_and_second_derivatives_are_refused(mq):
     import torch
     g = _gen(2)
