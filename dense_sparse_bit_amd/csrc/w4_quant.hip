@@ -16,96 +16,98 @@ __device__ __forceinline__ int lds_word(int row, int lane) {
 }
 __device__ __forceinline__ int lds_unit(int t) { return (t >> 6) * kTile + (t >> 4 & 3) * kQuarter + (t & 15) * 4; }
 
-// Codes of eight values that share the scale s > 0 (finite), from 0 to 15 with z added.
-// Quotients go by a reciprocal, which is off by less than 1e-5 of a step where the code is
-// not clamped anyway; where one comes within 1e-4 of a border, the remainder v - q s (exact: a
-// multiple of the lesser of v's and s's last places, and less than s) tells on which side it is.
-__device__ __forceinline__ void round8(float (&v)[8], float s, float z, uint32_t (&c)[8]) {
-    const float up = s < 0x1p-64f ? 0x1p64f : 1.0f;   // away from subnormal reciprocals' loss
-    s *= up;
-    const float inv = 1.0f / s;
-    float q[8], far = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] *= up;
-        const float t = v[i] * inv;
-        q[i] = __builtin_rintf(t);
-        far = fmaxf(far, fabsf(t - q[i]));
-    }
-    if (far > 0.4999f) {
-        const float half = 0.5f * s;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float d = __builtin_fmaf(-q[i], s, v[i]), e = fabsf(d) - half;
-            const bool odd = 0.5f * q[i] != __builtin_rintf(0.5f * q[i]);
-            if (e > 0 || (e == 0 && odd)) q[i] += copysignf(1.0f, d);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = static_cast<uint32_t>(__builtin_amdgcn_fmed3f(q[i] + z, 0.0f, 15.0f));
+// v / D, rounded once: a product by the reciprocal and its exact remainder's (Markstein),
+// which needs that no part of it is subnormal.
+template <int D>
+__device__ __forceinline__ float over(float v) {
+    constexpr float kInv = 1.0f / D;
+    float q = v * kInv;
+    q = __builtin_fmaf(__builtin_fmaf(-static_cast<float>(D), q, v), kInv, q);
+    if (v < 0x1p-90f || v > 0x1p127f) q = v / D;           // (infinities among them)
+    return q;
 }
 
-// rne(v / s), s > 0, between 0 and 15
-__device__ __forceinline__ float round1(float v, float s) {
-    const float up = s < 0x1p-64f ? 0x1p64f : 1.0f;
-    s *= up;
-    v *= up;
-    float q = __builtin_rintf(v / s);
-    const float d = __builtin_fmaf(-q, s, v), e = fabsf(d) - 0.5f * s;
-    const bool odd = 0.5f * q != __builtin_rintf(0.5f * q);
-    if (e > 0 || (e == 0 && odd)) q += copysignf(1.0f, d);
-    return __builtin_amdgcn_fmed3f(q, 0.0f, 15.0f);
+// v / s rounded once, likewise: inv is 1 / s rounded once, and s has no more than 11 bits, so
+// that the remainder is exact however the first product was rounded. To round that again to a
+// whole number changes nothing: v and s times half a whole number differ by a last place of v
+// at least, or not at all.
+__device__ __forceinline__ float quotient(float v, float s, float inv) {
+    const float q = v * inv;
+    return __builtin_fmaf(__builtin_fmaf(-q, s, v), inv, q);
 }
 
 // The word of codes, the scale and the zero point of eight values of a group whose others
 // are in neighbouring lanes.
-template <bool Z>
-__device__ __forceinline__ uint32_t quant8(float (&v)[8], int group, bool bf, uint32_t& scale, uint32_t& zero) {
-    int peak = 0;
-    float lo = 0, hi = 0;
+template <bool Z, typename T>
+__device__ __forceinline__ uint32_t quant8(const MxRaw8<T>& raw, int group, bool bf, uint32_t& scale, uint32_t& zero) {
+    constexpr float kWhole = 12582912.0f;                // 1.5 * 2^23: the last place is 1
+    float v[8];
+    w4_values(raw, v);
+    const int peak = w4_over_group(static_cast<int>(raw.peak()), group, [](int a, int b) { return max(a, b); });
+    float s, lo = 0;
+    if constexpr (Z) {
+        float hi = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        peak = max(peak, static_cast<int>(__float_as_uint(v[i]) & 0x7fffffffu));
-        if constexpr (Z) {
+        for (int i = 0; i < 8; ++i) {
             lo = fminf(lo, v[i]);
             hi = fmaxf(hi, v[i]);
         }
-    }
-    peak = w4_over_group(peak, group, [](int a, int b) { return max(a, b); });
-    float s = __int_as_float(peak) / 7.0f;
-    if constexpr (Z) {
         const auto least = [](int a, int b) { return __float_as_int(fminf(__int_as_float(a), __int_as_float(b))); };
         const auto most = [](int a, int b) { return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b))); };
         lo = __int_as_float(w4_over_group(__float_as_int(lo), group, least));
         hi = __int_as_float(w4_over_group(__float_as_int(hi), group, most));
-        s = (hi - lo) / 15.0f;
-    }
-    s = fminf(s, bf ? __uint_as_float(0x7f7f0000u) : 65504.0f);
-    scale = w4_bits(s, bf);
-    s = w4_float(scale, bf);
-    float z = Z ? 0.0f : 8.0f;
-    const bool bad = peak >= 0x7f800000;
-    if (bad) scale = bf ? 0x7fc0 : 0x7e00;
-    uint32_t c[8];
-    if (s > 0 && !bad) {
-        if constexpr (Z) z = round1(-lo, s);
-        round8(v, s, z, c);
+        s = over<15>(hi - lo);
     } else {
+        s = over<7>(__int_as_float(peak));
+    }
+    scale = w4_bits(fminf(s, bf ? __uint_as_float(0x7f7f0000u) : 65504.0f), bf);
+    s = w4_float(scale, bf);
+    const bool bad = peak >= 0x7f800000, live = s > 0 && !bad;
+    if (bad) scale = bf ? 0x7fc0 : 0x7e00;
+    if (s < 0x1p-64f || s > 0x1p64f) {                   // reciprocals and remainders to normal numbers
+        const float to = s < 1.0f ? 0x1p64f : 0x1p-64f;
+        s *= to;
+        lo *= to;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = static_cast<uint32_t>(z);
+        for (int i = 0; i < 8; ++i) v[i] *= to;
+    }
+    float inv = __builtin_amdgcn_rcpf(s);
+    inv = __builtin_fmaf(__builtin_fmaf(-s, inv, 1.0f), inv, inv);
+    // Quotients are rounded, ties to even, by adding a number whose last place is 1 and even;
+    // an odd zero point's last bit is added to the codes of both halves of a byte at once.
+    float z = 8.0f, odd = 0.0f;
+    if constexpr (Z) {
+        z = __builtin_amdgcn_fmed3f(__builtin_rintf(quotient(-lo, s, inv)), 0.0f, 15.0f);
+        if (!live) z = 0.0f;
+        odd = z - 2.0f * floorf(0.5f * z);
     }
     zero = w4_bits(z, bf);
-    return w4_word(c);
+    const float base = kWhole + (z - odd);
+    uint32_t c[8], p[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        c[i] = __float_as_uint(__builtin_amdgcn_fmed3f(quotient(v[i], s, inv) + base, kWhole - odd, kWhole + 15.0f - odd));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        p[i] = (c[i + 4] << 4) + c[i];                   // the low byte: codes i and i + 4
+        if constexpr (Z) p[i] += odd > 0 ? 17 : 0;
+    }
+    const uint32_t ab = __builtin_amdgcn_perm(p[1], p[0], 0x0c0c0400u), cd = __builtin_amdgcn_perm(p[3], p[2], 0x0c0c0400u);
+    return live ? ab | cd << 16 : (Z ? 0 : 0x88888888u);
 }
 
 // One workgroup: 16 rows x 512 inputs (four code tiles). Wave w reads rows 4w .. 4w + 3, 1 KB
 // of a 16-bit type at a time; lane l holds inputs 8l .. 8l + 7. Codes go through LDS, because a
-// tile keeps the rows of a few inputs together: they leave as 4 KB runs. Bound by the
-// read of x.
+// tile keeps the rows of a few inputs together: they leave as 4 KB runs, scales as runs of 128 B
+// or more. Bound by memory, closely followed by the arithmetic: with a division a value, and
+// scales stored two bytes at a time, it took 92 us for 17408 x 5120 of bf16, with quotients by
+// the reciprocal 44 us (5.1 TB/s read and written), 59 us with zero points (two more
+// reductions).
 template <typename T, bool Z>
 __global__ __launch_bounds__(kThreads) void k_w4_quant(W4QuantArgs a) {
     __shared__ __align__(16) uint32_t lds[4 * kTile];
-    const int G = (a.K + 127) / 128, Q = (a.K + 511) / 512, per = 512 / a.group;
+    __shared__ __align__(16) uint16_t lds_s[16 * 16], lds_z[Z ? 16 * 16 : 1];
+    const int G = (a.K + 127) / 128, Q = (a.K + 511) / 512, bits = __builtin_ctz(a.group), per = 512 >> bits;
     const int64_t RT = (a.R + 15) / 16, b = blockIdx.z;
     const int q = blockIdx.x, t = threadIdx.x, wave = t >> 6, lane = t & 63;
     const int k0 = q * 512 + 8 * lane;
@@ -121,26 +123,28 @@ __global__ __launch_bounds__(kThreads) void k_w4_quant(W4QuantArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 4 * wave + i;
-            float v[8];
-            w4_values(raw[i], v);
             uint32_t scale, zero;
-            uint32_t word = quant8<Z>(v, a.group, bf, scale, zero);
+            uint32_t word = quant8<Z>(raw[i], a.group, bf, scale, zero);
             // what is behind the matrix's end holds zeros
-            if (rt * 16 + row >= a.R || k0 / a.group * a.group >= a.K) word = scale = zero = 0;
+            if (rt * 16 + row >= a.R || k0 >> bits << bits >= a.K) word = scale = zero = 0;
             else if (k0 + 8 > a.K) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (k0 + j >= a.K) word &= ~(15u << (j < 4 ? 8 * j : 8 * (j - 4) + 4));
             }
             lds[lds_word(row, lane)] = word;
-            const int unit = a.group / 8;
-            if ((lane & (unit - 1)) == 0) {
-                const int64_t at = (((b * RT + rt) * Q + q) * 16 + row) * per + lane / unit;
-                a.scales[at] = static_cast<uint16_t>(scale);
-                if constexpr (Z) a.zeros[at] = static_cast<uint16_t>(zero);
+            if ((8 * lane & (a.group - 1)) == 0) {
+                const int at = row * per + (8 * lane >> bits);
+                lds_s[at] = static_cast<uint16_t>(scale);
+                if constexpr (Z) lds_z[at] = static_cast<uint16_t>(zero);
             }
         }
         __syncthreads();
+        if (t < 8 * per) {
+            const int64_t at = ((b * RT + rt) * Q + q) * 16 * per + 2 * t;
+            *reinterpret_cast<uint32_t*>(a.scales + at) = *reinterpret_cast<const uint32_t*>(&lds_s[2 * t]);
+            if constexpr (Z) *reinterpret_cast<uint32_t*>(a.zeros + at) = *reinterpret_cast<const uint32_t*>(&lds_z[2 * t]);
+        }
         if (q * 4 + wave < G)
             *reinterpret_cast<uint4*>(a.codes + ((b * RT + rt) * G + q * 4) * 1024 + t * 16) =
                 *reinterpret_cast<const uint4*>(&lds[lds_unit(t)]);
@@ -148,10 +152,11 @@ __global__ __launch_bounds__(kThreads) void k_w4_quant(W4QuantArgs a) {
     }
 }
 
-// Given codes, scales and zero points into the same places.
+// Given codes, scales and zero points into the same places. Bound by memory.
 __global__ __launch_bounds__(kThreads) void k_w4_pack(W4QuantArgs a) {
     __shared__ __align__(16) uint32_t lds[4 * kTile];
-    const int G = (a.K + 127) / 128, Q = (a.K + 511) / 512, per = 512 / a.group, n = (a.K + a.group - 1) / a.group;
+    const int G = (a.K + 127) / 128, Q = (a.K + 511) / 512, bits = __builtin_ctz(a.group), per = 512 >> bits;
+    const int n = (a.K + a.group - 1) >> bits;
     const int64_t RT = (a.R + 15) / 16, b = blockIdx.z;
     const int q = blockIdx.x, t = threadIdx.x, wave = t >> 6, lane = t & 63;
     const int k0 = q * 512 + 8 * lane;
@@ -176,11 +181,10 @@ __global__ __launch_bounds__(kThreads) void k_w4_pack(W4QuantArgs a) {
                 }
             }
             lds[lds_word(row, lane)] = w4_word(c);
-            const int unit = a.group / 8;
-            if ((lane & (unit - 1)) == 0) {
-                const int g = k0 / a.group;
+            if ((8 * lane & (a.group - 1)) == 0) {
+                const int g = k0 >> bits;
                 const bool there = r < a.R && g < n;
-                const int64_t from = (b * a.R + r) * n + g, at = (((b * RT + rt) * Q + q) * 16 + row) * per + lane / unit;
+                const int64_t from = (b * a.R + r) * n + g, at = (((b * RT + rt) * Q + q) * 16 + row) * per + (8 * lane >> bits);
                 a.scales[at] = there ? a.s[from] : 0;
                 if (a.z) a.zeros[at] = there ? a.z[from] : 0;
             }
@@ -194,11 +198,11 @@ __global__ __launch_bounds__(kThreads) void k_w4_pack(W4QuantArgs a) {
 }
 
 // The way back, tile by tile: codes come in as one run, change places in LDS and leave as
-// rows. Bound by the writes.
+// rows. Bound by the writes: 17408 x 5120 to bf16 in 38 us (4.7 TB/s written).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_w4_dequant(W4QuantArgs a, T* y) {
     __shared__ __align__(16) uint32_t lds[4 * kTile];
-    const int G = (a.K + 127) / 128, Q = (a.K + 511) / 512, per = 512 / a.group;
+    const int G = (a.K + 127) / 128, Q = (a.K + 511) / 512, bits = __builtin_ctz(a.group), per = 512 >> bits;
     const int64_t RT = (a.R + 15) / 16, b = blockIdx.z;
     const int q = blockIdx.x, t = threadIdx.x, wave = t >> 6, lane = t & 63;
     const int k0 = q * 512 + 8 * lane, have = a.K - k0;
@@ -210,7 +214,7 @@ __global__ __launch_bounds__(kThreads) void k_w4_dequant(W4QuantArgs a, T* y) {
         float s[4], z[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t at = (((b * RT + rt) * Q + q) * 16 + 4 * wave + i) * per + lane / (a.group / 8);
+            const int64_t at = (((b * RT + rt) * Q + q) * 16 + 4 * wave + i) * per + (8 * lane >> bits);
             s[i] = w4_float(a.scales[at], bf);
             z[i] = a.zeros ? w4_float(a.zeros[at], bf) : 8.0f;
         }
