@@ -138,8 +138,9 @@ __device__ __forceinline__ void loads_and_barrier() {
 // The sums stand in units of the column's present scale: where a group begins, they are
 // multiplied by the last scale over the new one, and go on through the matrix instructions.
 // Beside them a second set, to be added to once a group, has no room in the registers of
-// a tile of this size. A scale that is 0, or below 2^-48 of the present one (whose sums would
-// leave fp32's range), does not become the unit: its codes count as zeros.
+// a tile of this size. A scale below 2^-64 of the largest before it (in whose units the sums
+// would leave fp32's range), or below 2^-126 (its reciprocal would), does not become the unit:
+// its codes count as zeros.
 template <typename E, int GS, int RT, int CT, int D>
 __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, int row0, int rows, int n0) {
     typedef typename Op<E>::V V;
@@ -230,18 +231,21 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
         }
     };
     mx_f16 acc[RT][CT] = {};
-    // A group's: the factor from the last unit to its own, its unit, -z as the matrix
+    // A group's: the factor from the last unit to its own, its unit, the least scale that becomes one, -z as the matrix
     // instructions take it (the sums' pieces meet the high part, then the low part), its codes'
     // mask.
-    float unit[CT] = {}, by[CT], next[CT];
+    float unit[CT] = {}, least[CT], by[CT], next[CT];
+#pragma unroll
+    for (int j = 0; j < CT; ++j) least[j] = 0x1p-126f;
     w4_b8 zb[CT];
     uint32_t mask[CT];
     auto begin = [&](const Weights& w, int g) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
             const float s = w4_float(static_cast<uint32_t>(w.s[j] >> 16 * g) & 0xffff, bf);
-            const bool keep = s == 0.0f || fabsf(s) < fabsf(unit[j]) * 0x1p-48f;
+            const bool keep = fabsf(s) < least[j];
             next[j] = keep ? unit[j] : s;
+            least[j] = fmaxf(least[j], fabsf(s) * 0x1p-64f);
             const float to = keep ? 1.0f : s, from = keep ? 1.0f : unit[j], inv = __builtin_amdgcn_rcpf(to), q = from * inv;
             by[j] = __builtin_fmaf(__builtin_fmaf(-q, to, from), inv, q);
             mask[j] = keep ? 0 : 0x0f0f0f0fu;

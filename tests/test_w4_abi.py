@@ -97,6 +97,16 @@ def test_a_missing_workspace_is_refused(lib):
         assert lib.mq_w4_experts_workspace_bytes(*size) == 0
 
 
+def test_ways_of_products(lib):
+    import tests.w4_reference as ref
+    for x_type, group, M, N, K, way in ref.WAYS:
+        assert lib.mq_w4_linear_way(M, N, K, {"fp32": 0, "bf16": 1, "fp16": 2}[x_type], group) == way
+    assert {way for *_, way in ref.WAYS} == {0, 1, 2, 4, 5} | {8 * p + t for p in (1, 2, 4, 8) for t in range(5)}
+    for size, status in (((-1, 64, 512, 1, 128), -1), ((4, 0, 512, 1, 128), -1), ((4, 64, 512, 1, 48), -1), ((4, 64, 512, 7, 128), -1),
+                         ((4, 64, 1 << 21, 1, 128), -2)):
+        assert lib.mq_w4_linear_way(*size) == status
+
+
 def test_stated_sizes(lib):
     for R, K, group in ((1, 1, 32), (16, 128, 128), (17, 129, 64), (100, 5000, 32)):
         RT, G, Q = -(-R // 16), -(-K // 128), -(-K // 512)
