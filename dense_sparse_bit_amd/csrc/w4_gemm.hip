@@ -76,10 +76,10 @@ __device__ __forceinline__ void store1(void* y, int dtype, int64_t at, float v) 
 
 // GS consecutive scales or zero points
 template <int GS>
-__device__ __forceinline__ uint64_t load_scales(const uint16_t* p) {
-    if constexpr (GS == 1) return *p;
-    else if constexpr (GS == 2) return *reinterpret_cast<const uint32_t*>(p);
-    else return *reinterpret_cast<const uint64_t*>(p);
+__device__ __forceinline__ typename W4Scales<GS>::T load_scales(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
+    if constexpr (GS == 1) return __builtin_amdgcn_raw_buffer_load_b16(r, lane_at, at, 0);
+    else if constexpr (GS == 2) return __builtin_amdgcn_raw_buffer_load_b32(r, lane_at, at, 0);
+    else return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(r, lane_at, at, 0));
 }
 
 // The scales or zero points of a quad of code tiles (4 GS of them).
@@ -351,10 +351,17 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_w4_one(W4GemmArgs a) {
 
 // One workgroup: 16 MT rows x NT column tiles of 16, its waves each a run of K, tile by tile;
 // rows reach the matrix instructions through LDS (256 bytes of four rows a load; lanes that
-// read their own operands, 64 bytes of 16 rows, take twice the time).
+// read their own operands, 64 bytes of 16 rows, take twice the time). Bound by instructions:
+// 32 rows, 14336 x 4096 take 17.0 us with the weights from memory and 15.1 us from caches, where
+// reading them takes 6; in 1.9 us a code tile (two waves a SIMD) each wave has 200 vector instructions (64 conversions of
+// two codes, 64 sums of groups) and 40 matrix instructions.
 template <typename XT, int GS, bool Z, int NT, int MT, int W>
 __global__ __launch_bounds__(64 * W) void k_w4_few(W4GemmArgs a) {
     constexpr int kPitch = kRowPitch<XT>, kUnit = 8 * sizeof(XT);
+    // The next code tile is loaded during this one's products where registers are left for it
+    // (64 tokens' rows of 64 experts, 1024 x 4096: 44 us, 48 without); 32 rows and 64 columns
+    // have none (32 x 14336 x 4096: 18.7 us, 17.4 without).
+    constexpr bool kAhead = NT * MT <= 4;
     // each wave's rows, then the waves' sums
     __shared__ __align__(16) uint8_t lds[W * (16 * MT * kPitch > NT * MT * 1024 ? 16 * MT * kPitch : NT * MT * 1024)];
     const int lane = threadIdx.x & 63;
@@ -387,36 +394,48 @@ __global__ __launch_bounds__(64 * W) void k_w4_few(W4GemmArgs a) {
                 }
                 from[i] = static_cast<const XT*>(a.x) + r * a.stride_x;
             }
-            const uint8_t* w[NT];
-            const uint16_t *ws[NT], *wz[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int64_t tile = static_cast<int64_t>(e) * n_tiles + min(ct + j, n_tiles - 1);
-                w[j] = a.codes + tile * G * 1024 + lane * 16;
-                ws[j] = a.scales + (tile * Q * 16 + (lane & 15)) * 4 * GS;
-                wz[j] = Z ? a.zeros + (tile * Q * 16 + (lane & 15)) * 4 * GS : nullptr;
-            }
+            // (through buffers, whose addresses take no vector registers; past the last column
+            // tile they give zeros)
+            const int have = min(NT, n_tiles - ct), scale_bytes = Q * 16 * 4 * GS * 2;
+            const int64_t tile = static_cast<int64_t>(e) * n_tiles + ct;
+            const __amdgpu_buffer_rsrc_t wr = buffer(a.codes + tile * G * 1024, static_cast<int64_t>(have) * G * 1024);
+            const __amdgpu_buffer_rsrc_t scr = buffer(a.scales + tile * (scale_bytes / 2), static_cast<int64_t>(have) * scale_bytes);
+            const __amdgpu_buffer_rsrc_t zr = Z ? buffer(a.zeros + tile * (scale_bytes / 2), static_cast<int64_t>(have) * scale_bytes) : scr;
             const int h0 = static_cast<int>(static_cast<int64_t>(G) * wave / waves);
             const int h1 = static_cast<int>(static_cast<int64_t>(G) * (wave + 1) / waves);
-            for (int h = h0; h < h1; ++h) {
-                MxRaw8<XT> v[4 * MT];
-                mx_i4 c[NT];
-                uint64_t sc[NT], zc[NT] = {};
+            MxRaw8<XT> v[4 * MT];
+            mx_i4 next[NT];
+            typename W4Scales<GS>::T next_s[NT], next_z[NT] = {};
+            auto load = [&](int h) __attribute__((always_inline)) {
 #pragma unroll
                 for (int i = 0; i < 4 * MT; ++i)
                     if (4 * i < rows) v[i] = load8(from[i], 128 * h + 8 * (lane & 15), a.K, 128 * (h + 1) <= a.K);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    c[j] = *reinterpret_cast<const mx_i4*>(w[j] + static_cast<int64_t>(h) * 1024);
-                    const int at = ((h >> 2) * 16 * 4 + (h & 3)) * GS;
-                    sc[j] = load_scales<GS>(ws[j] + at);
-                    if constexpr (Z) zc[j] = load_scales<GS>(wz[j] + at);
+                    next[j] = load16(wr, lane * 16, (j * G + h) * 1024);
+                    const int at = j * scale_bytes + ((h >> 2) * 16 * 4 + (h & 3)) * GS * 2;
+                    next_s[j] = load_scales<GS>(scr, (lane & 15) * 8 * GS, at);
+                    if constexpr (Z) next_z[j] = load_scales<GS>(zr, (lane & 15) * 8 * GS, at);
                 }
+            };
+            if (kAhead && h0 < h1) load(h0);
+            for (int h = h0; h < h1; ++h) {
+                if (!kAhead) load(h);
                 mx_wave_sync();                            // the last tile's reads come first
 #pragma unroll
                 for (int i = 0; i < 4 * MT; ++i)
                     if (4 * i < rows) put8(mine + (4 * i + (lane >> 4)) * kPitch + (lane & 15) * kUnit, v[i]);
                 mx_wave_sync();
+                mx_i4 c[NT];
+                typename W4Scales<GS>::T sc[NT], zc[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    c[j] = next[j];
+                    sc[j] = next_s[j];
+                    zc[j] = next_z[j];
+                }
+                if (kAhead && h + 1 < h1) load(h + 1);
+                if (kAhead) __builtin_amdgcn_sched_barrier(0);
                 tile_products<XT, GS>(c, mine + (lane & 15) * kPitch + (lane >> 4) * kUnit, kPitch,
                                       [&](int g, int j) __attribute__((always_inline)) { return w4_float(static_cast<uint32_t>(sc[j] >> 16 * g) & 0xffff, bf); },
                                       [&](int g, int j) __attribute__((always_inline)) {
