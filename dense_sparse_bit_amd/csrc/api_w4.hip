@@ -128,17 +128,22 @@ Way tiles_way(int rt, int ct, int64_t parts, int64_t stages) {
     return {mq::kW4One, rt, ct, static_cast<int>(parts < 1 ? 1 : (parts < stages ? parts : stages))};
 }
 
-// The costs below are fits, in us, of times measured on weights that no cache holds: ten
-// sizes from 1024 x 1024 to 17408 x 5120, 2 to 2048 rows, every way. Over the 150 sizes of
-// more than four rows the choice is within 22% of the fastest way, 2% on average.
+// The costs below are fits, in us, of times measured on weights that no cache holds: 23 sizes
+// from 512 x 512 to 17408 x 5120, 5 to 2048 rows, every way. Over 298 of those with up to 256
+// rows the choice is within 23% of the fastest way, 0.9% on average (fp32 rows, 88 sizes: 26% and
+// 1.5%).
 //
 // A kernel of few rows: in rounds of workgroups (`per` rounds for each 256 of eight waves), a start
 // and each wave's code tiles, whose time grows with the groups in them.
-double few_cost(int64_t M, int64_t N, int64_t K, int group, int rows, int cols, double start, double round, double tile,
-                double per, double groups) {
-    const double G = static_cast<double>(mq::w4_tiles(K)), waves = G >= 32 ? 8 : (G >= 8 ? 4 : (G >= 4 ? 2 : 1));
-    const double n = static_cast<double>((N + cols - 1) / cols) * static_cast<double>((M + rows - 1) / rows) / 256;
-    return start + (round + tile * (G / waves) * (1 + groups * (128 / group - 1))) * fmax(1.0, per * n * waves / 8);
+struct FewCost {
+    int rows, cols;
+    double start, round, tile, per, groups;
+};
+double few_cost(const FewCost& c, int64_t M, int64_t N, int64_t K, int group) {
+    const int64_t wgs = ((N + c.cols - 1) / c.cols) * ((M + c.rows - 1) / c.rows);
+    const double waves = static_cast<double>(mq::w4_few_waves(wgs, K, c.rows * c.cols / 256));
+    const double tiles = static_cast<double>(mq::w4_tiles(K)) / waves * (1 + c.groups * (128 / group - 1));
+    return c.start + (c.round + c.tile * tiles) * fmax(1.0, c.per * static_cast<double>(wgs) / 256 * waves / 8);
 }
 
 // Tiles: the sums of the rows' groups, then the stages, each as long as its chain of
@@ -165,10 +170,8 @@ double tile_cost(const TileCost& c, int64_t M, int64_t N, int64_t K, int planes,
 Way dense_way(int64_t M, int64_t N, int64_t K, int x_dtype, int group) {
     const int planes = mq::w4_planes(x_dtype);
     const int64_t stages = mq::w4_tiles(K) * planes;
-    // Four rows, 4096 x 4096: by four 5.8 us, by 16 7.7; 14336 x 4096: 17.8, 12.2. Sixteen rows,
-    // 16 columns a workgroup / 32: 7.3 / 8.2 and 18.0 / 14.0.
+    // Four rows, 4096 x 4096: by four 5.8 us, by 16 7.7; 14336 x 4096: 17.8, 12.2.
     if (M == 1 || (M <= 4 && N <= 8192)) return {mq::kW4One, 0, 0, 1};
-    if (M <= 16) return {N <= 8192 ? mq::kW4Rows16 : mq::kW4Rows16x32, 0, 0, 1};
     Way best = {mq::kW4Rows16, 0, 0, 1};
     double least = 1e300;
     auto take = [&](Way w, double cost) {
@@ -178,11 +181,13 @@ Way dense_way(int64_t M, int64_t N, int64_t K, int x_dtype, int group) {
         }
     };
     if (M <= 256) {
+        const double more = planes == 1 ? 1 : 2;           // fp32 rows: three times the products
+        take({mq::kW4Rows16, 0, 0, 1}, few_cost({16, 16, 2.88, 0.63, more * 0.72, 0.85, 0.20}, M, N, K, group));
+        take({mq::kW4Rows16x32, 0, 0, 1}, few_cost({16, 32, 3.68, 0.24, more * 0.85, 1.12, 0.22}, M, N, K, group));
+        if (M <= 16) return best;
         if (planes == 1) {
-            take({mq::kW4Rows32x32, 0, 0, 1}, few_cost(M, N, K, group, 32, 32, 1.66, 2.53, 1.37, 1.18, 0.22));
-            take({mq::kW4Rows32x64, 0, 0, 1}, few_cost(M, N, K, group, 32, 64, 2.81, 2.47, 1.88, 1.40, 0.24));
-        } else {                                           // fp32 rows: three times the products
-            take({mq::kW4Rows16, 0, 0, 1}, few_cost(M, N, K, group, 16, 16, 0, 2.51, 2 * 0.98, 0.73, 0.12));
+            take({mq::kW4Rows32x32, 0, 0, 1}, few_cost({32, 32, 2.18, 2.50, 1.34, 1.21, 0.23}, M, N, K, group));
+            take({mq::kW4Rows32x64, 0, 0, 1}, few_cost({32, 64, 3.06, 2.77, 1.71, 1.42, 0.33}, M, N, K, group));
         }
     }
     for (const TileCost& c : kTiles) {

@@ -353,8 +353,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_w4_one(W4GemmArgs a) {
 // rows reach the matrix instructions through LDS (256 bytes of four rows a load; lanes that
 // read their own operands, 64 bytes of 16 rows, take twice the time). Bound by instructions:
 // 32 rows, 14336 x 4096 take 17.0 us with the weights from memory and 15.1 us from caches, where
-// reading them takes 6; in 1.9 us a code tile (two waves a SIMD) each wave has 200 vector instructions (64 conversions of
-// two codes, 64 sums of groups) and 40 matrix instructions.
+// reading them takes 6; in the 1.9 us of a code tile (two waves a SIMD) each wave has 200 vector
+// instructions (64 conversions of two codes, 64 sums of groups) and 40 matrix instructions.
 template <typename XT, int GS, bool Z, int NT, int MT, int W>
 __global__ __launch_bounds__(64 * W) void k_w4_few(W4GemmArgs a) {
     constexpr int kPitch = kRowPitch<XT>, kUnit = 8 * sizeof(XT);
@@ -451,9 +451,9 @@ __global__ __launch_bounds__(64 * W) void k_w4_few(W4GemmArgs a) {
 
 template <typename XT, int GS, bool Z, int NT, int MT, int W>
 hipError_t few(const W4GemmArgs& a, hipStream_t st) {
-    const int G = (a.K + 127) / 128, want = G >= 32 ? 8 : (G >= 8 ? 4 : (G >= 4 ? 2 : 1)), waves = want < W ? want : W;
     const unsigned cols = static_cast<unsigned>(((a.N + 15) / 16 + NT - 1) / NT);
     const int blocks = (a.M + 16 * MT - 1) / (16 * MT);
+    const int waves = static_cast<int>(w4_few_waves(static_cast<int64_t>(cols) * blocks, a.K, NT * MT));
     k_w4_few<XT, GS, Z, NT, MT, W><<<dim3(cols, blocks < 65535 ? blocks : 65535), 64 * waves, 0, st>>>(a);
     return hipGetLastError();
 }

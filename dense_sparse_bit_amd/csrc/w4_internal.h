@@ -105,6 +105,16 @@ hipError_t launch_w4_dequant(const W4QuantArgs& a, void* y, int y_dtype, hipStre
 // time, or 16 or 32 rows and these columns, tile by tile; each splits K over its waves. fp32
 // and a plan's rows: at most 16 rows, at most 32 columns for fp32, 64 else.
 enum W4Few { kW4One, kW4Rows16, kW4Rows16x32, kW4Rows16x64, kW4Rows32x32, kW4Rows32x64 };
+
+// Waves of a workgroup of few rows, which share its code tiles: eight where there are so many.
+// Where workgroups fill the chip, four find them short of nothing and have half the sums to add:
+// 100 rows, 2048 x 2048, by 16 rows and 16 columns (896 workgroups) 8.4 us against 10.3; 64 tokens'
+// rows of 64 experts, 4096 x 1024 (6000) 49 against 96. Where they do not, eight are faster: 20 rows,
+// 512 x 2048 (64) 4.5 us against 5.0; 100 rows, 2048 x 2048 by 16 and 32 (448) 7.9 against 8.2.
+inline int64_t w4_few_waves(int64_t workgroups, int64_t K, int tiles) {
+    const int64_t G = w4_tiles(K), most = workgroups > (tiles == 1 ? 256 : 512) && G < 32 ? 4 : 8;
+    return G < most ? G : most;
+}
 hipError_t launch_w4_few(const W4GemmArgs& a, W4Few kind, hipStream_t st);
 hipError_t launch_w4_rows(const W4RowsArgs& a, hipStream_t st);
 // tiles of 32 rt rows and 128 ct columns: rt <= 2 with ct = 1, 2 <= rt <= 4 with ct = 2 (3 or 4 for

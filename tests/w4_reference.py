@@ -77,13 +77,14 @@ def pack_scales(s, R, K, group):
 # Products that between them take every way of the library's (type of x, group, M, N, K, way):
 # few rows, tiles of each size, K in 1, 2, 4 and 8 parts; N and K that fit no tile.
 WAYS = [("bf16", 32, 1, 50, 150, 0), ("fp32", 32, 4, 90, 200, 0), ("fp32", 128, 5, 20, 100, 1), ("fp16", 64, 13, 70, 1030, 1),
-        ("bf16", 32, 3, 8211, 150, 2), ("fp16", 128, 2, 8201, 384, 2), ("fp32", 32, 16, 8300, 200, 2),
-        ("bf16", 64, 20, 33, 200, 4), ("bf16", 32, 150, 12290, 250, 4), ("fp16", 128, 200, 12301, 136, 5), ("bf16", 128, 202, 2050, 8190, 5),
+        ("bf16", 32, 3, 8211, 150, 1), ("fp16", 128, 64, 2049, 8190, 2), ("fp32", 128, 100, 4099, 1500, 2), ("bf16", 64, 64, 4100, 1030, 2),
+        ("bf16", 64, 20, 33, 200, 1), ("fp16", 128, 64, 4090, 2050, 2), ("bf16", 32, 90, 3001, 4090, 4), ("fp16", 128, 250, 2050, 1027, 2),
+        ("bf16", 128, 202, 2050, 8190, 5),
         ("bf16", 128, 301, 30, 100, 8), ("fp16", 64, 300, 17, 1030, 16), ("fp32", 128, 300, 20, 500, 16), ("bf16", 32, 299, 40, 2100, 32),
         ("fp16", 128, 290, 36, 4097, 64), ("bf16", 128, 770, 4100, 129, 9), ("fp16", 32, 1501, 8200, 140, 9),
-        ("fp16", 32, 1003, 1030, 4090, 17), ("fp32", 128, 202, 2050, 5120, 33), ("fp16", 32, 2047, 33, 5130, 65),
+        ("fp16", 32, 1003, 1030, 4090, 17), ("fp32", 32, 400, 1030, 1030, 33), ("fp16", 32, 2047, 33, 5130, 65),
         ("fp16", 64, 200, 16385, 8190, 10), ("fp32", 128, 1001, 4100, 4096, 10), ("fp32", 64, 200, 8208, 4096, 18),
-        ("fp32", 128, 80, 8208, 5120, 34), ("fp32", 128, 200, 2045, 5119, 66), ("bf16", 32, 770, 12200, 4000, 11),
+        ("fp32", 128, 80, 8208, 5120, 34), ("fp32", 64, 60, 8190, 5119, 66), ("bf16", 32, 770, 12200, 4000, 11),
         ("bf16", 128, 2050, 12290, 160, 11), ("fp32", 32, 400, 12290, 2049, 19), ("fp16", 64, 80, 12300, 8192, 35),
         ("bf16", 32, 80, 8191, 8190, 67), ("fp32", 128, 80, 8190, 4095, 67), ("bf16", 128, 2047, 12287, 127, 12),
         ("fp32", 128, 1001, 16381, 130, 12), ("fp32", 128, 1000, 4095, 4094, 20), ("fp16", 128, 199, 8190, 8190, 36),
