@@ -212,3 +212,66 @@ def test_a_layer_of_experts_as_it_is_served(mq, T, dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(z, layer()[0])
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 512), (4, 40, 512), (30, 40, 512), (300, 100, 512), (1000, 4100, 128), (300, 40, 4100)])
+@pytest.mark.parametrize("x_type", ["bf16", "fp32"])
+def test_rows_that_share_their_memory(mq, x_type, M, N, K):
+    """Expanded and overlapping rows: strides of 0, of 8 and of K - 8."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    w, _, _, values = _weights(mq, g, N, K, 64, "fp16", lambda shape: torch.full(shape, 2.0 ** -6, device="cuda"), True)
+    flat = torch.randint(-4, 5, (M * K,), generator=g, device="cuda").to(_dtype(x_type))
+    for stride in (0, 8, K - 8):
+        x = flat.as_strided((M, K), (stride, 1))
+        want = (x.double() @ values.T.contiguous()).float()
+        assert torch.equal(mq.w4_linear(x, w, out_dtype=torch.float32), want)
+
+
+@pytest.mark.parametrize("T", [1, 6, 40, 700])
+def test_a_token_with_one_expert_twice(mq, T):
+    """Each slot has a row of its own, and the sums go over all of them; gradients too."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T)
+    E, k, D, N = 5, 3, 136, 40
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    ids[:, 1] = ids[:, 0]
+    plan = mq.expert_plan(ids, E)
+    x = torch.randint(-4, 5, (T, D), generator=g, device="cuda").float().requires_grad_()
+    weights = (torch.randint(1, 5, (T, k), generator=g, device="cuda") / 4.0).requires_grad_()
+    rows = mq.experts_gather(x, plan)
+    y = mq.experts_combine(rows, plan, weights)
+    assert torch.equal(y, x * weights.sum(1, keepdim=True))
+    dy = torch.randint(-3, 4, (T, D), generator=g, device="cuda").float()
+    dx, dw = torch.autograd.grad(y, (x, weights), dy)
+    assert torch.equal(dx, dy * weights.sum(1, keepdim=True))
+    assert torch.equal(dw, (dy * x).sum(1, keepdim=True).expand(T, k))
+    w, _, _, values = _weights(mq, g, N, D, 64, "fp16", lambda shape: torch.full(shape, 2.0 ** -6, device="cuda"), True, (E,))
+    out = mq.experts_combine(mq.w4_experts_linear(x.detach(), w, plan, by_token=True, out_dtype=torch.float32), plan)
+    want = sum((values[ids[:, j].long()] * x.detach().double()[:, None, :]).sum(2) for j in range(k))
+    assert torch.equal(out, want.float())
+
+
+def test_rows_past_32_bits(mq):
+    """Rows of x spread over 5.2 GB: byte offsets beyond 2^32, for every call that takes strides."""
+    import torch
+    flat = torch.empty(2_600_000_000, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    K, N, E = 256, 40, 4
+    w, _, _, values = _weights(mq, g, N, K, 64, "fp16", lambda shape: torch.full(shape, 2.0 ** -6, device="cuda"), True)
+    we, _, _, ve = _weights(mq, g, N, K, 64, "fp16", lambda shape: torch.full(shape, 2.0 ** -6, device="cuda"), True, (E,))
+    for M in (3, 4, 30, 300, 1500):
+        x = torch.randint(-4, 5, (M, K), generator=g, device="cuda").bfloat16()
+        far = flat.as_strided((M, K), ((flat.numel() - K) // (M - 1) // 8 * 8, 1))
+        far.copy_(x)
+        assert (M - 1) * far.stride(0) * 2 > 2 ** 32
+        want = (x.double() @ values.T.contiguous()).float()
+        assert torch.equal(mq.w4_linear(far, w, out_dtype=torch.float32), want)
+        a, b = mq.w4_quantize(far, group=32, zeros=True), mq.w4_quantize(x, group=32, zeros=True)
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales) and torch.equal(a.zeros, b.zeros)
+        plan = mq.expert_plan(torch.rand(M, E, generator=g, device="cuda").topk(2, 1).indices.int(), E)
+        rows = mq.experts_gather(x, plan)
+        assert torch.equal(mq.experts_gather(far, plan), rows)
+        near = mq.w4_experts_linear(x, we, plan, by_token=True, out_dtype=torch.float32)
+        assert torch.equal(mq.w4_experts_linear(far, we, plan, by_token=True, out_dtype=torch.float32), near)
+        assert torch.equal(near, mq.w4_experts_linear(rows, we, plan, out_dtype=torch.float32))
