@@ -243,7 +243,8 @@ def experts_gather(x, plan: ExpertPlan, weights=None, rows=None, stream=None):
     """Tokens to the rows of their experts: rows [P, D] of x's type, x[t] (times weights[t, j],
     where given) at row plan.row_of[t, j], zero for rows of no token. x [T, D] (fp32, bf16,
     fp16; its last axis contiguous), weights fp32 [T, k]. Has gradients of x (the sum over the
-    token's rows, in the order of the slots) and of weights."""
+    token's rows, in the order of the slots) and of weights. A backward pass that is captured
+    into a graph takes leaves of its own and torch.autograd.grad, as of any torch function."""
     if stream is not None:
         _input(x, "x", 2)
         with _on(x.get_device(), stream, x, plan, weights, rows):

@@ -373,7 +373,10 @@ def test_a_layer_of_plain_experts_trains_through_them(mq):
     each = torch.stack([torch.stack([e64[int(ids[t, j])] @ x64[t] for j in range(k)]) for t in range(T)])
     want = torch.autograd.grad((w64[:, :, None] * each).sum(1), (x64, r64, e64), dy.double())
     for a, b in zip(got, want):
-        # a few dozen fp32 products and sums deep, of values near 1
+        # The longest way, to the router's gradient: a logit's 24 products, a softmax (8), an expert's 24, a dot's
+        # 24, the softmax's gradient (8), a sum over 40 tokens: 128 roundings of half a step (2^-24), each of
+        # sums whose magnitudes add up to at most 25 times the largest value: 3200 of them, and a fourth for
+        # the products of errors and for exp.
         assert (a.double() - b).abs().max() <= 4000 * 2.0 ** -24 * b.abs().max()
 
 
