@@ -250,7 +250,8 @@ def experts_gather(x, plan: ExpertPlan, weights=None, rows=None, stream=None):
         with _on(x.get_device(), stream, x, plan, weights, rows):
             return experts_gather(x, plan, weights, rows)
     if _wants_gradient(rows, "rows", x, weights):
-        return _Gather.apply(x, weights, plan)
+        done = None if _binding is None else _binding.gather_grad(x, plan, weights)
+        return _Gather.apply(x, weights, plan) if done is None else done
     return _gather(x, plan, weights, None, rows, None)
 
 
@@ -265,7 +266,8 @@ def experts_combine(rows, plan: ExpertPlan, weights=None, out_dtype=None, y=None
         with _on(rows.get_device(), stream, rows, plan, weights, y):
             return experts_combine(rows, plan, weights, out_dtype, y)
     if _wants_gradient(y, "y", rows, weights):
-        return _Combine.apply(rows, weights, plan, out_dtype)
+        done = None if _binding is None else _binding.combine_grad(rows, plan, weights, out_dtype)
+        return _Combine.apply(rows, weights, plan, out_dtype) if done is None else done
     return _combine(rows, plan, weights, out_dtype, y, None)
 
 

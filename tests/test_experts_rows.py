@@ -406,3 +406,48 @@ def test_the_long_way_gives_the_same_bits(mq, monkeypatch):
         monkeypatch.setattr(f"dense_sparse_bit_amd.{name}._binding", None)
     for a, b in zip(calls(), short):
         assert a.dtype == b.dtype and torch.equal(a, b)
+
+
+def test_a_graph_kept_freed_and_differentiated_twice(mq):
+    """A kept graph gives the same again, a freed one and a second derivative are errors, and a
+    thread of its own runs one while another goes on."""
+    import threading
+    import torch
+    g = _gen(11)
+    _, plan = _plan(mq, g, 20, 4, 2)
+    x = torch.randn(20, 24, generator=g, device="cuda").requires_grad_()
+    w = torch.rand(20, 2, generator=g, device="cuda").requires_grad_()
+    dy = torch.randn(20, 24, generator=g, device="cuda")
+    y = mq.experts_combine(mq.experts_gather(x, plan, w), plan, w)
+    first = torch.autograd.grad(y, (x, w), dy, retain_graph=True)
+    again = torch.autograd.grad(y, (x, w), dy)
+    for a, b in zip(first, again):
+        assert torch.equal(a, b)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y, (x, w), dy)
+    for d in (dy, dy.clone().requires_grad_()):
+        y = mq.experts_combine(mq.experts_gather(x, plan, w), plan, w)
+        dx, dw = torch.autograd.grad(y, (x, w), d, create_graph=True)
+        assert torch.equal(dx, first[0]) and torch.equal(dw, first[1])
+        for v in (dx, dw):
+            with pytest.raises(RuntimeError):
+                v.sum().backward(retain_graph=True)
+    with torch.no_grad():
+        assert not mq.experts_gather(x, plan, w).requires_grad
+    results = [None] * 4
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            torch.cuda.current_stream().wait_stream(torch.cuda.default_stream())
+            xl, wl = x.detach().clone().requires_grad_(), w.detach().clone().requires_grad_()
+            for _ in range(10):
+                y = mq.experts_combine(mq.experts_gather(xl, plan, wl), plan, wl)
+                results[i] = torch.autograd.grad(y, (xl, wl), dy)
+            torch.cuda.current_stream().synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for r in results:
+        assert torch.equal(r[0], first[0]) and torch.equal(r[1], first[1])
