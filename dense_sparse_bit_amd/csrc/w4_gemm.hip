@@ -220,7 +220,9 @@ __device__ __forceinline__ MxRaw8<XT> load8(const XT* row, int k, int K, bool wh
 // code tiles (512 inputs), which are loaded while the quad before is multiplied. A row reaches
 // the matrix instructions through LDS, one load of 1 KB a quad; the sums of its groups come
 // from the lanes that loaded it. The instructions' rows 0 .. RB - 1 (lanes 0 .. 15 of the
-// result) are the rows, the others repeat the last. GS: groups in 128 inputs.
+// result) are the rows, the others repeat the last. GS: groups in 128 inputs. Bound by latency: a
+// launch, the row, a batch of loads; 1 x 4096 x 4096 takes 4.1 to 4.4 us, one token by 8 experts of
+// 1024 x 4096 6.4 (reading their weights at the rate of a large copy: 1.7 and 3.4).
 template <typename XT, int GS, bool Z, int RB>
 __global__ __launch_bounds__(64 * kMaxWaves) void k_w4_one(W4GemmArgs a) {
     typedef W4Op<XT> Op;

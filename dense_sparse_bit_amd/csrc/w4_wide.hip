@@ -17,7 +17,9 @@ constexpr int kThreads = 256;
 // The sums of each row's groups, [stage][group][row] units of 16 bytes: bf16 hi, mid, lo, hi,
 // mid, lo, 0, 0 (the second three meet the low part of z), and where `copy` is given the
 // rows themselves, [row][stage][128], zeros past K. A stage is 128 inputs; of fp32 rows, of
-// one of their planes (stage 3h + plane). One wave: 512 inputs of four rows.
+// one of their planes (stage 3h + plane). One wave: 512 inputs of four rows. Once for all the tiles
+// that take a row, which would else each make its sums again. 2048 x 5120
+// of bf16 6 us, 33000 x 1024 19 us (3.5 TB/s): bound by the reads.
 constexpr int kRows = 4;
 template <typename XT>
 __global__ __launch_bounds__(kThreads) void k_w4_rows(const XT* x, int64_t R, int64_t stride, int K, int group, uint4* sums,
@@ -373,7 +375,7 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[c] += n + c < N ? bias[n + c] : 0.0f;
             }
-            if (row_token && !parted && static_cast<unsigned>(row_token[p]) >= static_cast<unsigned>(T)) {
+            if (row_token && static_cast<unsigned>(row_token[p]) >= static_cast<unsigned>(T)) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[c] = 0.0f;
             }
@@ -388,9 +390,8 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
 // zeros for rows after the last expert's
 template <int COLS>
 __device__ void zero_rows(const Args& a, int row0, int rows, int n0) {
-    const bool parted = a.partial != nullptr;
-    void* const y = parted ? a.partial + static_cast<int64_t>(blockIdx.y) * a.M * a.N : a.y;
-    const int y_dtype = parted ? MQ_F32 : a.y_dtype;
+    void* const y = a.y;                                 // (a plan's rows have no parts of K)
+    const int y_dtype = a.y_dtype;
     const float none[8] = {};
     for (int i = threadIdx.x; i < rows * (COLS / 8); i += kThreads) {
         const int n = n0 + i % (COLS / 8) * 8;
@@ -402,29 +403,26 @@ __device__ void zero_rows(const Args& a, int row0, int rows, int n0) {
     }
 }
 
-// y = the parts' sums, in the order of the parts, and the bias; zero for rows of no token.
-// Eight outputs a thread.
+// y = the parts' sums, in the order of the parts, and the bias.
+// Eight outputs a thread. A launch, and about 0.4 us for each MB of sums written and read.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_w4_add(const float* partial, int parts, int64_t M, int N, const float* bias,
-                                                     const int32_t* row_token, int tokens, T* y) {
+__global__ __launch_bounds__(kThreads) void k_w4_add(const float* partial, int parts, int64_t M, int N, const float* bias, T* y) {
     const int n = (blockIdx.x * kThreads + threadIdx.x) * 8;
     if (n >= N) return;
     for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
         float sum[8] = {};
-        if (!row_token || static_cast<unsigned>(row_token[m]) < static_cast<unsigned>(tokens)) {
-            for (int p0 = 0; p0 < parts; p0 += 4) {
-                MxRaw8<float> v[4];
+        for (int p0 = 0; p0 < parts; p0 += 4) {
+            MxRaw8<float> v[4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) v[p] = mx_load8(partial + ((p0 + p) * M + m) * N + n, p0 + p < parts ? N - n : 0);
+            for (int p = 0; p < 4; ++p) v[p] = mx_load8(partial + ((p0 + p) * M + m) * N + n, p0 + p < parts ? N - n : 0);
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
+            for (int p = 0; p < 4; ++p)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sum[i] += v[p].v[i];
-            }
-            if (bias) {
+                for (int i = 0; i < 8; ++i) sum[i] += v[p].v[i];
+        }
+        if (bias) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] += n + i < N ? bias[n + i] : 0.0f;
-            }
+            for (int i = 0; i < 8; ++i) sum[i] += n + i < N ? bias[n + i] : 0.0f;
         }
         w4_store8(y + m * N + n, N - n, sum);
     }
@@ -433,11 +431,14 @@ __global__ __launch_bounds__(kThreads) void k_w4_add(const float* partial, int p
 template <typename T>
 hipError_t add_parts(const W4WideArgs& a, hipStream_t st) {
     const dim3 grid((a.N + 8 * kThreads - 1) / (8 * kThreads), a.M < 65535 ? a.M : 65535);
-    k_w4_add<T><<<grid, kThreads, 0, st>>>(a.partial, a.parts, a.M, a.N, a.bias, a.row_token, a.T, static_cast<T*>(a.y));
+    k_w4_add<T><<<grid, kThreads, 0, st>>>(a.partial, a.parts, a.M, a.N, a.bias, static_cast<T*>(a.y));
     return hipGetLastError();
 }
 
-// Four waves side by side, on blocks of at most 32 RT rows.
+// Four waves side by side, on blocks of at most 32 RT rows. Bound by the matrix units, whose power
+// holds the clock near 1.9 GHz, and by the changes of units: 2048 x 17408 x 5120 of bf16 again and
+// again, groups of 128 / 64 / 32: 362 / 418 / 528 us (1.01 / 0.87 / 0.69 PFLOP/s; a bf16 library
+// product of the size 0.92). Which tile a product takes is fitted in api_w4.hip.
 template <typename E, int GS, int RT, int CT>
 __global__ __launch_bounds__(kThreads, 2) void k_w4_wide(W4WideArgs) {
     const Args& a = *(const Args*)__builtin_amdgcn_kernarg_segment_ptr();
