@@ -502,8 +502,8 @@ int mq_w4_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* co
                  void* y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /* The way that such a product takes, a status below 0 outside the supported sizes. Kernels of
- * few rows, K split over a workgroup's waves: 0: 4 rows and 16 columns a workgroup; 1, 2, 3: 16
- * rows and 16, 32, 64 columns; 4, 5: 32 rows and 32, 64 columns. 8 p + t: tiles with K in p
+ * few rows, K split over a workgroup's waves: 0: 4 rows and 16 columns a workgroup; 1, 2: 16
+ * rows and 16, 32 columns; 4, 5: 32 rows and 32, 64 columns. 8 p + t: tiles with K in p
  * parts, t = 0 .. 4: 32 x 128, 64 x 128, 64 x 256, 96 x 256, 128 x 256. Tiles hold sums in
  * units of the present scale of a row of w: there a group counts as zero whose scale is below 2^-64 of
  * the largest of the row's earlier groups, or below 2^-126. The ways give the same sums in another
