@@ -201,14 +201,21 @@ Way dense_way(int64_t M, int64_t N, int64_t K, int x_dtype, int group) {
 }
 
 // 64 experts, 8 a token, 1024 x 4096 / 4096 x 1024, in us: 1 token one row at a time 5.9 / 5.7, by
-// 16 rows 6.8 / 7.0; 64 tokens by 16 rows 39 / 43, by tiles 51 / 43; 128 tokens 51 / 58 and 51 / 44.
-// By 16 rows, 32 columns a workgroup / 64: 1024 x 4096 39 / 48, 4096 x 1024 49 / 43. K in parts
-// for tiles of 256 tokens: 65 / 61 / 59 in 1, 2, 4 (1024 x 4096) and 51 / 77 / 124.
-Way experts_way(int64_t T, int64_t k, int64_t E, int64_t K, bool by_token, int x_dtype, int group) {
+// 16 rows 6.8 / 7.0; 64 tokens by 16 rows 42 / 49, by tiles 44 / 41; 128 tokens 57 / 82 and 50 / 49.
+// By 16 rows, 32 columns a workgroup / 64: 1024 x 4096 41 / 49, 4096 x 1024 55 / 45. Where the
+// smallest tiles leave CUs idle 16 rows serve longer: 64 tokens of 2 of 8, 4096 x 4096 34 against 38.
+// Tiles of 32 or 64 rows and 128 columns where they make few workgroups, the largest else: 512 tokens
+// of 8 of 64, 1024 x 4096 (512) 83 against 102; 256 of 2 of 8, 4096 x 4096 (256) 50 against 77; 4096
+// of 8 of 64 (4096) 342 against 317. K in parts for 256 tokens: 65 / 61 / 59 in 1, 2, 4
+// (1024 x 4096) and 51 / 77 / 124.
+Way experts_way(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, bool by_token, int x_dtype, int group) {
     if (T == 1) return {mq::kW4One, 0, 0, 1};
     // the tiles find tokens' rows by offsets of 32 bits (in a copy, where x's own are too far apart)
     const bool held = !by_token || mq::w4_copy_size(T, K, mq::w4_planes(x_dtype)) <= kMaxOffset;
-    if (T * k <= 12 * E || !held) return {K > 2048 || x_dtype == MQ_F32 ? mq::kW4Rows16x32 : mq::kW4Rows16x64, 0, 0, 1};
+    const int64_t each = (T * k + E - 1) / E, cols = (N + 127) / 128;
+    if (each <= (E * cols <= 256 ? 24 : 12) || !held)
+        return {K > 2048 || x_dtype == MQ_F32 ? mq::kW4Rows16x32 : mq::kW4Rows16x64, 0, 0, 1};
+    if (E * ((each + 63) / 64) * cols <= 1024) return tiles_way(each <= 32 ? 1 : 2, 1, 1, 1);
     return tiles_way(group == 32 ? 3 : 4, 2, 1, 1);
 }
 
@@ -366,7 +373,7 @@ int mq_w4_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* co
 
 size_t mq_w4_experts_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int by_token, int x_dtype, int group) {
     if (check_experts(T, k, E, N, K, group) || bad_type(x_dtype)) return 0;
-    const Way way = experts_way(T, k, E, K, by_token != 0, x_dtype, group);
+    const Way way = experts_way(T, k, E, N, K, by_token != 0, x_dtype, group);
     const int64_t P = mq::plan_rows(T, k, E);
     return way.rt ? Parts(by_token ? T : P, K, x_dtype, group, mq::w4_blocks_cap(P, E, way.rt), way.parts, P, N).bytes : 0;
 }
@@ -389,7 +396,7 @@ int mq_w4_experts(const void* x, int x_dtype, int64_t stride_r, int by_token, in
     a.E = static_cast<int>(E);
     a.T = static_cast<int>(T);
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const Way way = experts_way(T, k, E, K, by_token != 0, x_dtype, group);
+    const Way way = experts_way(T, k, E, N, K, by_token != 0, x_dtype, group);
     return way.rt ? wide(a, way, by_token ? T : a.M, offsets, workspace, workspace_bytes, st) : status_of(mq::launch_w4_few(a, way.few, st));
 }
 

@@ -29,7 +29,9 @@ __global__ __launch_bounds__(kThreads) void k_w4_rows(const XT* x, int64_t R, in
     if (static_cast<int>(blockIdx.x) < first) {
         if (blockIdx.y == 0) {
             if (rt == 4) plan_tiles<8>(plan, lds);
-            else plan_tiles<6>(plan, lds);
+            else if (rt == 3) plan_tiles<6>(plan, lds);
+            else if (rt == 2) plan_tiles<4>(plan, lds);
+            else plan_tiles<2>(plan, lds);
         }
         return;
     }

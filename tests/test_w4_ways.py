@@ -127,7 +127,8 @@ def test_a_scale_that_falls_step_by_step(mq, M, group):
 
 @pytest.mark.parametrize("x_type", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("group", [32, 64, 128])
-@pytest.mark.parametrize("T,E,k,N,K", [(400, 4, 2, 300, 264), (90, 2, 1, 2100, 130), (2000, 8, 4, 530, 512), (257, 3, 3, 64, 4100)])
+@pytest.mark.parametrize("T,E,k,N,K", [(400, 4, 2, 300, 264), (90, 2, 1, 2100, 130), (2000, 8, 4, 530, 512), (257, 3, 3, 64, 4100),
+                                       (60, 4, 2, 300, 264), (70, 8, 4, 4500, 200), (100, 40, 10, 900, 130), (900, 16, 4, 4100, 130)])
 def test_experts_tiles_by_token_and_by_row(mq, x_type, group, T, E, k, N, K):
     """Tiles of both sizes, rows from x itself and from a copy; a tenth of the slots without an expert."""
     import torch
