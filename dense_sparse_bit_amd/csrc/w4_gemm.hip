@@ -8,6 +8,7 @@
 // instructions, against ones.
 #include "w4_device.h"
 #include "w4_internal.h"
+#include "w4_tiles.h"
 
 namespace mq {
 namespace {
@@ -396,9 +397,8 @@ __global__ __launch_bounds__(64 * W) void k_w4_few(W4GemmArgs a) {
                 }
                 from[i] = static_cast<const XT*>(a.x) + r * a.stride_x;
             }
-            // (through buffers, whose addresses take no vector registers; past the last column
-            // tile they give zeros)
-            const int have = min(NT, n_tiles - ct), scale_bytes = Q * 16 * 4 * GS * 2;
+            // (through buffers, whose addresses take no vector registers)
+            const int have = min(NT, n_tiles - ct), scale_bytes = w4_scale_bytes(Q, GS);
             const int64_t tile = static_cast<int64_t>(e) * n_tiles + ct;
             const __amdgpu_buffer_rsrc_t wr = buffer(a.codes + tile * G * 1024, static_cast<int64_t>(have) * G * 1024);
             const __amdgpu_buffer_rsrc_t scr = buffer(a.scales + tile * (scale_bytes / 2), static_cast<int64_t>(have) * scale_bytes);
@@ -414,10 +414,10 @@ __global__ __launch_bounds__(64 * W) void k_w4_few(W4GemmArgs a) {
                     if (4 * i < rows) v[i] = load8(from[i], 128 * h + 8 * (lane & 15), a.K, 128 * (h + 1) <= a.K);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    next[j] = load16(wr, lane * 16, (j * G + h) * 1024);
-                    const int at = j * scale_bytes + ((h >> 2) * 16 * 4 + (h & 3)) * GS * 2;
-                    next_s[j] = load_scales<GS>(scr, (lane & 15) * 8 * GS, at);
-                    if constexpr (Z) next_z[j] = load_scales<GS>(zr, (lane & 15) * 8 * GS, at);
+                    const int t = w4_block_tile(j, 1, have), at = w4_scale_at(t, h, Q, GS);
+                    next[j] = load16(wr, w4_lane_code(lane), w4_code_at(t, h, G));
+                    next_s[j] = load_scales<GS>(scr, w4_lane_scale(lane, GS), at);
+                    if constexpr (Z) next_z[j] = load_scales<GS>(zr, w4_lane_scale(lane, GS), at);
                 }
             };
             if (kAhead && h0 < h1) load(h0);

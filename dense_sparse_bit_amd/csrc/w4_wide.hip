@@ -7,6 +7,7 @@
 #include "plan_tiles.h"
 #include "w4_device.h"
 #include "w4_internal.h"
+#include "w4_tiles.h"
 
 namespace mq {
 namespace {
@@ -207,12 +208,14 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
     // weights: a wave with no column of its own (past N) reads the last tile's and writes nothing
     const int tile0 = min(n0 / 16, n_tiles - 1), have = min(n_tiles - tile0, 2 * CT);
     const int64_t first = static_cast<int64_t>(e) * n_tiles + tile0;
-    const int scale_bytes = Q * 16 * 4 * GS * 2;         // of a row tile
+    const int scale_bytes = w4_scale_bytes(Q, GS);       // of a row tile
     const __amdgpu_buffer_rsrc_t wr = buffer(a.codes + first * G * 1024, static_cast<int64_t>(have) * G * 1024);
     const __amdgpu_buffer_rsrc_t scr = buffer(a.scales + first * (scale_bytes / 2), static_cast<int64_t>(have) * scale_bytes);
     const __amdgpu_buffer_rsrc_t zr = has_zeros ? buffer(a.zeros + first * (scale_bytes / 2), static_cast<int64_t>(have) * scale_bytes) : scr;
-    const int wat = (lane >> 4 & 1) * G * 1024 + (half * 16 + (lane & 15)) * 16;
-    const int scat = (lane >> 4 & 1) * scale_bytes + (lane & 15) * 8 * GS;
+    const int wat = w4_pair_code(lane, have, G), scat = w4_pair_scale(lane, have, Q, GS);
+    int block[CT];                                       // the first tiles of the blocks of 32 columns
+#pragma unroll
+    for (int j = 0; j < CT; ++j) block[j] = w4_block_tile(j, 2, have);
     // words w of [j][0] are steps 2w, of [j][1] steps 2w + 1
     typedef typename W4Scales<GS>::T Scales;
     struct Weights {
@@ -225,13 +228,14 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
         else return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(r, scat, at, 0));
     };
     auto load_w = [&](int stage, Weights& to) __attribute__((always_inline)) {
-        const int h = planes == 1 ? stage : stage / 3, at = ((h >> 2) * 64 + (h & 3)) * GS * 2;
+        const int h = planes == 1 ? stage : stage / 3;
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
-            to.c[j][0] = load16(wr, wat, 2 * j * G * 1024 + h * 1024);
-            to.c[j][1] = load16(wr, wat, 2 * j * G * 1024 + h * 1024 + 512);
-            to.s[j] = scales_at(scr, 2 * j * scale_bytes + at);
-            to.z[j] = scales_at(zr, 2 * j * scale_bytes + at);
+            const int at = w4_code_at(block[j], h, G);
+            to.c[j][0] = load16(wr, wat, at);
+            to.c[j][1] = load16(wr, wat, at + 512);
+            to.s[j] = scales_at(scr, w4_scale_at(block[j], h, Q, GS));
+            to.z[j] = scales_at(zr, w4_scale_at(block[j], h, Q, GS));
         }
     };
     mx_f16 acc[RT][CT] = {};
@@ -363,7 +367,7 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
         for (int j = 0; j < CT; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                *reinterpret_cast<float*>(tile + (8 * (r >> 2) + 4 * half + (r & 3)) * kPitch + (32 * j + (lane & 31)) * 4) =
+                *reinterpret_cast<float*>(tile + (8 * (r >> 2) + 4 * half + (r & 3)) * kPitch + (16 * block[j] + (lane & 31)) * 4) =
                     acc[i][j][r] * unit[j];
         mx_wave_sync();
 #pragma unroll
