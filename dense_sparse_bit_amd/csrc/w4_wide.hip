@@ -129,6 +129,7 @@ template <int RT, int GS, int D> struct WideLds {
     static constexpr int kOut = 32 * (64 * 4 + 16);      // a wave's results on their way out
     static constexpr int kBytes = D * kStage > 4 * kOut ? D * kStage : 4 * kOut;
 };
+template <int N> struct Count { static constexpr int value = N; };
 // Every wave's loads but the last N are done, and so are all waves' reads before.
 template <int N>
 __device__ __forceinline__ void loads_and_barrier() {
@@ -192,7 +193,10 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
     }
     const uint16_t* const x0 = a.x + first_row * a.ldx;
     const int64_t x_bytes = ((by_token ? T : rows) - 1) * a.ldx * 2 + 256;         // behind a stage's first input
-    constexpr int kLoads = 2 * RT + kSumsPer + 4 * CT;   // of a stage, in every wave
+    // Loads of a stage, in every wave. A stage's rows are waited for by the number of loads issued
+    // after them, so all of a stage's are issued before the next stage's first: the barriers
+    // within run() see to that, and the fences between the stages that come before it.
+    constexpr int kLoads = 2 * RT + kSumsPer + 4 * CT;
     static_assert(D == 2 || kUnits <= 64);
     auto load_x = [&](int stage, int buf) __attribute__((always_inline)) {
         uint8_t* const to = lds + buf * L::kStage;
@@ -275,16 +279,19 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
     for (int d = 0; d < D - 1; ++d) {
         load_x(min(first_stage + d, last), d);
         load_w(min(first_stage + d, last), W[d]);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     }
     begin(W[0], 0);
 #pragma unroll
     for (int i = 0; i < RT; ++i) convert(W[0], 0, i);
     const int swap = (half ^ (lane & 15)) * 16;
     // Stage `stage` (whose weights are in `now`, the next one's in `after`). Loads past the last
-    // stage are of that again, and not used: a wave's loads are counted.
+    // stage are of that again, and not used: a wave's loads are counted. `later`: how many of them
+    // may still be on their way.
     int buf = 0;
-    auto run = [&](int stage, Weights& now, Weights& after) __attribute__((always_inline)) {
-        loads_and_barrier<(D - 2) * kLoads>();           // stage's rows are there, reads of the buffer to be filled are done
+    auto run = [&](auto later, int stage, Weights& now, Weights& after) __attribute__((always_inline)) {
+        loads_and_barrier<decltype(later)::value>();     // stage's rows are there, reads of the buffer to be filled are done
         const Weights w = now;
         load_x(min(stage + D - 1, last), buf == 0 ? D - 1 : buf - 1);
         load_w(min(stage + D - 1, last), now);
@@ -345,14 +352,17 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
             }
         }
     };
+    constexpr Count<(D - 2) * kLoads> kLater{};
     int stage = first_stage;
     for (; stage + D - 2 <= last; stage += D - 1) {
 #pragma unroll
-        for (int d = 0; d < D - 1; ++d) run(stage + d, W[d], W[d + 1 == D - 1 ? 0 : d + 1]);
+        for (int d = 0; d < D - 1; ++d) run(kLater, stage + d, W[d], W[d + 1 == D - 1 ? 0 : d + 1]);
     }
-#pragma unroll
-    for (int d = 0; d < D - 2; ++d)
-        if (stage + d <= last) run(stage + d, W[d], W[d + 1]);
+    // (nothing uses the weights that the first of these loads, and the compiler leaves them out: the
+    // second cannot count on them, and has nothing but loads of the last stage again behind it)
+    static_assert(D <= 4);
+    if (D > 2 && stage <= last) run(kLater, stage, W[0], W[D > 2 ? 1 : 0]);
+    if (D > 3 && stage + 1 <= last) run(Count<0>{}, stage + 1, W[D > 3 ? 1 : 0], W[D > 3 ? 2 : 0]);
 
     // The results leave through LDS, piece by piece: a lane holds one column of rows
     // 8 (r / 4) + 4 (l / 32) + r % 4; read back, a lane holds eight columns of a row.
