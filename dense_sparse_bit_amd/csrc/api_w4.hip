@@ -219,13 +219,15 @@ Way experts_way(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, bool by_t
     return tiles_way(group == 32 ? 3 : 4, 2, 1, 1);
 }
 
-// Workspace of the tiles: the rows' sums, a copy of the rows, row blocks
+// Workspace of the tiles: the rows' sums, a copy of the rows (whether x needs one or not: the
+// size is asked for without x), the W tiles' marks, row blocks, sums of parts of K
 struct Parts {
-    size_t copy, tiles, partial, bytes;
-    Parts(int64_t R, int64_t K, int x_dtype, int group, int64_t blocks, int parts, int64_t M, int64_t N) {
+    size_t copy, wild, tiles, partial, bytes;
+    Parts(int64_t R, int64_t K, int x_dtype, int group, int64_t blocks, int parts, int64_t M, int64_t N, int64_t E) {
         const int planes = mq::w4_planes(x_dtype);
         copy = mq::w4_sums_size(R, K, planes, group);
-        tiles = copy + round16(mq::w4_copy_size(R, K, planes));
+        wild = copy + round16(mq::w4_copy_size(R, K, planes));
+        tiles = wild + round16(E * mq::w4_row_tiles(N) * 4);
         partial = tiles + round16(blocks ? (4 + 4 * blocks) * 4 : 0);
         bytes = partial + (parts > 1 ? round16(parts * M * N * 4) : 0);
     }
@@ -234,7 +236,7 @@ struct Parts {
 // The rows' part, then the tiles. R: rows of x.
 int wide(const mq::W4GemmArgs& a, Way way, int64_t R, const int32_t* offsets, void* workspace, size_t workspace_bytes, hipStream_t st) {
     const int64_t blocks = offsets ? mq::w4_blocks_cap(a.M, a.E, way.rt) : 0;
-    const Parts parts(R, a.K, a.x_dtype, a.group, blocks, way.parts, a.M, a.N);
+    const Parts parts(R, a.K, a.x_dtype, a.group, blocks, way.parts, a.M, a.N, offsets ? a.E : 1);
     if (workspace_bytes < parts.bytes || !workspace || off(workspace, 16)) return MQ_ERR_INVALID_ARG;
     uint8_t* const work = static_cast<uint8_t*>(workspace);
     const bool as_it_is = a.x_dtype != MQ_F32 && !off(a.x, 16) && a.stride_x % 8 == 0 && a.K % 128 == 0 &&
@@ -250,6 +252,9 @@ int wide(const mq::W4GemmArgs& a, Way way, int64_t R, const int32_t* offsets, vo
     r.copy = as_it_is ? nullptr : work + parts.copy;
     int32_t* const tiles = reinterpret_cast<int32_t*>(work + parts.tiles);
     r.rt = way.rt;
+    r.scales = a.scales;
+    r.tiles = a.scale_dtype == MQ_BF16 ? (offsets ? a.E : 1) * mq::w4_row_tiles(a.N) : 0;
+    r.wild = reinterpret_cast<int*>(work + parts.wild);
     if (offsets) r.plan = {offsets, a.E, a.M / 16, tiles, static_cast<int>(blocks)};
     if (mq::launch_w4_rows(r, st) != hipSuccess) return MQ_ERR_HIP;
     mq::W4WideArgs w = {};
@@ -260,6 +265,7 @@ int wide(const mq::W4GemmArgs& a, Way way, int64_t R, const int32_t* offsets, vo
     w.rows_x = R;
     w.planes = mq::w4_planes(a.x_dtype);
     w.sums = static_cast<const uint4*>(r.sums);
+    w.wild = r.wild;
     w.codes = a.codes;
     w.scales = a.scales;
     w.zeros = a.zeros;
@@ -343,7 +349,7 @@ int mq_w4_dequantize(const uint8_t* codes, const void* scales, const void* zeros
 size_t mq_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_dtype, int group) {
     if (check_product(M, N, K, group) || bad_type(x_dtype)) return 0;
     const Way way = dense_way(M, N, K, x_dtype, group);
-    return way.rt ? Parts(M, K, x_dtype, group, 0, way.parts, M, N).bytes : 0;
+    return way.rt ? Parts(M, K, x_dtype, group, 0, way.parts, M, N, 1).bytes : 0;
 }
 
 int mq_w4_linear_way(int64_t M, int64_t N, int64_t K, int x_dtype, int group) {
@@ -375,7 +381,7 @@ size_t mq_w4_experts_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N,
     if (check_experts(T, k, E, N, K, group) || bad_type(x_dtype)) return 0;
     const Way way = experts_way(T, k, E, N, K, by_token != 0, x_dtype, group);
     const int64_t P = mq::plan_rows(T, k, E);
-    return way.rt ? Parts(by_token ? T : P, K, x_dtype, group, mq::w4_blocks_cap(P, E, way.rt), way.parts, P, N).bytes : 0;
+    return way.rt ? Parts(by_token ? T : P, K, x_dtype, group, mq::w4_blocks_cap(P, E, way.rt), way.parts, P, N, E).bytes : 0;
 }
 
 int mq_w4_experts(const void* x, int x_dtype, int64_t stride_r, int by_token, int64_t T, int64_t k, int64_t E, int64_t N,

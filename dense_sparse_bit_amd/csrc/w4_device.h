@@ -82,6 +82,33 @@ __device__ __forceinline__ uint32_t w4_word(const uint32_t (&c)[8]) {
 // The scales or zero points of a code tile's groups in one word.
 template <int GS> struct W4Scales { typedef uint32_t T; };
 template <> struct W4Scales<4> { typedef uint64_t T; };
+template <int GS>
+__device__ __forceinline__ typename W4Scales<GS>::T w4_scales(const uint16_t* p) {
+    if constexpr (GS == 1) return *p;
+    else return *reinterpret_cast<const typename W4Scales<GS>::T*>(p);
+}
+
+// The scales or zero points of a quad of code tiles (4 GS of them).
+template <int GS> struct W4Quad {
+    uint32_t w[2 * GS];
+    __device__ __forceinline__ void load(const uint16_t* p) {
+        if constexpr (GS == 1) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            w[0] = v.x;
+            w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < GS / 2; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ float get(int i, bool bf) const { return w4_float(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffff, bf); }
+};
 
 // Eight codes as bf16 or fp16, exactly, in the order of the inputs: as e4m3 bytes they are
 // c * 2^-9. A mask of 0 makes them zeros.

@@ -83,28 +83,6 @@ __device__ __forceinline__ typename W4Scales<GS>::T load_scales(__amdgpu_buffer_
     else return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(r, lane_at, at, 0));
 }
 
-// The scales or zero points of a quad of code tiles (4 GS of them).
-template <int GS> struct Quad {
-    uint32_t w[2 * GS];
-    __device__ __forceinline__ void load(const uint16_t* p) {
-        if constexpr (GS == 1) {
-            const uint2 v = *reinterpret_cast<const uint2*>(p);
-            w[0] = v.x;
-            w[1] = v.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < GS / 2; ++i) {
-                const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-                w[4 * i] = v.x;
-                w[4 * i + 1] = v.y;
-                w[4 * i + 2] = v.z;
-                w[4 * i + 3] = v.w;
-            }
-        }
-    }
-    __device__ __forceinline__ float get(int i, bool bf) const { return w4_float(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffff, bf); }
-};
-
 // ------------------------------------------------------------------- few rows
 constexpr int kMaxWaves = 8;
 // 16 rows of one code tile (128 inputs) in LDS, 16 bytes further apart than they are long, so
@@ -273,7 +251,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_w4_one(W4GemmArgs a) {
             }
             MxRaw8<XT> v[RB];
             mx_i4 c[4], cc[4];
-            Quad<GS> sc, zc, ss, zz;
+            W4Quad<GS> sc, zc, ss, zz;
             auto load = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
                 for (int i = 0; i < RB; ++i)

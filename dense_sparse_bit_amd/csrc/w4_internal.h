@@ -50,7 +50,8 @@ struct W4GemmArgs {
 inline int64_t w4_blocks_cap(int64_t P, int64_t E, int rt) { return P / 16 / (2 * rt) + E + 2; }
 
 // What launch_w4_wide takes of x: the sums of its groups, and a copy where x itself does not
-// do (fp32, or rows that are not made of aligned 16-byte units).
+// do (fp32, or rows that are not made of aligned 16-byte units). And of the scales: which 16-row tiles
+// of W have rows whose scales are too far apart for sums in units of them.
 struct W4RowsArgs {
     const void* x;
     int dtype;
@@ -58,7 +59,10 @@ struct W4RowsArgs {
     int K, group;
     void *sums, *copy;
     MxTilesArgs plan;                // row blocks that the launch makes too,
-    int rt;                          // of 32 rt rows (3 or 4)
+    int rt;                          // of 32 rt rows (1 to 4)
+    const uint16_t* scales;          // bf16
+    int64_t tiles;                   // of all matrices, 0 for fp16 scales
+    int* wild;                       // [tiles], not 0 for those
 };
 inline int w4_planes(int x_dtype) { return x_dtype == 0 ? 3 : 1; }
 inline int64_t w4_sums_size(int64_t R, int64_t K, int planes, int group) { return w4_tiles(K) * planes * (128 / group) * R * 16; }
@@ -70,6 +74,7 @@ struct W4WideArgs {
     int64_t ldx, rows_x;             // rows of x
     int planes;                      // runs of 128 inputs for each 128 of K
     const uint4* sums;
+    const int* wild;
     const uint8_t* codes;
     const uint16_t *scales, *zeros;
     int scale_dtype, group;

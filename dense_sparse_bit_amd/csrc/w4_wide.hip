@@ -22,9 +22,39 @@ constexpr int kThreads = 256;
 // that take a row, which would else each make its sums again. 2048 x 5120
 // of bf16 6 us, 33000 x 1024 19 us (3.5 TB/s): bound by the reads.
 constexpr int kRows = 4;
+
+// One wave, a 16-row tile of W: ~0 in wild[tile] where a row's scales (bf16) that are not 0 are more than
+// 2^40 apart or outside 2^-126 .. 2^126 (NaN among them). Lane l has row l % 16 of every fourth quad.
+// With fp16's scales no two are further apart, and the tiles do not ask.
+template <int GS>
+__device__ void wild_scales(const uint16_t* scales, int64_t tile, int Q, int* wild) {
+    const int lane = threadIdx.x & 63;
+    uint32_t least = 0x7f800000u, most = 0;                // bits of magnitudes, in order
+    const uint16_t* const from = scales + (tile * Q * 16 + (lane & 15)) * 4 * GS;
+    for (int q = lane >> 4; q < Q; q += 4) {
+        W4Quad<GS> s;
+        s.load(from + static_cast<int64_t>(q) * 64 * GS);
+#pragma unroll
+        for (int i = 0; i < 4 * GS; ++i) {
+            const uint32_t a = __float_as_uint(s.get(i, true)) & 0x7fffffffu;
+            most = max(most, a);
+            least = min(least, a ? a : 0x7f800000u);
+        }
+    }
+    for (int o = 16; o < 64; o <<= 1) {
+        most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), o)));
+        least = min(least, static_cast<uint32_t>(__shfl_xor(static_cast<int>(least), o)));
+    }
+    // (rows of zeros: least is infinity)
+    const bool far = most && (least < 0x00800000u || most > 0x7e800000u || most - least > 40u << 23);
+    const uint64_t any = __ballot(far);
+    if (lane == 0) wild[tile] = any ? ~0 : 0;
+}
+
 template <typename XT>
 __global__ __launch_bounds__(kThreads) void k_w4_rows(const XT* x, int64_t R, int64_t stride, int K, int group, uint4* sums,
-                                                      uint16_t* copy, MxTilesArgs plan, int rt) {
+                                                      uint16_t* copy, MxTilesArgs plan, int rt, int row_blocks, const uint16_t* scales,
+                                                      int64_t tiles, int* wild) {
     __shared__ int lds[kTilesLds];
     const int first = plan.offsets ? 1 : 0;            // workgroups (0, 0): the plan's row blocks alone
     if (static_cast<int>(blockIdx.x) < first) {
@@ -34,6 +64,15 @@ __global__ __launch_bounds__(kThreads) void k_w4_rows(const XT* x, int64_t R, in
             else if (rt == 2) plan_tiles<4>(plan, lds);
             else plan_tiles<2>(plan, lds);
         }
+        return;
+    }
+    if (static_cast<int>(blockIdx.x) >= first + row_blocks) {               // the scales
+        const int64_t tile = (static_cast<int64_t>(blockIdx.x - first - row_blocks) * gridDim.y + blockIdx.y) * 4 + (threadIdx.x >> 6);
+        const int Q = (K + 511) / 512;
+        if (tile >= tiles) return;
+        if (group == 128) wild_scales<1>(scales, tile, Q, wild);
+        else if (group == 64) wild_scales<2>(scales, tile, Q, wild);
+        else wild_scales<4>(scales, tile, Q, wild);
         return;
     }
     constexpr int kPlanes = sizeof(XT) == 4 ? 3 : 1;
@@ -93,10 +132,12 @@ __global__ __launch_bounds__(kThreads) void k_w4_rows(const XT* x, int64_t R, in
 
 template <typename XT>
 hipError_t rows(const W4RowsArgs& a, hipStream_t st) {
-    const unsigned first = a.plan.offsets ? 1 : 0;
-    const dim3 grid(static_cast<unsigned>((a.R + 4 * kRows - 1) / (4 * kRows)) + first, static_cast<unsigned>((a.K + 511) / 512));
-    k_w4_rows<XT><<<grid, kThreads, 0, st>>>(static_cast<const XT*>(a.x), a.R, a.stride, a.K, a.group, static_cast<uint4*>(a.sums),
-                                             static_cast<uint16_t*>(a.copy), a.plan, a.rt);
+    const int64_t first = a.plan.offsets ? 1 : 0, row_blocks = (a.R + 4 * kRows - 1) / (4 * kRows), quads = w4_quads(a.K);
+    const int64_t blocks = first + row_blocks + ((a.tiles + 3) / 4 + quads - 1) / quads;
+    if (blocks >= int64_t(1) << 24) return hipErrorInvalidConfiguration;     // a grid's axis holds 2^32 threads
+    k_w4_rows<XT><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(quads)), kThreads, 0, st>>>(
+        static_cast<const XT*>(a.x), a.R, a.stride, a.K, a.group, static_cast<uint4*>(a.sums), static_cast<uint16_t*>(a.copy), a.plan, a.rt,
+        static_cast<int>(row_blocks), a.scales, a.tiles, a.wild);
     return hipGetLastError();
 }
 
@@ -136,6 +177,74 @@ __device__ __forceinline__ void loads_and_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// The scale of a code tile's group g; -z of it as the matrix instructions take it: the sums' pieces
+// meet its high part, then its low part (`none`: 0, for the lanes of the other inputs).
+template <typename S>
+__device__ __forceinline__ float scale_of(S s, int g, bool bf) { return w4_float(static_cast<uint32_t>(s >> 16 * g) & 0xffff, bf); }
+template <typename S>
+__device__ __forceinline__ w4_b8 zero_of(S z, int g, bool bf, bool has_zeros, bool none) {
+    const float given = -scale_of(z, g, bf), v = has_zeros ? given : -8.0f;
+    const uint32_t hi = none ? 0 : __float_as_uint(v) >> 16;
+    const uint32_t lo = none ? 0 : __float_as_uint(v - __uint_as_float(__float_as_uint(v) & 0xffff0000u)) >> 16;
+    return __builtin_bit_cast(w4_b8, w4_u4{hi | hi << 16, hi | lo << 16, lo | lo << 16, 0});
+}
+
+// x's row of row r of a block; those past its end read the last one's.
+__device__ __forceinline__ int row_at(const Args& a, int row0, int rows, int r) {
+    const int p = min(r, rows - 1);
+    if (!a.by_token) return p;
+    const int token = a.row_token[row0 + p];
+    return static_cast<unsigned>(token) < static_cast<unsigned>(a.T) ? token : 0;
+}
+
+// 32 rows from p0 on, `rows` of them there, leave through LDS (`tile`, a wave's own): a lane holds one
+// column of rows 8 (r / 4) + 4 (l / 32) + r % 4 in value(j, r), read back it holds eight columns of a row.
+// True where one of a row that counts is not finite.
+template <int CT, typename Value>
+__device__ __forceinline__ bool leave(const Args& a, uint8_t* tile, int p0, int rows, int n0, int have, Value value) {
+    constexpr int kPitch = 32 * CT * 4 + 16, kLanes = 4 * CT, kRound = 64 / kLanes;
+    const int lane = threadIdx.x & 63, half = lane >> 5, N = a.N, column = (lane % kLanes) * 8, block = column / 32, n = n0 + column;
+    // a part of K: its sums go to its own fp32 rows, and become outputs with the others'
+    const bool parted = a.partial != nullptr;
+    const int T = a.T, y_dtype = parted ? MQ_F32 : a.y_dtype;
+    const int32_t* const row_token = a.row_token;
+    const float* const bias = parted ? nullptr : a.bias;
+    void* const y = parted ? a.partial + static_cast<int64_t>(blockIdx.y) * a.M * N : a.y;
+    float peak = 0;
+    mx_wave_sync();
+#pragma unroll
+    for (int j = 0; j < CT; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            *reinterpret_cast<float*>(tile + (8 * (r >> 2) + 4 * half + (r & 3)) * kPitch + (32 * j + (lane & 31)) * 4) = value(j, r);
+    mx_wave_sync();
+    // (the second block's columns begin at its first tile)
+    const uint8_t* const from = tile + (32 * block + column - 16 * w4_block_tile(block, 2, have)) * 4;
+#pragma unroll
+    for (int q = 0; q < 32 / kRound; ++q) {
+        const int r = q * kRound + lane / kLanes, p = p0 + r;
+        if (r >= rows || n >= N) continue;
+        const mx_f4 lo = *reinterpret_cast<const mx_f4*>(from + r * kPitch);
+        const mx_f4 hi = *reinterpret_cast<const mx_f4*>(from + r * kPitch + 16);
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        if (row_token && static_cast<unsigned>(row_token[p]) >= static_cast<unsigned>(T)) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = 0.0f;
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) peak = __builtin_elementwise_maximum(peak, fabsf(v[c]));         // (NaN stays)
+        if (bias) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] += n + c < N ? bias[n + c] : 0.0f;
+        }
+        const int64_t at = static_cast<int64_t>(p) * N + n;
+        if (y_dtype == MQ_F32) w4_store8(static_cast<float*>(y) + at, N - n, v);
+        else if (y_dtype == MQ_BF16) w4_store8(static_cast<__bf16*>(y) + at, N - n, v);
+        else w4_store8(static_cast<_Float16*>(y) + at, N - n, v);
+    }
+    return !(peak < __builtin_inff());
+}
+
 // One wave's part of a tile of 32 RT rows: 32 CT columns. The rows of a stage (128 inputs) go
 // from memory to LDS, units of 16 bytes in an order that has a row's sixteen and sixteen
 // rows' alike in different banks; the weights go to registers, each wave its own, a stage
@@ -144,11 +253,13 @@ __device__ __forceinline__ void loads_and_barrier() {
 // The sums stand in units of the column's present scale: where a group begins, they are
 // multiplied by the last scale over the new one, and go on through the matrix instructions.
 // Beside them a second set, to be added to once a group, has no room in the registers of
-// a tile of this size. A scale below 2^-64 of the largest before it (in whose units the sums
-// would leave fp32's range), or below 2^-126 (its reciprocal would), does not become the unit:
-// its codes count as zeros.
+// a tile of this size. Not all sums have a value in all units. Where a scale falls they may leave
+// fp32's range, and end as infinities or NaN; where it rises they lose what is below 2^-126 of the
+// new unit. So 32 rows with a result that is not finite are computed again with a second set
+// (wide_again), and all of them where k_w4_rows found the columns' scales too far apart.
+// Returns which: bit i for the rows 32 i on.
 template <typename E, int GS, int RT, int CT, int D>
-__device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, int row0, int rows, int n0) {
+__device__ __forceinline__ uint32_t wide_tile(const Args& a, uint8_t* lds, int e, int row0, int rows, int n0) {
     typedef typename Op<E>::V V;
     typedef WideLds<RT, GS, D> L;
     constexpr int kSteps = 8 / GS;
@@ -156,24 +267,11 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int N = a.N, planes = a.planes, G = (a.K + 127) / 128, Q = (G + 3) / 4, stages = G * planes, n_tiles = (N + 15) / 16;
     const bool bf = a.scale_dtype == MQ_BF16, has_zeros = a.zeros != nullptr, by_token = a.by_token != 0;
-    const int32_t* const row_token = a.row_token;
     const int64_t rows_x = a.rows_x;
     const uint4* const all_sums = a.sums;
-    // a part of K: its sums go to its own fp32 rows, and become outputs with the others'
-    const bool parted = a.partial != nullptr;
-    const int T = a.T, y_dtype = parted ? MQ_F32 : a.y_dtype;
-    const float* const bias = parted ? nullptr : a.bias;
-    void* const y = parted ? a.partial + static_cast<int64_t>(blockIdx.y) * a.M * a.N : a.y;
     // (there are no more parts than stages: each has one at least)
     const int first_stage = static_cast<int>(static_cast<int64_t>(stages) * blockIdx.y / gridDim.y);
     const int last = static_cast<int>(static_cast<int64_t>(stages) * (blockIdx.y + 1) / gridDim.y) - 1;
-    // x's row of a row of the block; those past its end read the last one's
-    auto row_at = [&](int r) __attribute__((always_inline)) -> int {
-        const int p = min(r, rows - 1);
-        if (!by_token) return p;
-        const int token = row_token[row0 + p];
-        return static_cast<unsigned>(token) < static_cast<unsigned>(T) ? token : 0;
-    };
     const int64_t first_row = by_token ? 0 : row0;
     // this lane's places: rows 4 (2 RT wave + i) + lane / 16, unit lane % 16 of LDS is unit
     // (lane % 16) ^ (row % 16) of the row
@@ -181,7 +279,7 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
 #pragma unroll
     for (int i = 0; i < 2 * RT; ++i) {
         const int r = 4 * (2 * RT * wave + i) + (lane >> 4);
-        xat[i] = static_cast<uint32_t>(row_at(r)) * static_cast<uint32_t>(a.ldx) * 2 + 16 * ((lane & 15) ^ (r & 15));
+        xat[i] = static_cast<uint32_t>(row_at(a, row0, rows, r)) * static_cast<uint32_t>(a.ldx) * 2 + 16 * ((lane & 15) ^ (r & 15));
     }
     // and the wave's fourth of the sums' units
     constexpr int kUnits = 8 * GS * RT, kSumsPer = (kUnits + 63) / 64;
@@ -189,16 +287,19 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
 #pragma unroll
     for (int i = 0; i < kSumsPer; ++i) {
         const int u = wave * kUnits + min(i * 64 + lane, kUnits - 1);
-        sat[i] = (static_cast<uint32_t>(u / (32 * RT)) * static_cast<uint32_t>(rows_x) + row_at(u % (32 * RT))) * 16;
+        sat[i] = (static_cast<uint32_t>(u / (32 * RT)) * static_cast<uint32_t>(rows_x) + row_at(a, row0, rows, u % (32 * RT))) * 16;
     }
     const uint16_t* const x0 = a.x + first_row * a.ldx;
-    const int64_t x_bytes = ((by_token ? T : rows) - 1) * a.ldx * 2 + 256;         // behind a stage's first input
+    const int64_t x_bytes = ((by_token ? a.T : rows) - 1) * a.ldx * 2 + 256;         // behind a stage's first input
     // Loads of a stage, in every wave. A stage's rows are waited for by the number of loads issued
     // after them, so all of a stage's are issued before the next stage's first: the barriers
     // within run() see to that, and the fences between the stages that come before it.
     constexpr int kLoads = 2 * RT + kSumsPer + 4 * CT;
     static_assert(D == 2 || kUnits <= 64);
-    auto load_x = [&](int stage, int buf) __attribute__((always_inline)) {
+    // (the stage is said to be the same in all lanes, or the tiles of three stages take it for a vector,
+    // and each load of the weights for one of many)
+    auto load_x = [&](int at, int buf) __attribute__((always_inline)) {
+        const int stage = __builtin_amdgcn_readfirstlane(at);
         uint8_t* const to = lds + buf * L::kStage;
         const __amdgpu_buffer_rsrc_t xr = buffer(x0 + static_cast<int64_t>(stage) * 128, x_bytes);
         const __amdgpu_buffer_rsrc_t sr = buffer(all_sums + static_cast<int64_t>(stage) * GS * rows_x + first_row,
@@ -216,10 +317,15 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
     const __amdgpu_buffer_rsrc_t wr = buffer(a.codes + first * G * 1024, static_cast<int64_t>(have) * G * 1024);
     const __amdgpu_buffer_rsrc_t scr = buffer(a.scales + first * (scale_bytes / 2), static_cast<int64_t>(have) * scale_bytes);
     const __amdgpu_buffer_rsrc_t zr = has_zeros ? buffer(a.zeros + first * (scale_bytes / 2), static_cast<int64_t>(have) * scale_bytes) : scr;
+    uint32_t redo = 0;                                   // the columns' scales are too far apart
+    if (bf) {
+#pragma unroll
+        for (int t = 0; t < 2 * CT; ++t) redo |= a.wild[first + min(t, have - 1)];
+    }
     const int wat = w4_pair_code(lane, have, G), scat = w4_pair_scale(lane, have, Q, GS);
     int block[CT];                                       // the first tiles of the blocks of 32 columns
 #pragma unroll
-    for (int j = 0; j < CT; ++j) block[j] = w4_block_tile(j, 2, have);
+    for (int j = 0; j < CT; ++j) block[j] = __builtin_amdgcn_readfirstlane(w4_block_tile(j, 2, have));
     // words w of [j][0] are steps 2w, of [j][1] steps 2w + 1
     typedef typename W4Scales<GS>::T Scales;
     struct Weights {
@@ -231,7 +337,8 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
         else if constexpr (GS == 2) return __builtin_amdgcn_raw_buffer_load_b32(r, scat, at, 0);
         else return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(r, scat, at, 0));
     };
-    auto load_w = [&](int stage, Weights& to) __attribute__((always_inline)) {
+    auto load_w = [&](int which, Weights& to) __attribute__((always_inline)) {
+        const int stage = __builtin_amdgcn_readfirstlane(which);
         const int h = planes == 1 ? stage : stage / 3;
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
@@ -243,29 +350,37 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
         }
     };
     mx_f16 acc[RT][CT] = {};
-    // A group's: the factor from the last unit to its own, its unit, the least scale that becomes one, -z as the matrix
-    // instructions take it (the sums' pieces meet the high part, then the low part), its codes'
-    // mask.
-    float unit[CT] = {}, least[CT], by[CT], next[CT];
-#pragma unroll
-    for (int j = 0; j < CT; ++j) least[j] = 0x1p-126f;
+    // A group's: the factor from the last unit to its own, its unit, -z as the matrix instructions
+    // take it. A scale of 0 leaves the unit as it is and its codes out: by their mask, or, in the
+    // tiles of 128 rows, whose registers are all in use, by clearing them where one is met, and with
+    // one unit instead of the last and the next (groups of 64 spill 12 registers else: 4096 tokens of 8
+    // of 64, 4096 x 1024, 414 us and 379 so; 64 x 256 tiles take 3% longer so).
+    constexpr bool kTight = RT == 4;
+    float unit[CT] = {}, by[CT], next[CT];
     w4_b8 zb[CT];
     uint32_t mask[CT];
-    auto begin = [&](const Weights& w, int g) __attribute__((always_inline)) {
+    // there: not a stage past the last one
+    auto begin = [&](Weights& w, int g, bool there) __attribute__((always_inline)) {
+        bool any = false;
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
-            const float s = w4_float(static_cast<uint32_t>(w.s[j] >> 16 * g) & 0xffff, bf);
-            const bool keep = fabsf(s) < least[j];
-            next[j] = keep ? unit[j] : s;
-            least[j] = fmaxf(least[j], fabsf(s) * 0x1p-64f);
-            const float to = keep ? 1.0f : s, from = keep ? 1.0f : unit[j], inv = __builtin_amdgcn_rcpf(to), q = from * inv;
+            const float s = scale_of(w.s[j], g, bf);
+            const bool none = s == 0;
+            const float to = none ? 1.0f : s, from = none ? 1.0f : unit[j], inv = __builtin_amdgcn_rcpf(to), q = from * inv;
             by[j] = __builtin_fmaf(__builtin_fmaf(-q, to, from), inv, q);
-            mask[j] = keep ? 0 : 0x0f0f0f0fu;
-            const float given = -w4_float(static_cast<uint32_t>(w.z[j] >> 16 * g) & 0xffff, bf), z = has_zeros ? given : -8.0f;
-            const bool none = keep || half;
-            const uint32_t hi = none ? 0 : __float_as_uint(z) >> 16;
-            const uint32_t lo = none ? 0 : __float_as_uint(z - __uint_as_float(__float_as_uint(z) & 0xffff0000u)) >> 16;
-            zb[j] = __builtin_bit_cast(w4_b8, w4_u4{hi | hi << 16, hi | lo << 16, lo | lo << 16, 0});
+            if constexpr (kTight) unit[j] = none || !there ? unit[j] : s;
+            else next[j] = none ? unit[j] : s;
+            any |= none;
+            mask[j] = !kTight && none ? 0 : 0x0f0f0f0fu;
+            zb[j] = zero_of(w.z[j], g, bf, has_zeros, none || half);
+        }
+        if (kTight && __ballot(any)) {
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                const uint32_t keep = scale_of(w.s[j], g, bf) == 0 ? 0 : ~0u;
+#pragma unroll
+                for (int s = g * kSteps; s < (g + 1) * kSteps; ++s) w.c[j][s & 1][s >> 1] &= keep;
+            }
         }
     };
     V x_of[2][RT], b[2][CT];
@@ -282,7 +397,7 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     }
-    begin(W[0], 0);
+    begin(W[0], 0, true);
 #pragma unroll
     for (int i = 0; i < RT; ++i) convert(W[0], 0, i);
     const int swap = (half ^ (lane & 15)) * 16;
@@ -292,7 +407,7 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
     int buf = 0;
     auto run = [&](auto later, int stage, Weights& now, Weights& after) __attribute__((always_inline)) {
         loads_and_barrier<decltype(later)::value>();     // stage's rows are there, reads of the buffer to be filled are done
-        const Weights w = now;
+        Weights w = now;
         load_x(min(stage + D - 1, last), buf == 0 ? D - 1 : buf - 1);
         load_w(min(stage + D - 1, last), now);
         const uint8_t* const x = lds + buf * L::kStage + (lane & 31) * 256;
@@ -317,7 +432,7 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
 #pragma unroll
         for (int g = 0; g < GS; ++g) {
 #pragma unroll
-            for (int j = 0; j < CT; ++j) unit[j] = next[j];
+            for (int j = 0; j < CT; ++j) unit[j] = kTight ? unit[j] : next[j];
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 const int step = g * kSteps + s;
@@ -335,7 +450,7 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
                         read(step + 1, i);
                         convert(w, step + 1, i);
                     } else if (g + 1 < GS) {
-                        if (i == 0) begin(w, g + 1);
+                        if (i == 0) begin(w, g + 1, true);
                         read_sum(g + 1, i);
                         read(step + 1, i);
                         convert(w, step + 1, i);
@@ -343,7 +458,7 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
                         if (i == 0) {
 #pragma unroll
                             for (int j = 0; j < CT; ++j) asm volatile("" : "+v"(after.s[j]), "+v"(after.z[j]));    // no use of these loads sooner
-                            begin(after, 0);
+                            begin(after, 0, stage < last);
                         }
                         convert(after, 0, i);
                     }
@@ -364,42 +479,71 @@ __device__ __forceinline__ void wide_tile(const Args& a, uint8_t* lds, int e, in
     if (D > 2 && stage <= last) run(kLater, stage, W[0], W[D > 2 ? 1 : 0]);
     if (D > 3 && stage + 1 <= last) run(Count<0>{}, stage + 1, W[D > 3 ? 1 : 0], W[D > 3 ? 2 : 0]);
 
-    // The results leave through LDS, piece by piece: a lane holds one column of rows
-    // 8 (r / 4) + 4 (l / 32) + r % 4; read back, a lane holds eight columns of a row.
-    constexpr int kPitch = 32 * CT * 4 + 16, kLanes = 4 * CT, kRound = 64 / kLanes;
     uint8_t* const tile = lds + wave * L::kOut;
     loads_and_barrier<0>();                              // nothing is on its way to LDS any more
-    const int n = n0 + (lane % kLanes) * 8;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        mx_wave_sync();
+    for (int i = 0; i < RT; ++i)
+        if (__ballot(leave<CT>(a, tile, row0 + 32 * i, rows - 32 * i, n0, have, [&](int j, int r) __attribute__((always_inline)) { return acc[i][j][r] * unit[j]; })))
+            redo |= 1u << i;
+    return redo;
+}
+
+// Rows of a wave's part of a tile once more (the bits of `redo`, 32 each): a group's products in sums
+// of their own, which its scale multiplies. Operands come from memory as they are used: the rare
+// way, for inputs that few products see. All rows of 2048 x 17408 x 5120 again: 1100 us where the tiles
+// alone take 355 (groups of 32: 1630, 505); one row with a NaN, which is among 32 in all columns: 490.
+// A lane writes the outputs that it wrote before.
+template <typename E, int GS, int CT>
+__device__ __forceinline__ void wide_again(const Args& a, uint8_t* tile, int e, int row0, int rows, int n0, uint32_t redo) {
+    typedef typename Op<E>::V V;
+    constexpr int kSteps = 8 / GS;
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int planes = a.planes, G = (a.K + 127) / 128, Q = (G + 3) / 4, stages = G * planes, n_tiles = (a.N + 15) / 16;
+    const bool bf = a.scale_dtype == MQ_BF16, has_zeros = a.zeros != nullptr;
+    const int first_stage = static_cast<int>(static_cast<int64_t>(stages) * blockIdx.y / gridDim.y);
+    const int last = static_cast<int>(static_cast<int64_t>(stages) * (blockIdx.y + 1) / gridDim.y) - 1;
+    const int64_t first_row = a.by_token ? 0 : row0;
+    const int tile0 = min(n0 / 16, n_tiles - 1), have = min(n_tiles - tile0, 2 * CT);
+    const int64_t first = static_cast<int64_t>(e) * n_tiles + tile0;
+    const uint8_t* const codes = a.codes + first * G * 1024 + w4_pair_code(lane, have, G);
+    const int64_t scales_at = first * (w4_scale_bytes(Q, GS) / 2) + w4_pair_scale(lane, have, Q, GS) / 2;
+#pragma unroll 1
+    for (int i = 0; 32 * i < rows; ++i) {
+        if (!(redo >> i & 1)) continue;
+        const int row = row_at(a, row0, rows, 32 * i + (lane & 31));
+        const uint16_t* const x = a.x + (first_row + row) * a.ldx + 8 * half;
+        mx_f16 sum[CT] = {};
+#pragma unroll 1
+        for (int stage = first_stage; stage <= last; ++stage) {
+            const int h = planes == 1 ? stage : stage / 3;
+            mx_i4 c[CT][2];
+            typename W4Scales<GS>::T s[CT], z[CT];
 #pragma unroll
-        for (int j = 0; j < CT; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                *reinterpret_cast<float*>(tile + (8 * (r >> 2) + 4 * half + (r & 3)) * kPitch + (16 * block[j] + (lane & 31)) * 4) =
-                    acc[i][j][r] * unit[j];
-        mx_wave_sync();
-#pragma unroll
-        for (int q = 0; q < 32 / kRound; ++q) {
-            const int r = q * kRound + lane / kLanes, p = row0 + 32 * i + r;
-            if (32 * i + r >= rows || n >= N) continue;
-            const mx_f4 lo = *reinterpret_cast<const mx_f4*>(tile + r * kPitch + (lane % kLanes) * 32);
-            const mx_f4 hi = *reinterpret_cast<const mx_f4*>(tile + r * kPitch + (lane % kLanes) * 32 + 16);
-            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            if (bias) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) v[c] += n + c < N ? bias[n + c] : 0.0f;
+            for (int j = 0; j < CT; ++j) {
+                const int t = w4_block_tile(j, 2, have);
+                const int64_t at = scales_at + w4_scale_at(t, h, Q, GS) / 2;
+                c[j][0] = *reinterpret_cast<const mx_i4*>(codes + w4_code_at(t, h, G));
+                c[j][1] = *reinterpret_cast<const mx_i4*>(codes + w4_code_at(t, h, G) + 512);
+                s[j] = w4_scales<GS>(a.scales + at);
+                z[j] = has_zeros ? w4_scales<GS>(a.zeros + at) : s[j];
             }
-            if (row_token && static_cast<unsigned>(row_token[p]) >= static_cast<unsigned>(T)) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) v[c] = 0.0f;
+            for (int g = 0; g < GS; ++g) {
+                const w4_b8 rows_sum = __builtin_bit_cast(w4_b8, a.sums[(static_cast<int64_t>(stage) * GS + g) * a.rows_x + first_row + row]);
+                mx_f16 P[CT] = {};
+#pragma unroll
+                for (int j = 0; j < CT; ++j) P[j] = Op<__bf16>::mfma(rows_sum, zero_of(z[j], g, bf, has_zeros, half), P[j]);
+#pragma unroll
+                for (int step = g * kSteps; step < (g + 1) * kSteps; ++step) {
+                    const V v = *reinterpret_cast<const V*>(x + static_cast<int64_t>(stage) * 128 + 16 * step);
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) P[j] = Op<E>::mfma(v, w4_codes<E>(c[j][step & 1][step >> 1]), P[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < CT; ++j) sum[j] += scale_of(s[j], g, bf) * P[j];
             }
-            const int64_t at = static_cast<int64_t>(p) * N + n;
-            if (y_dtype == MQ_F32) w4_store8(static_cast<float*>(y) + at, N - n, v);
-            else if (y_dtype == MQ_BF16) w4_store8(static_cast<__bf16*>(y) + at, N - n, v);
-            else w4_store8(static_cast<_Float16*>(y) + at, N - n, v);
         }
+        leave<CT>(a, tile, row0 + 32 * i, rows - 32 * i, n0, have, [&](int j, int r) __attribute__((always_inline)) { return sum[j][r]; });
     }
 }
 
@@ -503,10 +647,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_w4_wide(W4WideArgs) {
         return;
     }
     const int n0 = col * kCols + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 32 * CT;
-    if (RT >= 4 && rows > 96) wide_tile<E, GS, RT, CT, D>(a, lds, e, row0, rows, n0);
-    else if (RT >= 3 && rows > 64) wide_tile<E, GS, RT < 3 ? RT : 3, CT, D>(a, lds, e, row0, rows, n0);
-    else if (RT >= 2 && rows > 32) wide_tile<E, GS, RT < 2 ? RT : 2, CT, D>(a, lds, e, row0, rows, n0);
-    else wide_tile<E, GS, 1, CT, D>(a, lds, e, row0, rows, n0);
+    uint32_t redo;
+    if (RT >= 4 && rows > 96) redo = wide_tile<E, GS, RT, CT, D>(a, lds, e, row0, rows, n0);
+    else if (RT >= 3 && rows > 64) redo = wide_tile<E, GS, RT < 3 ? RT : 3, CT, D>(a, lds, e, row0, rows, n0);
+    else if (RT >= 2 && rows > 32) redo = wide_tile<E, GS, RT < 2 ? RT : 2, CT, D>(a, lds, e, row0, rows, n0);
+    else redo = wide_tile<E, GS, 1, CT, D>(a, lds, e, row0, rows, n0);
+    if (__builtin_expect(redo != 0, 0))
+        wide_again<E, GS, CT>(a, lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * WideLds<RT, GS, D>::kOut, e, row0, rows, n0, redo);
 }
 
 template <typename E, int GS, int RT, int CT>

@@ -505,9 +505,11 @@ int mq_w4_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* co
  * few rows, K split over a workgroup's waves: 0: 4 rows and 16 columns a workgroup; 1, 2: 16
  * rows and 16, 32 columns; 4, 5: 32 rows and 32, 64 columns. 8 p + t: tiles with K in p
  * parts, t = 0 .. 4: 32 x 128, 64 x 128, 64 x 256, 96 x 256, 128 x 256. Tiles hold sums in
- * units of the present scale of a row of w: there a group counts as zero whose scale is below 2^-64 of
- * the largest of the row's earlier groups, or below 2^-126. The ways give the same sums in another
- * order of additions. */
+ * units of the present scale of a row of w. Where that leaves fp32's range (32 rows with a result that
+ * is not finite), and for rows of w with bf16 scales outside 2^-126 .. 2^126 or more than 2^40 apart, they
+ * compute those outputs again group by group, in up to three times a product's time. The ways give
+ * the same sums in another order of additions; sums of x times codes below 2^-86 may count as zero
+ * in tiles. */
 int mq_w4_linear_way(int64_t M, int64_t N, int64_t K, int x_dtype, int group);
 
 /*
