@@ -330,9 +330,9 @@ PyObject* experts_down(PyObject* const* a) {
     return wrapped(a[5], y);
 }
 
-// no gradient is wanted of it
+// no gradient is wanted of it, and it carries no tangent of forward mode
 const at::Tensor& plain(const at::Tensor& t) {
-    need(!t.requires_grad() || !at::GradMode::is_enabled());
+    need((!t.requires_grad() || !at::GradMode::is_enabled()) && !t._fw_grad(0).defined());
     return t;
 }
 

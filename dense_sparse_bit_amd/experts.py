@@ -5,6 +5,7 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import MQError, _binding, _lib
 from .mx import _TYPES, MX, _check, _current_device, _input, _mx, _on, _output, _raw_stream
@@ -230,8 +231,17 @@ class _Combine(torch.autograd.Function):
         return (*done, None, None) if ctx.dots else (done, None, None, None)
 
 
+def _no_tangent(*inputs):
+    """A tangent of forward mode would be lost, and a lost one reads as zero."""
+    if getattr(forward_ad, "_current_level", 0) >= 0:              # within a dual level
+        for t in inputs:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("this call has no forward-mode derivative: give it inputs without tangents")
+
+
 def _wants_gradient(out, name, *inputs):
     """Whether a call has to leave its gradient; not with an output of the caller's."""
+    _no_tangent(*inputs)
     if not torch.is_grad_enabled() or not any(isinstance(t, torch.Tensor) and t.requires_grad for t in inputs):
         return False
     if out is not None:
@@ -244,7 +254,8 @@ def experts_gather(x, plan: ExpertPlan, weights=None, rows=None, stream=None):
     where given) at row plan.row_of[t, j], zero for rows of no token. x [T, D] (fp32, bf16,
     fp16; its last axis contiguous), weights fp32 [T, k]. Has gradients of x (the sum over the
     token's rows, in the order of the slots) and of weights. A backward pass that is captured
-    into a graph takes leaves of its own and torch.autograd.grad, as of any torch function."""
+    into a graph takes leaves of its own and torch.autograd.grad, as of any torch function. Inputs with
+    tangents of forward mode are refused."""
     if stream is not None:
         _input(x, "x", 2)
         with _on(x.get_device(), stream, x, plan, weights, rows):
@@ -260,7 +271,7 @@ def experts_combine(rows, plan: ExpertPlan, weights=None, out_dtype=None, y=None
     rows[row_of[t, j]] (weights None: of the rows), in the order of the slots, rounded once to
     out_dtype (the rows' type where None). A slot without a row adds weights[t, j] * 0. rows [P, D]
     (fp32, bf16, fp16), weights fp32 [T, k]. Has gradients of rows (zero for rows of no token)
-    and of weights (0 for slots without a row)."""
+    and of weights (0 for slots without a row); inputs with tangents of forward mode are refused."""
     if stream is not None:
         _input(rows, "rows", 2)
         with _on(rows.get_device(), stream, rows, plan, weights, y):

@@ -13,7 +13,7 @@ from typing import NamedTuple
 import torch
 
 from . import MQError, _binding, _lib
-from .experts import ExpertPlan, _plan
+from .experts import ExpertPlan, _no_tangent, _plan
 from .mx import _TYPES, _check, _current_device, _input, _on, _output, _raw_stream
 
 GROUPS = (32, 64, 128)
@@ -85,6 +85,7 @@ def _new(R, K, group, batch, dtype, zeros, device):
 
 
 def _no_gradient(*inputs):
+    _no_tangent(*inputs)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in inputs):
         raise ValueError("this product has no gradient: detach its inputs, or call it under torch.no_grad()")
 
@@ -184,7 +185,7 @@ def w4_dequantize(a: W4, dtype=torch.float32, out=None, stream=None):
 
 def w4_linear(x, w: W4, bias=None, out_dtype=torch.bfloat16, y=None, stream=None):
     """y = x w^T + bias: x [M, K] (fp32, bf16, fp16) as it is, w a W4 matrix [N, K], bias fp32
-    [N]. Without gradient: x and bias that ask for one are refused."""
+    [N]. Without gradient: x and bias that ask for one, or carry a tangent, are refused."""
     if stream is None and _binding is not None:
         done = _binding.w4_linear(x, w, bias, out_dtype, y)
         if done is not None:
@@ -214,7 +215,7 @@ def w4_linear(x, w: W4, bias=None, out_dtype=torch.bfloat16, y=None, stream=None
 def w4_experts_linear(x, w: W4, plan: ExpertPlan, by_token: bool = False, out_dtype=torch.bfloat16, y=None, stream=None):
     """y [rows, N]: for each row p of the plan x[p] w[e]^T, e the row's expert, zero for rows of
     no token. x [rows, K], or by_token [T, K], where row p takes its token's; w: a W4 batch
-    [experts, N, K]. Without gradient: an x that asks for one is refused."""
+    [experts, N, K]. Without gradient: an x that asks for one, or carries a tangent, is refused."""
     if stream is None and _binding is not None:
         done = _binding.w4_experts(x, w, plan, by_token, out_dtype, y)
         if done is not None:
