@@ -141,8 +141,11 @@ at::Tensor output(const Here& here, PyObject* o, PyObject* type, at::IntArrayRef
     return y;
 }
 
+// The caller's output, written, which counts as a change of it (a gradient may have kept what it
+// held), or the new one.
 PyObject* wrapped(PyObject* given, const at::Tensor& y) {
     if (given == Py_None) return THPVariable_Wrap(y);
+    if (!y.is_inference()) y.unsafeGetTensorImpl()->bump_version();
     Py_INCREF(given);
     return given;
 }

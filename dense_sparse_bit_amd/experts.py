@@ -8,7 +8,7 @@ import torch
 from torch.autograd import forward_ad
 
 from . import MQError, _binding, _lib
-from .mx import _TYPES, MX, _check, _current_device, _input, _mx, _on, _output, _raw_stream
+from .mx import _TYPES, MX, _changed, _check, _current_device, _input, _mx, _on, _output, _raw_stream
 
 _SCORES = {"softmax": 0, "sigmoid": 1}        # MQ_SCORE_*
 _GROUP_SCORES = {"max": 0, "top2": 1}         # MQ_GROUP_*
@@ -73,11 +73,11 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     else:
-        _check(ids, "ids", torch.int32, (T, k), index)
+        _changed(_check(ids, "ids", torch.int32, (T, k), index))
     if weights is None:
         weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
     else:
-        _check(weights, "weights", torch.float32, (T, k), index)
+        _changed(_check(weights, "weights", torch.float32, (T, k), index))
     rc = _route(logits.data_ptr(), code, T, logits.stride(0), E, b, score_code, groups, top_groups, group_code, k,
                 1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _raw_stream(index))
     if rc:

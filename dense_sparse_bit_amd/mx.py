@@ -86,6 +86,13 @@ def _mx(a, name, index, batch=None):
     return a
 
 
+def _changed(*given):
+    """The caller's outputs are about to be written: a gradient that kept what they held is told."""
+    for t in given:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _output(y, name, shape, dtype, index):
     if y is None:
         _type(dtype, name)
@@ -94,6 +101,7 @@ def _output(y, name, shape, dtype, index):
     _check(y, name, dtype, shape, index)
     if y.data_ptr() % 16:
         raise ValueError(f"{name} must be 16-byte aligned")
+    _changed(y)
     return y
 
 

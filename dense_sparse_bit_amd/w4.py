@@ -14,7 +14,7 @@ import torch
 
 from . import MQError, _binding, _lib
 from .experts import ExpertPlan, _no_tangent, _plan
-from .mx import _TYPES, _check, _current_device, _input, _on, _output, _raw_stream
+from .mx import _TYPES, _changed, _check, _current_device, _input, _on, _output, _raw_stream
 
 GROUPS = (32, 64, 128)
 _SCALE_TYPES = (torch.float16, torch.bfloat16)
@@ -117,6 +117,7 @@ def w4_quantize(x, group: int = 128, zeros: bool = False, scale_dtype=torch.floa
         _w4(out, "out", index, batch)
         if out[3:] != (R, K, group) or out.scales.dtype != scale_dtype or (out.zeros is not None) != bool(zeros):
             raise ValueError(f"out is {out.rows} x {out.cols} of group {out.group}, {out.scales.dtype}, not what is asked for")
+        _changed(out.codes, out.scales, *(() if out.zeros is None else (out.zeros,)))
     rc = _quantize(x.data_ptr(), code, batch if batched else 1, x.stride(0) if batched else 0, R, x.stride(-2), K, group,
                    scale_code, *_pointers(out), _raw_stream(index))
     if rc:
