@@ -584,8 +584,10 @@ struct RowsBackward : torch::autograd::Node {
     torch::autograd::variable_list apply(torch::autograd::variable_list&& grads) override {
         const std::lock_guard<std::mutex> lock(mutex_);
         torch::autograd::variable_list out(2);
-        if (!grads[0].defined()) return out;
-        const at::Tensor w = weights.unpack(), o = other.unpack(), po = offsets.unpack(), pt = row_token.unpack(), pr = row_of.unpack();
+        const bool first = task_should_compute_output(0), second = task_should_compute_output(1);
+        if (!grads[0].defined() || !(first || second)) return out;
+        const at::Tensor w = weights.unpack(), o = second ? other.unpack() : at::Tensor(), po = offsets.unpack(), pt = row_token.unpack(),
+                         pr = row_of.unpack();
         const bool tracked = at::GradMode::is_enabled() &&
                              (grads[0].requires_grad() || (w.defined() && w.requires_grad()) || (o.defined() && o.requires_grad()));
         {
@@ -598,16 +600,22 @@ struct RowsBackward : torch::autograd::Node {
                 const bool whole_rows = of_gather ? grads[0].is_contiguous() : grads[0].stride(-1) == 1;
                 const at::Tensor dy = whole_rows ? grads[0] : grads[0].contiguous();
                 if (o.defined()) out[1] = here.make({p.T, p.k}, ScalarType::Float);
-                out[0] = here.make({of_gather ? p.T : p.rows, dy.size(1)}, type);
-                if (of_gather) run_combine(here, p, plan_rows(here, dy, p), f, out[0], o, out[1]);
-                else run_gather(here, p, tokens(here, dy, p), f, out[0], o, out[1]);
+                if (of_gather || first) {
+                    out[0] = here.make({of_gather ? p.T : p.rows, dy.size(1)}, type);
+                    if (of_gather) run_combine(here, p, plan_rows(here, dy, p), f, out[0], o, out[1]);
+                    else run_gather(here, p, tokens(here, dy, p), f, out[0], o, out[1]);
+                } else {                                    // the dots alone: a combine has them too, beside T rows and not P
+                    const at::Tensor unused = here.make({p.T, dy.size(1)}, dy.scalar_type());
+                    run_combine(here, p, plan_rows(here, o, p), f, unused, tokens(here, dy, p), out[1]);
+                }
+                if (!first) out[0].reset();
             } catch (const No&) {
                 throw std::runtime_error(name() + ": this gradient cannot be computed");
             }
         }
         if (tracked) {
-            out[0].set_requires_grad(true);
-            if (out[1].defined()) out[1].set_requires_grad(true);
+            for (at::Tensor& t : out)
+                if (t.defined()) t.set_requires_grad(true);
             auto twice = std::make_shared<torch::autograd::DelayedError>(name() + " has no gradient of its own", 2);
             out = (*twice)(std::move(out));
         }

@@ -201,15 +201,17 @@ class _Gather(torch.autograd.Function):
         rows = _gather(x, plan, weights, None, None, None)
         dots = weights is not None and weights.requires_grad
         ctx.save_for_backward(weights, x if dots else None, *plan)
-        ctx.dtype, ctx.dots = x.dtype, dots
+        ctx.dtype = x.dtype
         return rows
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, drows):
         weights, x, *plan = ctx.saved_tensors
-        done = _combine(drows.contiguous(), ExpertPlan(*plan), weights, ctx.dtype, None, x)
-        return (*done, None) if ctx.dots else (done, None, None)
+        first, second = ctx.needs_input_grad[:2]
+        done = _combine(drows.contiguous(), ExpertPlan(*plan), weights, ctx.dtype, None, x if second else None)
+        dx, dots = done if second else (done, None)
+        return dx if first else None, dots, None
 
 
 class _Combine(torch.autograd.Function):
@@ -218,7 +220,7 @@ class _Combine(torch.autograd.Function):
         y = _combine(rows, plan, weights, dtype, None, None)
         dots = weights is not None and weights.requires_grad
         ctx.save_for_backward(weights, rows if dots else None, *plan)
-        ctx.dtype, ctx.dots = rows.dtype, dots
+        ctx.dtype = rows.dtype
         return y
 
     @staticmethod
@@ -227,8 +229,11 @@ class _Combine(torch.autograd.Function):
         weights, rows, *plan = ctx.saved_tensors
         if dy.stride(-1) != 1 or dy.stride(0) < 0:
             dy = dy.contiguous()
-        done = _gather(dy, ExpertPlan(*plan), weights, ctx.dtype, None, rows)
-        return (*done, None, None) if ctx.dots else (done, None, None, None)
+        first, second = ctx.needs_input_grad[:2]
+        if not first:                                # the dots alone: a combine has them too, beside T rows and not P
+            return None, _combine(rows, ExpertPlan(*plan), weights, dy.dtype, None, dy)[1], None, None
+        done = _gather(dy, ExpertPlan(*plan), weights, ctx.dtype, None, rows if second else None)
+        return (*done, None, None) if second else (done, None, None, None)
 
 
 def _no_tangent(*inputs):
