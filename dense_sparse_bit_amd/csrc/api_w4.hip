@@ -191,7 +191,7 @@ Way dense_way(int64_t M, int64_t N, int64_t K, int x_dtype, int group) {
         }
     }
     for (const TileCost& c : kTiles) {
-        if (c.rt == 4 && group == 32) continue;
+        if (!mq::w4_has_tile(c.rt, c.ct, group)) continue;
         const int64_t tiles = ((M + 32 * c.rt - 1) / (32 * c.rt)) * ((N + 128 * c.ct - 1) / (128 * c.ct));
         for (int parts = 1; parts <= 8; parts *= 2)
             if (parts == 1 || (stages >= 4 * parts && tiles * parts <= 1100))

@@ -122,8 +122,10 @@ inline int64_t w4_few_waves(int64_t workgroups, int64_t K, int tiles) {
 }
 hipError_t launch_w4_few(const W4GemmArgs& a, W4Few kind, hipStream_t st);
 hipError_t launch_w4_rows(const W4RowsArgs& a, hipStream_t st);
-// tiles of 32 rt rows and 128 ct columns: rt <= 2 with ct = 1, 2 <= rt <= 4 with ct = 2 (3 or 4 for
-// a plan's rows)
+// tiles of 32 rt rows and 128 ct columns: rt <= 2 with ct = 1, 2 <= rt <= 4 with ct = 2 (a plan's rows: 1 or
+// 2 with 1, 3 or 4 with 2). Groups of 32 take no 64 x 256, which the costs never choose for them, and no 128
+// x 256, whose registers do not hold them (96 x 256 keeps one of them in scratch memory while its loop runs).
+inline bool w4_has_tile(int rt, int ct, int group) { return group > 32 || ct == 1 || rt == 3; }
 hipError_t launch_w4_wide(const W4WideArgs& a, int rt, int ct, hipStream_t st);
 hipError_t launch_rows_gather(const RowsArgs& a, hipStream_t st);
 hipError_t launch_rows_combine(const RowsArgs& a, hipStream_t st);

@@ -670,8 +670,8 @@ hipError_t wide(const W4WideArgs& a, hipStream_t st) {
 template <typename E, int GS>
 hipError_t wide_tiles(const W4WideArgs& a, int rt, int ct, hipStream_t st) {
     if (ct == 1) return rt == 1 ? wide<E, GS, 1, 1>(a, st) : wide<E, GS, 2, 1>(a, st);
-    if (rt == 2) return wide<E, GS, 2, 2>(a, st);
-    if constexpr (GS < 4) {                                // (groups of 32: 128 rows go beyond the registers)
+    if constexpr (GS < 4) {                                // (groups of 32: only 96 rows, w4_has_tile)
+        if (rt == 2) return wide<E, GS, 2, 2>(a, st);
         if (rt == 4) return wide<E, GS, 4, 2>(a, st);
     }
     return wide<E, GS, 3, 2>(a, st);

@@ -504,7 +504,8 @@ int mq_w4_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* co
 /* The way that such a product takes, a status below 0 outside the supported sizes. Kernels of
  * few rows, K split over a workgroup's waves: 0: 4 rows and 16 columns a workgroup; 1, 2: 16
  * rows and 16, 32 columns; 4, 5: 32 rows and 32, 64 columns. 8 p + t: tiles with K in p
- * parts, t = 0 .. 4: 32 x 128, 64 x 128, 64 x 256, 96 x 256, 128 x 256. Tiles hold sums in
+ * parts, t = 0 .. 4: 32 x 128, 64 x 128, 64 x 256, 96 x 256, 128 x 256
+ * (groups of 32: not 2 and 4). Tiles hold sums in
  * units of the present scale of a row of w. Where that leaves fp32's range (32 rows with a result that
  * is not finite), and for rows of w with bf16 scales outside 2^-126 .. 2^126 or more than 2^40 apart, they
  * compute those outputs again group by group, in up to three times a product's time. The ways give

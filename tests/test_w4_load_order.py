@@ -63,7 +63,10 @@ def test_loads_are_issued_stage_by_stage(tmp_path):
         path.write_bytes(code)
         r = subprocess.run([os.path.join(TOOLS, "llvm-objdump"), "-d", "--no-show-raw-insn", str(path)], check=True, capture_output=True, text=True)
         found.update(_segments(r.stdout))
-    assert len(found) >= 26                            # two types, three groups, tiles
+    # the tiles that products take, and no others: 128 x 256 and 64 x 256 not with groups of 32
+    tiles = {(groups, rt, ct) for groups in (1, 2, 4) for rt, ct in ((1, 1), (2, 1), (2, 2), (3, 2), (4, 2)) if groups < 4 or rt % 2 or ct == 1}
+    built = [tuple(map(int, re.search(r"Li(\d)ELi(\d)ELi(\d)E+v", kernel).groups())) for kernel in found]
+    assert sorted(built) == sorted(2 * list(tiles))
     for kernel, segments in found.items():
         deep = max(len(re.findall("L+W+", s)) for s in segments)
         for s in segments:
