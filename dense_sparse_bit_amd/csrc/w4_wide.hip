@@ -20,18 +20,21 @@ constexpr int kThreads = 256;
 // rows themselves, [row][stage][128], zeros past K. A stage is 128 inputs; of fp32 rows, of
 // one of their planes (stage 3h + plane). One wave: 512 inputs of four rows. Once for all the tiles
 // that take a row, which would else each make its sums again. 2048 x 5120
-// of bf16 6 us, 33000 x 1024 19 us (3.5 TB/s): bound by the reads.
+// of bf16 6 us, 33000 x 1024 19 us (3.5 TB/s): bound by the reads; 22 us where it looks at the
+// bf16 scales of 64 matrices 4096 x 1024 beside (8 MB).
 constexpr int kRows = 4;
 
-// One wave, a 16-row tile of W: ~0 in wild[tile] where a row's scales (bf16) that are not 0 are more than
-// 2^40 apart or outside 2^-126 .. 2^126 (NaN among them). Lane l has row l % 16 of every fourth quad.
+// One wave, four 16-row tiles of W from `tile` on, a row a lane: all bits of wild[tile] where a row's scales
+// (bf16) that are not 0 are more than 2^40 apart or outside 2^-126 .. 2^126 (NaN among them).
 // With fp16's scales no two are further apart, and the tiles do not ask.
 template <int GS>
-__device__ void wild_scales(const uint16_t* scales, int64_t tile, int Q, int* wild) {
+__device__ void wild_scales(const uint16_t* scales, int64_t tile, int64_t tiles, int Q, int* wild) {
     const int lane = threadIdx.x & 63;
+    tile += lane >> 4;
     uint32_t least = 0x7f800000u, most = 0;                // bits of magnitudes, in order
-    const uint16_t* const from = scales + (tile * Q * 16 + (lane & 15)) * 4 * GS;
-    for (int q = lane >> 4; q < Q; q += 4) {
+    const uint16_t* const from = scales + ((tile < tiles ? tile : tiles - 1) * Q * 16 + (lane & 15)) * 4 * GS;
+#pragma unroll 2
+    for (int q = 0; q < Q; ++q) {
         W4Quad<GS> s;
         s.load(from + static_cast<int64_t>(q) * 64 * GS);
 #pragma unroll
@@ -41,14 +44,10 @@ __device__ void wild_scales(const uint16_t* scales, int64_t tile, int Q, int* wi
             least = min(least, a ? a : 0x7f800000u);
         }
     }
-    for (int o = 16; o < 64; o <<= 1) {
-        most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), o)));
-        least = min(least, static_cast<uint32_t>(__shfl_xor(static_cast<int>(least), o)));
-    }
     // (rows of zeros: least is infinity)
     const bool far = most && (least < 0x00800000u || most > 0x7e800000u || most - least > 40u << 23);
-    const uint64_t any = __ballot(far);
-    if (lane == 0) wild[tile] = any ? ~0 : 0;
+    const uint64_t which = __ballot(far);
+    if ((lane & 15) == 0 && tile < tiles) wild[tile] = which >> lane & 0xffff ? ~0 : 0;
 }
 
 template <typename XT>
@@ -67,12 +66,12 @@ __global__ __launch_bounds__(kThreads) void k_w4_rows(const XT* x, int64_t R, in
         return;
     }
     if (static_cast<int>(blockIdx.x) >= first + row_blocks) {               // the scales
-        const int64_t tile = (static_cast<int64_t>(blockIdx.x - first - row_blocks) * gridDim.y + blockIdx.y) * 4 + (threadIdx.x >> 6);
+        const int64_t tile = ((static_cast<int64_t>(blockIdx.x - first - row_blocks) * gridDim.y + blockIdx.y) * 4 + (threadIdx.x >> 6)) * 4;
         const int Q = (K + 511) / 512;
         if (tile >= tiles) return;
-        if (group == 128) wild_scales<1>(scales, tile, Q, wild);
-        else if (group == 64) wild_scales<2>(scales, tile, Q, wild);
-        else wild_scales<4>(scales, tile, Q, wild);
+        if (group == 128) wild_scales<1>(scales, tile, tiles, Q, wild);
+        else if (group == 64) wild_scales<2>(scales, tile, tiles, Q, wild);
+        else wild_scales<4>(scales, tile, tiles, Q, wild);
         return;
     }
     constexpr int kPlanes = sizeof(XT) == 4 ? 3 : 1;
@@ -133,7 +132,7 @@ __global__ __launch_bounds__(kThreads) void k_w4_rows(const XT* x, int64_t R, in
 template <typename XT>
 hipError_t rows(const W4RowsArgs& a, hipStream_t st) {
     const int64_t first = a.plan.offsets ? 1 : 0, row_blocks = (a.R + 4 * kRows - 1) / (4 * kRows), quads = w4_quads(a.K);
-    const int64_t blocks = first + row_blocks + ((a.tiles + 3) / 4 + quads - 1) / quads;
+    const int64_t blocks = first + row_blocks + ((a.tiles + 15) / 16 + quads - 1) / quads;
     if (blocks >= int64_t(1) << 24) return hipErrorInvalidConfiguration;     // a grid's axis holds 2^32 threads
     k_w4_rows<XT><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(quads)), kThreads, 0, st>>>(
         static_cast<const XT*>(a.x), a.R, a.stride, a.K, a.group, static_cast<uint4*>(a.sums), static_cast<uint16_t*>(a.copy), a.plan, a.rt,
@@ -317,7 +316,7 @@ __device__ __forceinline__ uint32_t wide_tile(const Args& a, uint8_t* lds, int e
     const __amdgpu_buffer_rsrc_t wr = buffer(a.codes + first * G * 1024, static_cast<int64_t>(have) * G * 1024);
     const __amdgpu_buffer_rsrc_t scr = buffer(a.scales + first * (scale_bytes / 2), static_cast<int64_t>(have) * scale_bytes);
     const __amdgpu_buffer_rsrc_t zr = has_zeros ? buffer(a.zeros + first * (scale_bytes / 2), static_cast<int64_t>(have) * scale_bytes) : scr;
-    uint32_t redo = 0;                                   // the columns' scales are too far apart
+    uint32_t redo = 0;                                   // all, where the columns' scales are too far apart
     if (bf) {
 #pragma unroll
         for (int t = 0; t < 2 * CT; ++t) redo |= a.wild[first + min(t, have - 1)];
@@ -596,9 +595,9 @@ hipError_t add_parts(const W4WideArgs& a, hipStream_t st) {
 }
 
 // Four waves side by side, on blocks of at most 32 RT rows. Bound by the matrix units, whose power
-// holds the clock near 1.9 GHz, and by the changes of units: 2048 x 17408 x 5120 of bf16 again and
-// again, groups of 128 / 64 / 32: 362 / 418 / 528 us (1.01 / 0.87 / 0.69 PFLOP/s; a bf16 library
-// product of the size 0.92). Which tile a product takes is fitted in api_w4.hip.
+// holds the clock near 1.9 GHz, and by the changes of units: 2048 x 17408 x 5120 of bf16, groups of
+// 128 / 64 / 32: 355 / 410 / 515 us, up to a tenth more on some cards (1.03 / 0.89 / 0.71 PFLOP/s; a
+// bf16 library product of the size 0.92). Which tile a product takes is fitted in api_w4.hip.
 template <typename E, int GS, int RT, int CT>
 __global__ __launch_bounds__(kThreads, 2) void k_w4_wide(W4WideArgs) {
     const Args& a = *(const Args*)__builtin_amdgcn_kernarg_segment_ptr();
