@@ -69,7 +69,8 @@ __device__ __forceinline__ MxRaw8<RT> row8(const RT* rows, int64_t p, bool there
 // Workgroups (y): the tokens, then one for every 16 rows of the plan, which zeroes those of
 // no token. DOTS: a workgroup takes a token's whole row, and loads its rows of `other` before the
 // first is used; else (x) 8 columns a thread of it. 4096 tokens of 8 slots, 4096 columns of bf16: 58 us
-// (5.2 TB/s), with dots 117 (4.9 TB/s).
+// (5.2 TB/s; 77 to rows that no cache holds any of), with dots 117 (4.9 TB/s). Narrow rows leave lanes
+// idle: 8192 tokens, 64 / 512 / 1024 columns 19 / 28 / 41 us, where their bytes take 1.8 / 15 / 29.
 template <typename XT, typename RT, bool DOTS>
 __global__ __launch_bounds__(kThreads) void k_gather(RowsArgs a) {
     __shared__ float lds[kThreads / 64 * kSlots];
@@ -134,7 +135,8 @@ __global__ __launch_bounds__(kThreads) void k_gather(RowsArgs a) {
 }
 
 // Workgroups (y): the tokens. The rows of up to SLOTS (2, 4 or 8) slots are loaded before the
-// first is added: 4096 tokens of 8 slots and 4096 columns 57 us, with each row added as it comes 76.
+// first is added: 4096 tokens of 8 slots and 4096 columns 57 us (65 from rows that no cache
+// holds), with each row added as it comes 76; 8192 tokens, 64 / 512 / 1024 columns 15 / 20 / 35 us.
 // DOTS: a workgroup takes a token's whole row, and each of its rows serves the sum and the dot (k <=
 // SLOTS; with more slots they are read twice); else (x) 8 columns a thread of it.
 template <typename XT, typename RT, int SLOTS, bool DOTS>

@@ -200,8 +200,9 @@ __device__ __forceinline__ MxRaw8<XT> load8(const XT* row, int k, int K, bool wh
 // the matrix instructions through LDS, one load of 1 KB a quad; the sums of its groups come
 // from the lanes that loaded it. The instructions' rows 0 .. RB - 1 (lanes 0 .. 15 of the
 // result) are the rows, the others repeat the last. GS: groups in 128 inputs. Bound by latency: a
-// launch, the row, a batch of loads; 1 x 4096 x 4096 takes 4.1 to 4.4 us, one token by 8 experts of
-// 1024 x 4096 6.4 (reading their weights at the rate of a large copy: 1.7 and 3.4).
+// launch, the row, a batch of loads; 1 x 4096 x 4096 takes 4.4 to 4.7 us, one token by 8 experts of
+// 1024 x 4096 6.1 to 6.7 (reading their weights at the rate of a large copy: 1.7 and 3.4); 1 x 17408 x
+// 5120 15.9 with the weights from memory (8.8).
 template <typename XT, int GS, bool Z, int RB>
 __global__ __launch_bounds__(64 * kMaxWaves) void k_w4_one(W4GemmArgs a) {
     typedef W4Op<XT> Op;
@@ -332,10 +333,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_w4_one(W4GemmArgs a) {
 
 // One workgroup: 16 MT rows x NT column tiles of 16, its waves each a run of K, tile by tile;
 // rows reach the matrix instructions through LDS (256 bytes of four rows a load; lanes that
-// read their own operands, 64 bytes of 16 rows, take twice the time). Bound by instructions:
-// 32 rows, 14336 x 4096 take 17.0 us with the weights from memory and 15.1 us from caches, where
-// reading them takes 6; in the 1.9 us of a code tile (two waves a SIMD) each wave has 200 vector
-// instructions (64 conversions of two codes, 64 sums of groups) and 40 matrix instructions.
+// read their own operands, 64 bytes of 16 rows, take twice the time). Bound by latency: 32 rows,
+// 14336 x 4096 take 17.2 us with the weights from memory and 15.0 us from caches, where reading them
+// takes 6. 32 x 64 workgroups have two waves a SIMD (212 registers, and 36 scalars in their lanes),
+// which wait for half of their time; vector instructions fill 38% of the cycles (64 conversions of two
+// codes and 64 sums of groups a code tile), matrix instructions 16%.
 template <typename XT, int GS, bool Z, int NT, int MT, int W>
 __global__ __launch_bounds__(64 * W) void k_w4_few(W4GemmArgs a) {
     constexpr int kPitch = kRowPitch<XT>, kUnit = 8 * sizeof(XT);

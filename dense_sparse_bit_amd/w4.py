@@ -126,8 +126,8 @@ def w4_quantize(x, group: int = 128, zeros: bool = False, scale_dtype=torch.floa
 
 
 def w4_pack(codes, scales, zeros=None, group: int = 128, stream=None) -> W4:
-    """Weights that are quantized already, as checkpoints hold them: codes u8 [R, K] or [B, R, K],
-    one to a byte (the low four bits count), scales and zeros (or None: 8) fp16 or bf16
+    """Weights that are quantized already: codes u8 [R, K] or [B, R, K], one to a byte (the low four
+    bits count; a checkpoint that holds several in a word is unpacked first), scales and zeros (or None: 8) fp16 or bf16
     [(B,) R, ceil(K / group)]; a weight is scale * (code - zero)."""
     if stream is None and _binding is not None:
         done = _binding.w4_pack(codes, scales, zeros, group)

@@ -479,9 +479,9 @@ size_t mq_w4_scales_bytes(int64_t R, int64_t K, int group);
 int mq_w4_quantize(const void* x, int x_dtype, int64_t B, int64_t stride_b, int64_t R, int64_t stride_r, int64_t K,
                    int group, int scale_dtype, uint8_t* codes, void* scales, void* zeros, void* stream);
 
-/* Weights that are quantized already, as checkpoints hold them: c [B][R][K], one code a
- * byte (its low four bits count; strides stride_b, stride_r), s and z (or NULL)
- * [B][R][ceil(K/group)], contiguous, of any 16-bit float type, in the library's layout. */
+/* Weights that are quantized already: c [B][R][K], one code a byte (its low four bits count;
+ * strides stride_b, stride_r; a checkpoint that holds several in a word is unpacked first), s and z (or
+ * NULL) [B][R][ceil(K/group)], contiguous, of any 16-bit float type, in the library's layout. */
 int mq_w4_pack(const uint8_t* c, int64_t B, int64_t stride_b, int64_t R, int64_t stride_r, int64_t K, int group,
                const void* s, const void* z, uint8_t* codes, void* scales, void* zeros, void* stream);
 
