@@ -27,6 +27,7 @@
 #include <string.h>
 
 #include <mutex>
+#include <utility>
 
 #include "../../include/mq.h"
 
@@ -449,6 +450,21 @@ PyObject* w4_dequantize(PyObject* const* a) {
     return wrapped(a[2], y);
 }
 
+// The memory from t's first to its last element.
+std::pair<uintptr_t, uintptr_t> span(const at::Tensor& t) {
+    const uintptr_t first = reinterpret_cast<uintptr_t>(t.const_data_ptr());
+    int64_t last = 0;
+    for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+    return {first, t.numel() ? first + (last + 1) * t.element_size() : first};
+}
+
+// The caller's output is not memory that is still read.
+const at::Tensor& apart(const at::Tensor& y, const at::Tensor& x) {
+    const auto a = span(y), b = span(x);
+    need(a.second <= b.first || b.second <= a.first);
+    return y;
+}
+
 // w4_linear(x, w, bias, out_dtype, y)
 PyObject* w4_linear(PyObject* const* a) {
     const Here here;
@@ -458,7 +474,7 @@ PyObject* w4_linear(PyObject* const* a) {
     need(x.size(1) == w.cols);
     const int64_t M = x.size(0);
     const int code = type_code(x.scalar_type());
-    const at::Tensor y = output(here, a[4], a[3], {M, w.rows});
+    const at::Tensor y = apart(output(here, a[4], a[3], {M, w.rows}), x);
     const size_t bytes = mq_w4_linear_workspace_bytes(M, w.rows, w.cols, code, w.group);
     at::Tensor work;
     if (bytes) work = here.make({static_cast<int64_t>(bytes)}, ScalarType::Byte);
@@ -475,7 +491,7 @@ PyObject* w4_experts(PyObject* const* a) {
     const Group4 w = group4(here, a[1], p.E);
     const int by_token = PyObject_IsTrue(a[3]), code = type_code(x.scalar_type());
     need(by_token >= 0 && x.size(0) == (by_token ? p.T : p.rows) && x.size(1) == w.cols);
-    const at::Tensor y = output(here, a[5], a[4], {p.rows, w.rows});
+    const at::Tensor y = apart(output(here, a[5], a[4], {p.rows, w.rows}), x);
     const size_t bytes = mq_w4_experts_workspace_bytes(p.T, p.k, p.E, w.rows, w.cols, by_token, code, w.group);
     at::Tensor work;
     if (bytes) work = here.make({static_cast<int64_t>(bytes)}, ScalarType::Byte);
@@ -539,7 +555,7 @@ PyObject* gather(PyObject* const* a) {
     const Plan p = plan(here, a[1]);
     const at::Tensor& x = plain(tokens(here, tensor(a[0]), p));
     const float* const weights = weights_of(here, a[2], p);
-    const at::Tensor rows = output_as(here, a[4], a[3], x.scalar_type(), {p.rows, x.size(1)});
+    const at::Tensor rows = apart(output_as(here, a[4], a[3], x.scalar_type(), {p.rows, x.size(1)}), x);
     at::Tensor other, dots;
     if (a[5] != Py_None) {
         other = contiguous(here, a[5], rows.scalar_type(), {p.rows, x.size(1)});
@@ -555,7 +571,7 @@ PyObject* combine(PyObject* const* a) {
     const Plan p = plan(here, a[1]);
     const at::Tensor& rows = plain(plan_rows(here, tensor(a[0]), p));
     const float* const weights = weights_of(here, a[2], p);
-    const at::Tensor y = output_as(here, a[4], a[3], rows.scalar_type(), {p.T, rows.size(1)});
+    const at::Tensor y = apart(output_as(here, a[4], a[3], rows.scalar_type(), {p.T, rows.size(1)}), rows);
     at::Tensor other, dots;
     if (a[5] != Py_None) {
         other = tokens(here, tensor(a[5]), p);

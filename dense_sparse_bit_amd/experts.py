@@ -8,7 +8,7 @@ import torch
 from torch.autograd import forward_ad
 
 from . import MQError, _binding, _lib
-from .mx import _TYPES, MX, _changed, _check, _current_device, _input, _mx, _on, _output, _raw_stream
+from .mx import _TYPES, MX, _apart, _changed, _check, _current_device, _input, _mx, _on, _output, _raw_stream
 
 _SCORES = {"softmax": 0, "sigmoid": 1}        # MQ_SCORE_*
 _GROUP_SCORES = {"max": 0, "top2": 1}         # MQ_GROUP_*
@@ -146,7 +146,7 @@ def _gather(x, plan, weights, dtype, rows, other):
         raise ValueError(f"x must be [{T}, columns] for this plan, got {tuple(x.shape)}")
     if weights is not None:
         _check(weights, "weights", torch.float32, (T, k), index)
-    rows = _output(rows, "rows", (P, D), x.dtype if dtype is None else dtype, index)
+    rows = _apart(_output(rows, "rows", (P, D), x.dtype if dtype is None else dtype, index), "rows", x, "x")
     dots = None
     if other is not None:
         _check(other, "other", rows.dtype, (P, D), index)
@@ -179,7 +179,7 @@ def _combine(rows, plan, weights, dtype, y, other):
     _check(rows, "rows", rows.dtype, (P, D), index)
     if weights is not None:
         _check(weights, "weights", torch.float32, (T, k), index)
-    y = _output(y, "y", (T, D), rows.dtype if dtype is None else dtype, index)
+    y = _apart(_output(y, "y", (T, D), rows.dtype if dtype is None else dtype, index), "y", rows, "rows")
     dots = None
     if other is not None:
         _input(other, "other", 2)

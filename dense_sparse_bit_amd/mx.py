@@ -93,6 +93,17 @@ def _changed(*given):
             torch.autograd.graph.increment_version(t)
 
 
+def _apart(y, name, x, other):
+    """An output of the caller's is not memory that is still read."""
+    spans = []
+    for t in (y, x):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        spans.append((t.data_ptr(), t.data_ptr() + ((last + 1) * t.element_size() if t.numel() else 0)))
+    if spans[0][0] < spans[1][1] and spans[1][0] < spans[0][1]:
+        raise ValueError(f"{name} shares memory with {other}")
+    return y
+
+
 def _output(y, name, shape, dtype, index):
     if y is None:
         _type(dtype, name)

@@ -14,7 +14,7 @@ import torch
 
 from . import MQError, _binding, _lib
 from .experts import ExpertPlan, _no_tangent, _plan
-from .mx import _TYPES, _changed, _check, _current_device, _input, _on, _output, _raw_stream
+from .mx import _TYPES, _apart, _changed, _check, _current_device, _input, _on, _output, _raw_stream
 
 GROUPS = (32, 64, 128)
 _SCALE_TYPES = (torch.float16, torch.bfloat16)
@@ -203,7 +203,7 @@ def w4_linear(x, w: W4, bias=None, out_dtype=torch.bfloat16, y=None, stream=None
         raise ValueError(f"x has {K} inputs, w has {w.cols}")
     N = w.rows
     b = None if bias is None else _check(bias, "bias", torch.float32, (N,), index).data_ptr()
-    y = _output(y, "y", (M, N), out_dtype if y is None else y.dtype, index)
+    y = _apart(_output(y, "y", (M, N), out_dtype if y is None else y.dtype, index), "y", x, "x")
     need = _linear_workspace(M, N, K, code, w.group)
     work = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
     rc = _linear(x.data_ptr(), code, x.stride(0), *_pointers(w), _TYPES[w.scales.dtype], w.group, M, N, K, b, y.data_ptr(),
@@ -233,7 +233,7 @@ def w4_experts_linear(x, w: W4, plan: ExpertPlan, by_token: bool = False, out_dt
     need = (T if by_token else rows, K)
     if x.shape != need:
         raise ValueError(f"x must be [{need[0]}, {K}] for this plan and these weights, got {tuple(x.shape)}")
-    y = _output(y, "y", (rows, N), out_dtype if y is None else y.dtype, index)
+    y = _apart(_output(y, "y", (rows, N), out_dtype if y is None else y.dtype, index), "y", x, "x")
     size = _experts_workspace(T, k, E, N, K, bool(by_token), code, w.group)
     work = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
     rc = _experts(x.data_ptr(), code, x.stride(0), bool(by_token), T, k, E, N, K, plan.offsets.data_ptr(),

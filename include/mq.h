@@ -494,7 +494,8 @@ int mq_w4_dequantize(const uint8_t* codes, const void* scales, const void* zeros
  * stride_m) as it is, w [N][K]: sums of x times codes, which are exact products, are held in
  * fp32, a group's sum is scaled once. A row of x with a NaN or an infinity gives NaN, and so
  * does a group whose sum of |x| times 15 leaves fp32's range. workspace: device scratch of at
- * least mq_w4_linear_workspace_bytes, 16-byte aligned (may be NULL where that is 0).
+ * least mq_w4_linear_workspace_bytes, 16-byte aligned (may be NULL where that is 0). y shares no
+ * memory with x, here and by expert.
  */
 size_t mq_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_dtype, int group);
 int mq_w4_linear(const void* x, int x_dtype, int64_t stride_m, const uint8_t* codes, const void* scales,
@@ -540,7 +541,8 @@ int mq_w4_experts(const void* x, int x_dtype, int64_t stride_r, int by_token, in
  *            rows[row_of[t][j]]
  * and 0 for slots without a row. x [T][D] (gather: its rows stride_t apart), rows
  * [mq_plan_rows][D]; each of its own type. Products and sums in fp32, rounded once. Entries of row_of and
- * row_token out of range are taken as "no row". D <= 2^20.
+ * row_token out of range are taken as "no row". D <= 2^20. What is written shares no memory with what is
+ * read.
  */
 int mq_experts_gather(const void* x, int x_dtype, int64_t stride_t, int64_t T, int64_t k, int64_t E, int64_t D,
                       const int32_t* row_token, const int32_t* row_of, const float* weights, void* rows, int rows_dtype,

@@ -85,3 +85,27 @@ def test_outputs_of_inference_mode(mq, way):
         assert torch.equal(y, mq.experts_combine(rows, plan, weights)) and torch.equal(v, mq.route(logits, 2)[1])
     with torch.no_grad():
         assert mq.experts_combine(rows, plan, weights, y=y) is y
+
+
+def test_outputs_over_the_input_are_refused(mq, way):
+    """Workgroups would overwrite rows that others still read. Memory before, behind and beside it is not refused."""
+    import torch
+    x, plan, weights, w, _ = _layer(mq)
+    T, D = x.shape
+    P = plan.row_token.numel()
+    one = w._replace(codes=w.codes[0], scales=w.scales[0])
+    both = torch.zeros(2 * P, D, device="cuda")
+    cases = [(lambda a, y: mq.w4_linear(a, one, y=y), T, T), (lambda a, y: mq.w4_experts_linear(a, w, plan, y=y), P, P),
+             (lambda a, y: mq.w4_experts_linear(a, w, plan, by_token=True, y=y), T, P), (lambda a, y: mq.experts_gather(a, plan, rows=y), T, P),
+             (lambda a, y: mq.experts_combine(a, plan, weights, y=y), P, T)]
+    for call, m, n in cases:
+        a = both[:m]
+        for y in (both[:n], both[m - 1:m - 1 + n], both.view(-1)[4:4 + n * D].view(n, D)):
+            with pytest.raises(ValueError, match="shares memory"):
+                call(a, y)
+        both.normal_()
+        apart = call(a.clone(), torch.empty(n, D, device="cuda"))
+        assert torch.equal(call(a, both[m:m + n] if m + n <= len(both) else torch.empty(n, D, device="cuda")), apart)
+        shifted = both[n:n + m]
+        want = call(shifted.clone(), torch.empty(n, D, device="cuda"))
+        assert torch.equal(call(shifted, both[:n]), want)
