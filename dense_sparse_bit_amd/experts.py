@@ -128,6 +128,14 @@ def _plan(plan, index):
     return T, k, E, rows
 
 
+def _no_tangent(*inputs):
+    """A tangent of forward mode would be lost, and a lost one reads as zero."""
+    if getattr(forward_ad, "_current_level", 0) >= 0:              # within a dual level
+        for t in inputs:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("this call has no forward-mode derivative: give it inputs without tangents")
+
+
 def _gather(x, plan, weights, dtype, rows, other):
     """rows [P, D] of `dtype` (x's where None): v[t, j] * x[t] at row_of[t, j], zero for rows
     of no token; with other [P, D] also dots [T, k] = x[t] . other[row_of[t, j]]."""
@@ -135,6 +143,7 @@ def _gather(x, plan, weights, dtype, rows, other):
         done = _binding.gather(x, plan, weights, dtype, rows, other)
         if done is not None:
             return done
+    _no_tangent(x, weights)
     code = _input(x, "x", 2)
     index = x.get_device()
     if index < 0 or index != _current_device():
@@ -167,6 +176,7 @@ def _combine(rows, plan, weights, dtype, y, other):
         done = _binding.combine(rows, plan, weights, dtype, y, other)
         if done is not None:
             return done
+    _no_tangent(rows, weights)
     code = _input(rows, "rows", 2)
     index = rows.get_device()
     if index < 0 or index != _current_device():
@@ -236,17 +246,8 @@ class _Combine(torch.autograd.Function):
         return (*done, None, None) if second else (done, None, None, None)
 
 
-def _no_tangent(*inputs):
-    """A tangent of forward mode would be lost, and a lost one reads as zero."""
-    if getattr(forward_ad, "_current_level", 0) >= 0:              # within a dual level
-        for t in inputs:
-            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
-                raise ValueError("this call has no forward-mode derivative: give it inputs without tangents")
-
-
 def _wants_gradient(out, name, *inputs):
     """Whether a call has to leave its gradient; not with an output of the caller's."""
-    _no_tangent(*inputs)
     if not torch.is_grad_enabled() or not any(isinstance(t, torch.Tensor) and t.requires_grad for t in inputs):
         return False
     if out is not None:
@@ -267,7 +268,10 @@ def experts_gather(x, plan: ExpertPlan, weights=None, rows=None, stream=None):
             return experts_gather(x, plan, weights, rows)
     if _wants_gradient(rows, "rows", x, weights):
         done = None if _binding is None else _binding.gather_grad(x, plan, weights)
-        return _Gather.apply(x, weights, plan) if done is None else done
+        if done is None:
+            _no_tangent(x, weights)
+            done = _Gather.apply(x, weights, plan)
+        return done
     return _gather(x, plan, weights, None, rows, None)
 
 
@@ -283,7 +287,10 @@ def experts_combine(rows, plan: ExpertPlan, weights=None, out_dtype=None, y=None
             return experts_combine(rows, plan, weights, out_dtype, y)
     if _wants_gradient(y, "y", rows, weights):
         done = None if _binding is None else _binding.combine_grad(rows, plan, weights, out_dtype)
-        return _Combine.apply(rows, weights, plan, out_dtype) if done is None else done
+        if done is None:
+            _no_tangent(rows, weights)
+            done = _Combine.apply(rows, weights, plan, out_dtype)
+        return done
     return _combine(rows, plan, weights, out_dtype, y, None)
 
 
